@@ -28,6 +28,8 @@ DEV_BAD_PAGE = 8
 DEV_KV_LEN_RANGE = 16
 DEV_WAIT_TIMEOUT = 32
 DEV_BAD_TOKEN = 64
+DEV_BAD_ROWS = 128
+DEV_NO_PAGES = 256
 
 KIND_GQA = 0
 KIND_MLA = 1
@@ -35,6 +37,11 @@ MASK_CAUSAL_TAIL = 0
 MASK_BLOCK_BIDIR = 1
 DTYPE_BF16 = 0
 DTYPE_F32 = 1
+ROPE_HALF = 0
+ROPE_PAIRS = 1
+ROPE_PLAIN = 0
+ROPE_LINEAR = 1
+ROPE_YARN = 2
 
 EXPORTS = ("dflash_step_bookkeeping", "dflash_ctx_workspace_bytes", "dflash_ctx_kv_update",
            "dflash_block_kv_scatter", "dflash_attention_num_segments",
@@ -45,7 +52,9 @@ EXPORTS = ("dflash_step_bookkeeping", "dflash_ctx_workspace_bytes", "dflash_ctx_
            "dflash_packed_kv_bytes", "dflash_packed_gamma_bytes", "dflash_pack_weights",
            "dflash_strict_accept", "dflash_embedding_gather", "dflash_ctx_prefill_workspace_bytes",
            "dflash_ctx_kv_prefill", "dflash_test_attention_skip_tile",
-           "dflash_block_scatter_attention")
+           "dflash_block_scatter_attention", "dflash_chunk_plan", "dflash_chunk_rope_store",
+           "dflash_chunk_attention", "dflash_chunk_attention_num_segments",
+           "dflash_chunk_attention_workspace_bytes")
 
 
 class DflashError(RuntimeError):
@@ -83,6 +92,22 @@ class StepOutputs(ctypes.Structure):
 
 
 STEP_OUTPUT_FIELDS = [f[0] for f in StepOutputs._fields_]
+
+
+class ChunkOutputs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "cu_rows", "n_pages", "alloc_limit", "seq_lens", "free_head", "row_req", "row_pos",
+        "row_page", "row_slot")]
+
+
+CHUNK_OUTPUT_FIELDS = [f[0] for f in ChunkOutputs._fields_]
+
+
+class RopeSpec(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("trained_ctx", ctypes.c_int32),
+                ("factor", ctypes.c_double), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double), ("magnitude", ctypes.c_double)]
 
 _lib = None
 
@@ -145,11 +170,26 @@ def load():
     lib.dflash_status_string.argtypes = [ctypes.c_int]
     lib.dflash_status_string.restype = ctypes.c_char_p
     lib.dflash_abi_version.argtypes = []
+    lib.dflash_chunk_plan.argtypes = [G, ctypes.c_int, ctypes.c_int, vp, vp, vp, vp, vp,
+                                      ctypes.c_int, vp, vp, i32, ctypes.POINTER(ChunkOutputs), vp,
+                                      vp]
+    lib.dflash_chunk_rope_store.argtypes = [G, ctypes.c_int, ctypes.c_int,
+                                            ctypes.POINTER(RopeSpec), vp, i64, vp, i64, vp, i64,
+                                            vp, vp, vp, vp, vp, vp, i64, vp, vp, vp]
+    lib.dflash_chunk_attention_num_segments.argtypes = [G, ctypes.c_int, ctypes.c_int]
+    lib.dflash_chunk_attention_workspace_bytes.argtypes = [G, ctypes.c_int, ctypes.c_int,
+                                                           ctypes.c_int]
+    lib.dflash_chunk_attention_workspace_bytes.restype = sz
+    lib.dflash_chunk_attention.argtypes = [G, ctypes.c_int, ctypes.c_int, ctypes.c_int, vp, i64,
+                                           vp, vp, vp, vp, vp, i32, vp, ctypes.c_float,
+                                           ctypes.c_int, ctypes.c_int, vp, sz, vp, i64, vp, vp]
     for name in ("dflash_step_bookkeeping", "dflash_ctx_kv_update", "dflash_block_kv_scatter",
                  "dflash_block_attention", "dflash_attention_num_segments", "dflash_abi_version",
                  "dflash_ctx_kv_project", "dflash_ctx_kv_commit", "dflash_q_norm_rope",
                  "dflash_pack_weights", "dflash_strict_accept", "dflash_embedding_gather",
-                 "dflash_ctx_kv_prefill", "dflash_block_scatter_attention"):
+                 "dflash_ctx_kv_prefill", "dflash_block_scatter_attention", "dflash_chunk_plan",
+                 "dflash_chunk_rope_store", "dflash_chunk_attention",
+                 "dflash_chunk_attention_num_segments"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -179,6 +219,26 @@ def _stream(stream):
         import torch
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _step(t):
+    """Elements between two rows."""
+    return 0 if t is None else t.stride(0)
+
+
+def _dense(*tensors):
+    for t in tensors:
+        assert t is None or t.is_contiguous()
+
+
+def _rows(t):
+    """Row-strided view: any step between rows, the rest of a row contiguous."""
+    if t is not None:
+        assert t.stride(-1) == 1 and (t.dim() < 3 or t.stride(1) == t.shape[2])
 
 
 def _check(fn, code):
@@ -395,6 +455,69 @@ def dflash_ctx_kv_prefill(geom, hidden, cu_rows, ctx_len, alloc_limit, block_tab
         _ptr(ctx_len), _ptr(alloc_limit), _ptr(block_table), _ptr(valid), ctypes.byref(w),
         _ptr(kv_pool), _ptr(workspace), workspace.numel() * workspace.element_size(),
         _ptr(dev_status), _stream(stream)))
+
+
+def dflash_chunk_plan(geom, n_new, ctx_len, n_pages, block_table, free_pages, free_range, valid,
+                      max_ctx, out: dict, dev_status=None, stream=None):
+    """n_new / ctx_len / n_pages int32 [B], block_table int32 [B, M] (new entries
+    are written), free_pages int32, free_range int32 [2] CUDA tensors, valid
+    uint8 [B] or None; out: dict of the dflash_chunk_outputs fields ->
+    preallocated int32 CUDA tensors (n_rows = length of row_req)."""
+    lib = load()
+    _dense(n_new, ctx_len, n_pages, block_table, free_pages, free_range, valid, *out.values())
+    o = ChunkOutputs(*[out[k].data_ptr() for k in CHUNK_OUTPUT_FIELDS])
+    _check("dflash_chunk_plan", lib.dflash_chunk_plan(
+        ctypes.byref(geom), n_new.shape[0], out["row_req"].shape[0], n_new.data_ptr(),
+        ctx_len.data_ptr(), n_pages.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
+        free_pages.shape[0], free_range.data_ptr(), _addr(valid), max_ctx, ctypes.byref(o),
+        _addr(dev_status), _stream(stream)))
+
+
+def dflash_chunk_rope_store(geom, layer, rope, q, k, v, row_pos, row_page, row_slot, q_out,
+                            kv_pool, *, gamma_q=None, gamma_k=None, dev_status=None, stream=None):
+    """rope: a RopeSpec; q [n_rows, hq * head_dim], k and v [n_rows, nkv *
+    head_dim] bf16 CUDA tensors (row-strided views of a packed projection output
+    allowed, also as [n_rows, heads, head_dim]); q_out like q.  q and q_out, or
+    k and v, may be None."""
+    lib = load()
+    for t in (q, k, v, q_out):
+        _rows(t)
+    _dense(row_pos, row_page, row_slot, kv_pool, gamma_q, gamma_k)
+    _check("dflash_chunk_rope_store", lib.dflash_chunk_rope_store(
+        ctypes.byref(geom), layer, row_pos.shape[0], ctypes.byref(rope), _addr(q), _step(q),
+        _addr(k), _step(k), _addr(v), _step(v), _addr(gamma_q), _addr(gamma_k),
+        row_pos.data_ptr(), _addr(row_page), _addr(row_slot), _addr(q_out), _step(q_out),
+        _addr(kv_pool), _addr(dev_status), _stream(stream)))
+
+
+def dflash_chunk_attention_num_segments(geom, B, n_rows) -> int:
+    return int(load().dflash_chunk_attention_num_segments(ctypes.byref(geom), B, n_rows))
+
+
+def dflash_chunk_attention_workspace_bytes(geom, B, n_rows, num_segments=0) -> int:
+    return int(load().dflash_chunk_attention_workspace_bytes(ctypes.byref(geom), B, n_rows,
+                                                             num_segments))
+
+
+def dflash_chunk_attention(geom, layer, q, kv_pool, block_table, cu_rows, ctx_len, kv_len, out,
+                           workspace=None, *, window=0, sinks=None, scale=None,
+                           mask_mode=MASK_CAUSAL_TAIL, num_segments=0, dev_status=None,
+                           stream=None):
+    """q, out bf16 CUDA tensors [n_rows, hq, head_dim] (row-strided views
+    allowed); block_table int32 [B, M], cu_rows int32 [B + 1], ctx_len and kv_len
+    int32 [B]; workspace: uint8 tensor of dflash_chunk_attention_workspace_bytes
+    bytes (None where that is 0)."""
+    lib = load()
+    _rows(q)
+    _rows(out)
+    _dense(kv_pool, block_table, cu_rows, ctx_len, kv_len, sinks)
+    _check("dflash_chunk_attention", lib.dflash_chunk_attention(
+        ctypes.byref(geom), kv_len.shape[0], layer, q.shape[0], q.data_ptr(), _step(q),
+        kv_pool.data_ptr(), block_table.data_ptr(), cu_rows.data_ptr(), ctx_len.data_ptr(),
+        kv_len.data_ptr(), window, _addr(sinks), 0.0 if scale is None else scale, mask_mode,
+        num_segments, _addr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), out.data_ptr(),
+        _step(out), _addr(dev_status), _stream(stream)))
 
 
 def dflash_test_attention_skip_tile(tile: int) -> None:

@@ -1,0 +1,236 @@
+// chunk_plan.cu -- row offsets, positions, page table and slot map of a ragged
+// chunk of new tokens, built on the GPU from the requests' lengths in one
+// launch.
+//
+// Mathematics: two exclusive prefix sums over the requests, of the rows n_r
+// and of the new pages need_r, then one lookup per row.  Both sums saturate
+// (min(a + b, cap) is associative), so lengths that make no sense cannot
+// overflow them: rows at n_rows + 1, pages at what the free list holds.
+//
+// Bound by latency: a few KB move, in three dependent memory round trips (the
+// lengths; a row's table or free-list entry; the stores).  So every CTA repeats
+// the sums over all requests in shared memory instead of waiting for another
+// CTA's (a second launch or a grid barrier costs more than the ~10 us of L2
+// reads it saves even at 8192 requests), and its rows find their request by
+// binary search there.  Entries of the page table below the owned count are
+// only read and those from it on only written, and rows on new pages take the
+// id from the free list, so CTAs never read what another one writes.
+#include "dflash_internal.cuh"
+#include "sm100_ptx.cuh"
+
+namespace dflash {
+namespace {
+
+struct PlanParams {
+  int B, n_rows, M, P, NP, n_free, max_ctx;
+  const int32_t *n_new, *ctx_len, *n_pages, *free_pages, *free_range;
+  const uint8_t *valid;
+  int32_t *tbl;
+  dflash_chunk_outputs o;
+  int32_t *st;
+};
+
+// Exclusive prefix sum over the block's threads, saturating at cap; *total is
+// the block's sum.  wsum: one word per warp, not reused before a later barrier.
+__device__ __forceinline__ unsigned block_scan_sat(unsigned v, unsigned cap, unsigned *wsum,
+                                                   unsigned *total) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  unsigned inc = min(v, cap);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc = min(inc + u, cap);
+  }
+  if (lane == 31) wsum[wid] = inc;
+  __syncthreads();
+  unsigned w = lane < nw ? wsum[lane] : 0u;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned u = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w = min(w + u, cap);
+  }
+  *total = __shfl_sync(0xffffffffu, w, nw - 1);
+  unsigned before = __shfl_sync(0xffffffffu, w, wid > 0 ? wid - 1 : 0);
+  if (wid == 0) before = 0u;
+  unsigned ex = __shfl_up_sync(0xffffffffu, inc, 1);
+  if (lane == 0) ex = 0u;
+  return min(before + ex, cap);
+}
+
+__global__ void __launch_bounds__(1024) chunk_plan_kernel(const PlanParams p) {
+  extern __shared__ int32_t plan_smem[];
+  int32_t *s_cu = plan_smem;             // [B + 1] first row of each request
+  int32_t *s_base = s_cu + p.B + 1;      // [B] first new page in the free list
+  int32_t *s_have = s_base + p.B;        // [B] pages owned before
+  int32_t *s_now = s_have + p.B;         // [B] pages owned after
+  __shared__ unsigned wsum[2][32];
+  ptx::griddep_launch();
+  ptx::griddep_wait();
+  const bool first = blockIdx.x == 0;
+  const int head = min(max(p.free_range[0], 0), p.n_free);
+  const int tail = min(max(p.free_range[1], head), p.n_free);
+  const unsigned avail = static_cast<unsigned>(tail - head);
+  const unsigned row_cap = static_cast<unsigned>(p.n_rows) + 1u;
+  unsigned rows = 0u, pages = 0u;  // sums over the requests before this pass
+  unsigned flags = 0u;
+  for (int r0 = 0; r0 < p.B; r0 += blockDim.x) {
+    const int r = r0 + threadIdx.x;
+    const bool in = r < p.B;
+    int n = 0, c = 0, have = 0;
+    bool live = false;
+    if (in) {
+      n = p.n_new[r];
+      c = p.ctx_len[r];
+      have = p.n_pages[r];
+      live = p.valid == nullptr || p.valid[r] != 0;
+    }
+    if (live) {
+      if (n < 0) flags |= DFLASH_DEV_BAD_ROWS;
+      if (have < 0 || have > p.M) flags |= DFLASH_DEV_BAD_PAGE;
+      if (c < 0 || c > INT32_MAX - p.n_rows - 1) {
+        flags |= DFLASH_DEV_BAD_CTX_LEN;
+        live = false;
+      }
+    }
+    have = min(max(have, 0), p.M);
+    unsigned total;
+    const unsigned ask = live && n > 0 ? static_cast<unsigned>(n) : 0u;
+    unsigned ex = block_scan_sat(ask, row_cap, wsum[0], &total);
+    ex = min(rows + ex, row_cap);
+    const int cu = static_cast<int>(min(ex, static_cast<unsigned>(p.n_rows)));
+    const int cu1 = static_cast<int>(
+        min(min(ex + min(ask, row_cap), row_cap), static_cast<unsigned>(p.n_rows)));
+    rows = min(rows + total, row_cap);
+    const int ne = cu1 - cu;  // rows of the request that fit
+    int need = 0;
+    if (ne > 0) {
+      const int want = (c + ne - 1) / p.P + 1;
+      if (want > p.M) flags |= DFLASH_DEV_NO_PAGES;
+      need = max(min(want, p.M) - have, 0);
+    }
+    unsigned base = block_scan_sat(static_cast<unsigned>(need), avail, wsum[1], &total);
+    base = min(pages + base, avail);
+    pages = min(pages + total, avail);
+    const int got = min(need, static_cast<int>(avail - base));
+    if (got < need) flags |= DFLASH_DEV_NO_PAGES;
+    if (in) {
+      s_cu[r] = cu;
+      s_base[r] = head + static_cast<int>(base);
+      s_have[r] = have;
+      s_now[r] = have + got;
+      if (first) {
+        const int now = live ? have + got : 0;
+        const int limit = min(now * p.P, p.max_ctx);
+        p.o.cu_rows[r] = cu;
+        p.o.n_pages[r] = now;
+        p.o.alloc_limit[r] = limit;
+        p.o.seq_lens[r] = live ? min(c + ne, limit) : 0;
+      }
+    }
+  }
+  if (first) {
+    if (threadIdx.x == 0) {
+      if (rows > static_cast<unsigned>(p.n_rows)) flags |= DFLASH_DEV_BAD_ROWS;
+      p.o.cu_rows[p.B] = static_cast<int>(min(rows, static_cast<unsigned>(p.n_rows)));
+      p.o.free_head[0] = head + static_cast<int>(pages);
+    }
+    if (flags) raise_status(p.st, flags);
+  }
+  if (threadIdx.x == 0) s_cu[p.B] = static_cast<int>(min(rows, static_cast<unsigned>(p.n_rows)));
+  __syncthreads();
+
+  // new table entries: one warp per request
+  const int lane = threadIdx.x & 31;
+  const int warps = blockDim.x >> 5;
+  for (int r = blockIdx.x * warps + (threadIdx.x >> 5); r < p.B; r += gridDim.x * warps) {
+    const int have = s_have[r], got = s_now[r] - have;
+    for (int j = lane; j < got; j += 32) {
+      int pg = p.free_pages[s_base[r] + j];
+      if (pg < 0 || pg >= p.NP) {
+        raise_status(p.st, DFLASH_DEV_BAD_PAGE);
+        pg = -1;
+      }
+      p.tbl[static_cast<int64_t>(r) * p.M + have + j] = pg;
+    }
+  }
+
+  // rows
+  for (int t = blockIdx.x * blockDim.x + threadIdx.x; t < p.n_rows; t += gridDim.x * blockDim.x) {
+    int req = -1, pos = -1, page = -1, slot = -1;
+    if (t < s_cu[p.B]) {
+      int lo = 0, hi = p.B - 1;  // the last request whose first row is <= t
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_cu[mid] <= t) lo = mid; else hi = mid - 1;
+      }
+      req = lo;
+      pos = p.ctx_len[req] + (t - s_cu[req]);
+      const int lp = pos / p.P, have = s_have[req], now = s_now[req];
+      if (lp < now && pos < p.max_ctx) {
+        const int pg = lp < have ? p.tbl[static_cast<int64_t>(req) * p.M + lp]
+                                 : p.free_pages[s_base[req] + lp - have];
+        if (pg >= 0 && pg < p.NP) {
+          page = pg;
+          slot = pos - lp * p.P;
+        } else {
+          raise_status(p.st, DFLASH_DEV_BAD_PAGE);
+        }
+      }
+    }
+    p.o.row_req[t] = req;
+    p.o.row_pos[t] = pos;
+    p.o.row_page[t] = page;
+    p.o.row_slot[t] = slot;
+  }
+}
+
+}  // namespace
+
+// Shared memory of the request arrays: 4 words a request.
+static int plan_smem_bytes(int B) { return (4 * B + 1) * 4; }
+int max_plan_requests() { return 8192; }
+
+cudaError_t launch_chunk_plan(const dflash_geom &g, int B, int n_rows, const int32_t *n_new,
+                              const int32_t *ctx_len, const int32_t *n_pages, int32_t *tbl,
+                              const int32_t *free_pages, int n_free, const int32_t *free_range,
+                              const uint8_t *valid, int32_t max_ctx,
+                              const dflash_chunk_outputs &o, int32_t *st, cudaStream_t s) {
+  PlanParams p;
+  p.B = B;
+  p.n_rows = n_rows;
+  p.M = g.max_pages;
+  p.P = g.page_size;
+  p.NP = g.num_pool_pages;
+  p.n_free = n_free;
+  p.max_ctx = max_ctx;
+  p.n_new = n_new;
+  p.ctx_len = ctx_len;
+  p.n_pages = n_pages;
+  p.free_pages = free_pages;
+  p.free_range = free_range;
+  p.valid = valid;
+  p.tbl = tbl;
+  p.o = o;
+  p.st = st;
+  cudaError_t e = ensure_smem_limit<chunk_plan_kernel>(plan_smem_bytes(max_plan_requests()));
+  if (e != cudaSuccess) return e;
+  // a thread per request and per row, 1024 at most; rows over as many CTAs as
+  // there are SMs
+  const int most = B > n_rows ? B : n_rows;
+  const int threads = most >= 1024 ? 1024 : (most + 31) / 32 * 32;
+  const int ctas = (n_rows + threads - 1) / threads;
+  const int sms = device_sm_count();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(ctas < 1 ? 1 : (ctas < sms ? ctas : sms));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = plan_smem_bytes(B);
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_plan_kernel, p);
+}
+
+}  // namespace dflash

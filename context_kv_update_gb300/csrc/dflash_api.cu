@@ -421,3 +421,168 @@ extern "C" int dflash_block_scatter_attention(
       block_table, kv_len, window, sinks, scale, mask_mode, S, workspace, out, dev_status,
       reinterpret_cast<cudaStream_t>(stream)));
 }
+
+// ------------------------------------------------------------ ragged chunk
+
+namespace {
+
+// Device memory of two int32 arrays overlaps.
+bool overlap(const int32_t *a, int64_t na, const int32_t *b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na > 0 && nb > 0 && x < y + static_cast<uintptr_t>(nb) * 4 &&
+         y < x + static_cast<uintptr_t>(na) * 4;
+}
+
+bool rows_ok(const void *p, int64_t stride, int64_t width) {
+  return aligned16(p) && stride >= width && stride % 8 == 0;
+}
+
+// Row strides apply between rows: a single row may have any.
+int64_t row_stride(int n_rows, int64_t stride, int64_t width) { return n_rows > 1 ? stride : width; }
+
+int chunk_attention_geom_status(const dflash_geom *g, int B, int n_rows) {
+  if (g->kind != DFLASH_KIND_GQA || (g->head_dim != 64 && g->head_dim != 128))
+    return DFLASH_ERR_UNSUPPORTED_GEOM;
+  const int P = g->page_size;
+  if (P % 8 != 0 || !(kAttnTileKeys % P == 0 || P % kAttnTileKeys == 0))
+    return DFLASH_ERR_UNSUPPORTED_GEOM;
+  // TMA row coordinates of the pool, key positions and output rows are signed
+  // 32-bit
+  const long long pool_rows =
+      2LL * g->num_layers * g->num_pool_pages * P * static_cast<long long>(g->nkv);
+  if (pool_rows >= (1LL << 31) || static_cast<long long>(g->max_pages) * P >= (1LL << 31) ||
+      static_cast<long long>(n_rows) * g->hq >= (1LL << 31) || B >= (1 << 24))
+    return DFLASH_ERR_UNSUPPORTED_GEOM;
+  return DFLASH_OK;
+}
+
+}  // namespace
+
+extern "C" int dflash_chunk_plan(const dflash_geom *g, int B, int n_rows, const int32_t *n_new,
+                                 const int32_t *ctx_len, const int32_t *n_pages,
+                                 int32_t *block_table, const int32_t *free_pages, int n_free,
+                                 const int32_t *free_range, const uint8_t *valid, int32_t max_ctx,
+                                 const dflash_chunk_outputs *out, int32_t *dev_status,
+                                 dflash_stream_t stream) {
+  if (!geom_ok(g) || !out || B < 0 || n_rows < 0 || n_free < 0 || max_ctx < 0)
+    return DFLASH_ERR_INVALID_ARG;
+  if (B > max_plan_requests() || n_rows >= (1 << 30) ||
+      static_cast<long long>(g->max_pages) * g->page_size >= (1LL << 31))
+    return DFLASH_ERR_UNSUPPORTED_GEOM;
+  const dflash_chunk_outputs &o = *out;
+  if (!free_range || !o.cu_rows || !o.free_head) return DFLASH_ERR_INVALID_ARG;
+  if (B > 0 && (!n_new || !ctx_len || !n_pages || !block_table || !o.n_pages || !o.alloc_limit ||
+                !o.seq_lens))
+    return DFLASH_ERR_INVALID_ARG;
+  if (n_free > 0 && !free_pages) return DFLASH_ERR_INVALID_ARG;
+  if (n_rows > 0 && (!o.row_req || !o.row_pos || !o.row_page || !o.row_slot))
+    return DFLASH_ERR_INVALID_ARG;
+  const struct { const int32_t *p; int64_t n; } outs[] = {
+      {o.cu_rows, B + 1LL}, {o.n_pages, B}, {o.alloc_limit, B}, {o.seq_lens, B}, {o.free_head, 1},
+      {o.row_req, n_rows}, {o.row_pos, n_rows}, {o.row_page, n_rows}, {o.row_slot, n_rows},
+      {block_table, static_cast<int64_t>(B) * g->max_pages}},
+      ins[] = {{n_new, B}, {ctx_len, B}, {n_pages, B}, {free_pages, n_free}, {free_range, 2}};
+  for (const auto &a : outs)
+    for (const auto &b : ins)
+      if (overlap(a.p, a.n, b.p, b.n)) return DFLASH_ERR_INVALID_ARG;
+  return cuda_status(launch_chunk_plan(*g, B, n_rows, n_new, ctx_len, n_pages, block_table,
+                                       free_pages, n_free, free_range, valid, max_ctx, o,
+                                       dev_status, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int dflash_chunk_rope_store(const dflash_geom *g, int layer, int n_rows,
+                                       const dflash_rope_spec *rope, const void *q,
+                                       int64_t q_row_stride, const void *k, int64_t k_row_stride,
+                                       const void *v, int64_t v_row_stride, const void *gamma_q,
+                                       const void *gamma_k, const int32_t *row_pos,
+                                       const int32_t *row_page, const int32_t *row_slot,
+                                       void *q_out, int64_t q_out_row_stride, void *kv_pool,
+                                       int32_t *dev_status, dflash_stream_t stream) {
+  if (!geom_ok(g) || !rope || layer < 0 || layer >= g->num_layers || n_rows < 0)
+    return DFLASH_ERR_INVALID_ARG;
+  if (g->kind != DFLASH_KIND_GQA || g->head_dim % 8 != 0 || g->head_dim > kMaxHeadDim)
+    return DFLASH_ERR_UNSUPPORTED_GEOM;
+  const dflash_rope_spec &r = *rope;
+  if (r.layout != DFLASH_ROPE_HALF && r.layout != DFLASH_ROPE_PAIRS) return DFLASH_ERR_INVALID_ARG;
+  if (r.scaling != DFLASH_ROPE_PLAIN && r.scaling != DFLASH_ROPE_LINEAR &&
+      r.scaling != DFLASH_ROPE_YARN)
+    return DFLASH_ERR_INVALID_ARG;
+  if (r.rot_dim < 2 || r.rot_dim % 2 != 0 || r.rot_dim > g->head_dim)
+    return DFLASH_ERR_UNSUPPORTED_GEOM;
+  if (r.scaling != DFLASH_ROPE_PLAIN && !(std::isfinite(r.factor) && r.factor >= 1.0))
+    return DFLASH_ERR_INVALID_ARG;
+  if (r.scaling == DFLASH_ROPE_YARN) {
+    if (r.trained_ctx < 1 || !std::isfinite(r.beta_fast) || !std::isfinite(r.magnitude) ||
+        !(r.beta_slow > 0.0 && r.beta_fast >= r.beta_slow))
+      return DFLASH_ERR_INVALID_ARG;
+    if (!(g->rope_theta > 1.0)) return DFLASH_ERR_UNSUPPORTED_GEOM;
+  }
+  if (n_rows == 0) return DFLASH_OK;
+  const int64_t wq = static_cast<int64_t>(g->hq) * g->head_dim;
+  const int64_t wk = static_cast<int64_t>(g->nkv) * g->head_dim;
+  if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (v == nullptr) || (!q && !k) ||
+      !row_pos)
+    return DFLASH_ERR_INVALID_ARG;
+  q_row_stride = row_stride(n_rows, q_row_stride, wq);
+  q_out_row_stride = row_stride(n_rows, q_out_row_stride, wq);
+  k_row_stride = row_stride(n_rows, k_row_stride, wk);
+  v_row_stride = row_stride(n_rows, v_row_stride, wk);
+  if (q && (!rows_ok(q, q_row_stride, wq) || !rows_ok(q_out, q_out_row_stride, wq) ||
+            (q == q_out && q_row_stride != q_out_row_stride)))
+    return DFLASH_ERR_INVALID_ARG;
+  if (k && (!rows_ok(k, k_row_stride, wk) || !rows_ok(v, v_row_stride, wk) || !kv_pool ||
+            !aligned16(kv_pool) || !row_page || !row_slot))
+    return DFLASH_ERR_INVALID_ARG;
+  if (!aligned16(gamma_q) || !aligned16(gamma_k)) return DFLASH_ERR_INVALID_ARG;
+  return cuda_status(launch_chunk_rope_store(
+      *g, layer, n_rows, r, q, q_row_stride, k, k_row_stride, v, v_row_stride, gamma_q, gamma_k,
+      row_pos, row_page, row_slot, q_out, q_out_row_stride, kv_pool, dev_status,
+      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int dflash_chunk_attention_num_segments(const dflash_geom *g, int B, int n_rows) {
+  if (!geom_ok(g) || B < 1 || n_rows < 1 || chunk_attention_geom_status(g, B, n_rows)) return 0;
+  return chunk_attention_num_segments(*g, B, n_rows);
+}
+
+extern "C" size_t dflash_chunk_attention_workspace_bytes(const dflash_geom *g, int B, int n_rows,
+                                                         int num_segments) {
+  if (!geom_ok(g) || B < 0 || n_rows < 0 || num_segments < 0 ||
+      chunk_attention_geom_status(g, B, n_rows))
+    return 0;
+  return chunk_attention_workspace_bytes(*g, B, n_rows, num_segments);
+}
+
+extern "C" int dflash_chunk_attention(const dflash_geom *g, int B, int layer, int n_rows,
+                                      const void *q, int64_t q_row_stride, const void *kv_pool,
+                                      const int32_t *block_table, const int32_t *cu_rows,
+                                      const int32_t *ctx_len, const int32_t *kv_len,
+                                      int32_t window, const float *sinks, float scale,
+                                      int mask_mode, int num_segments, void *workspace,
+                                      size_t ws_bytes, void *out, int64_t out_row_stride,
+                                      int32_t *dev_status, dflash_stream_t stream) {
+  if (!geom_ok(g) || B < 0 || n_rows < 0 || layer < 0 || layer >= g->num_layers || window < 0 ||
+      num_segments < 0 || !std::isfinite(scale))
+    return DFLASH_ERR_INVALID_ARG;
+  if (mask_mode != DFLASH_MASK_CAUSAL_TAIL && mask_mode != DFLASH_MASK_BLOCK_BIDIR)
+    return DFLASH_ERR_INVALID_ARG;
+  if (const int st = chunk_attention_geom_status(g, B, n_rows)) return st;
+  if (B == 0 || n_rows == 0) return DFLASH_OK;
+  if (!block_table || !cu_rows || !ctx_len) return DFLASH_ERR_INVALID_ARG;
+  if (const int st = attention_ptrs_status(B, q, nullptr, kv_pool, block_table, kv_len, out))
+    return st;
+  const int64_t wq = static_cast<int64_t>(g->hq) * g->head_dim;
+  q_row_stride = row_stride(n_rows, q_row_stride, wq);
+  out_row_stride = row_stride(n_rows, out_row_stride, wq);
+  if (!rows_ok(q, q_row_stride, wq) || !rows_ok(out, out_row_stride, wq))
+    return DFLASH_ERR_INVALID_ARG;
+  if (!(scale > 0.f)) scale = default_attention_scale(*g);
+  const int S = num_segments > 0 ? num_segments : chunk_attention_num_segments(*g, B, n_rows);
+  const size_t need = chunk_attention_workspace_bytes(*g, B, n_rows, S);
+  if (need > 0 && (!workspace || !aligned16(workspace))) return DFLASH_ERR_INVALID_ARG;
+  if (need > 0 && ws_bytes < need) return DFLASH_ERR_WORKSPACE_TOO_SMALL;
+  return cuda_status(launch_chunk_attention(*g, B, layer, n_rows, q, q_row_stride, kv_pool,
+                                            block_table, cu_rows, ctx_len, kv_len, window, sinks,
+                                            scale, mask_mode, S, workspace, out, out_row_stride,
+                                            dev_status, reinterpret_cast<cudaStream_t>(stream)));
+}

@@ -182,4 +182,27 @@ int block_scatter_args_status(const dflash_geom &g, const void *blk_k, const voi
                               const int32_t *blk_page, const int32_t *blk_slot,
                               const uint8_t *blk_mask, const void *kv_pool);
 
+// a ragged chunk: plan, RoPE + paged store, attention
+int max_plan_requests();
+cudaError_t launch_chunk_plan(const dflash_geom &g, int B, int n_rows, const int32_t *n_new,
+                              const int32_t *ctx_len, const int32_t *n_pages, int32_t *tbl,
+                              const int32_t *free_pages, int n_free, const int32_t *free_range,
+                              const uint8_t *valid, int32_t max_ctx,
+                              const dflash_chunk_outputs &o, int32_t *st, cudaStream_t s);
+cudaError_t launch_chunk_rope_store(const dflash_geom &g, int layer, int n_rows,
+                                    const dflash_rope_spec &rope, const void *q, int64_t q_stride,
+                                    const void *k, int64_t k_stride, const void *v,
+                                    int64_t v_stride, const void *gamma_q, const void *gamma_k,
+                                    const int32_t *pos, const int32_t *page, const int32_t *slot,
+                                    void *q_out, int64_t q_out_stride, void *pool, int32_t *st,
+                                    cudaStream_t s);
+int chunk_attention_num_segments(const dflash_geom &g, int B, int n_rows);
+size_t chunk_attention_workspace_bytes(const dflash_geom &g, int B, int n_rows, int S);
+cudaError_t launch_chunk_attention(const dflash_geom &g, int B, int layer, int n_rows,
+                                   const void *q, int64_t q_stride, const void *pool,
+                                   const int32_t *tbl, const int32_t *cu, const int32_t *ctx,
+                                   const int32_t *kv, int32_t window, const float *sinks,
+                                   float scale, int mask_mode, int S, void *ws, void *out,
+                                   int64_t out_stride, int32_t *st, cudaStream_t s);
+
 }  // namespace dflash

@@ -88,6 +88,8 @@ enum dflash_status_code {
 #define DFLASH_DEV_KV_LEN_RANGE 16u   /* kv_len < 0 or > max_pages * page_size: clamped */
 #define DFLASH_DEV_WAIT_TIMEOUT 32u   /* an on-chip pipeline wait hit its iteration limit */
 #define DFLASH_DEV_BAD_TOKEN 64u      /* embedding id outside [0, vocab): zero row written */
+#define DFLASH_DEV_BAD_ROWS 128u      /* chunk row counts or offsets out of range: rows dropped */
+#define DFLASH_DEV_NO_PAGES 256u      /* free pages or table entries ran out: rows not placed */
 
 enum dflash_kind { DFLASH_KIND_GQA = 0, DFLASH_KIND_MLA = 1 };
 enum dflash_mask_mode { DFLASH_MASK_CAUSAL_TAIL = 0, DFLASH_MASK_BLOCK_BIDIR = 1 };
@@ -164,6 +166,33 @@ typedef struct dflash_step_outputs {
   int32_t *ctx_len_new;  /* [B]    c' = min(c + n, A) (advertised context length) */
   int32_t *seq_lens;     /* [B]    c' + T (kv_len of the block attention) */
 } dflash_step_outputs;
+
+/* Outputs of dflash_chunk_plan (all device int32, dense). */
+typedef struct dflash_chunk_outputs {
+  int32_t *cu_rows;     /* [B + 1] first row of each request; [B] = rows in use */
+  int32_t *n_pages;     /* [B]     pages the request owns after the call */
+  int32_t *alloc_limit; /* [B]     min(max_ctx, n_pages * P) */
+  int32_t *seq_lens;    /* [B]     keys after the chunk: min(c + n, alloc_limit) */
+  int32_t *free_head;   /* [1]     first page of the free list still unused */
+  int32_t *row_req;     /* [n_rows] request of the row, -1 past the last request */
+  int32_t *row_pos;     /* [n_rows] position c + i, -1 past the last request */
+  int32_t *row_page;    /* [n_rows] physical page of the position, -1 if unplaced */
+  int32_t *row_slot;    /* [n_rows] slot in that page, -1 if unplaced */
+} dflash_chunk_outputs;
+
+/* Rotary positions of dflash_chunk_rope_store. */
+enum dflash_rope_layout { DFLASH_ROPE_HALF = 0, DFLASH_ROPE_PAIRS = 1 };
+enum dflash_rope_scaling { DFLASH_ROPE_PLAIN = 0, DFLASH_ROPE_LINEAR = 1, DFLASH_ROPE_YARN = 2 };
+typedef struct dflash_rope_spec {
+  int32_t layout;      /* HALF: dims (j, j + rot_dim/2) turn together; PAIRS: (2j, 2j + 1) */
+  int32_t rot_dim;     /* leading dims of the head that turn (even; the rest is copied) */
+  int32_t scaling;     /* DFLASH_ROPE_PLAIN, _LINEAR or _YARN */
+  int32_t trained_ctx; /* YARN: context length the angles were trained on */
+  double factor;       /* LINEAR, YARN: by how much the context is extended (>= 1) */
+  double beta_fast;    /* YARN: pairs turning more often than this over trained_ctx are kept */
+  double beta_slow;    /* YARN: pairs turning less often than this are divided by factor */
+  double magnitude;    /* YARN: factor on cos and sin; <= 0 selects 0.1 ln(factor) + 1 */
+} dflash_rope_spec;
 
 /* ---------------------------------------------------------------------
  * dflash_pack_weights -- stack every drafter layer's K/V (GQA) or latent (MLA)
@@ -568,6 +597,154 @@ DFLASH_API int dflash_block_attention_noalloc(const dflash_geom *g, int B, int l
 
 /* Size in bytes of the fixed scratch used by dflash_block_attention_noalloc. */
 DFLASH_API size_t dflash_block_attention_noalloc_max_scratch_bytes(void);
+
+/* ---------------------------------------------------------------------
+ * A ragged chunk of new tokens: dflash_chunk_plan, dflash_chunk_rope_store,
+ * dflash_chunk_attention.  A chunk holds n_rows token rows, packed request
+ * after request, any number per request (none, one, a prompt's piece): a
+ * prompt's prefill in pieces, single tokens of running requests beside it,
+ * drafts of different lengths.  The plan is built once per chunk; the other
+ * two calls run once per layer.  The pages describe uniform blocks only: these
+ * calls are this library's own, with no counterpart in the method.
+ *
+ * dflash_chunk_plan -- row offsets, positions, page table and slot map of the
+ * chunk from the requests' lengths, in one launch (nothing is read on the
+ * host, so a captured plan follows the lengths of each replay).
+ *
+ * For request r with c = ctx_len[r], have = n_pages[r], live = valid != 0:
+ *   n     = live ? n_new[r] : 0, cut where the rows before it leave less of
+ *           n_rows; cu_rows = exclusive prefix sum of n;
+ *   need  = n > 0 ? max(0, min(ceil((c + n) / P), max_pages) - have) : 0;
+ *   the new pages are taken from the free list in request order: page k of
+ *   all those needed is free_pages[free_range[0] + k], until free_range[1];
+ *   they are written to block_table[r, have ...], and n_pages_out[r] is the
+ *   number the request then owns;
+ *   row i of r: position p = c + i; page and slot of p where p < alloc_limit
+ *   and the table holds a page inside the pool, else -1 (not placed).
+ * A request that is not live owns nothing here: n_pages = alloc_limit =
+ * seq_lens = 0 (its table row is not touched).  Rows past the last request's
+ * get -1 everywhere, and the other two calls pass them over.
+ *
+ * n_new, ctx_len, n_pages  device int32 [B].  valid  device uint8 [B] or NULL.
+ * block_table  device int32 [B, max_pages]: entries below n_pages[r] are read
+ *              (the pages of the context), new entries written, others left.
+ * free_pages   device int32 [n_free]; free_range  device int32 [2]: first
+ *              unused entry and end, clamped to [0, n_free].
+ * out          every field; must not share memory with the inputs (n_pages and
+ *              free_head have inputs of the same name: swap two buffers).
+ * Flags: DFLASH_DEV_BAD_ROWS (n_new < 0, taken as 0; or more rows than
+ * n_rows), DFLASH_DEV_BAD_CTX_LEN (ctx_len < 0, or too long for int32: the
+ * request is passed over as not live), DFLASH_DEV_NO_PAGES (the free list or
+ * the table's width ran out: rows without a page), DFLASH_DEV_BAD_PAGE (an
+ * n_pages outside [0, max_pages], clamped; a page outside the pool in the free
+ * list or under a row: not placed).
+ * Errors: DFLASH_ERR_INVALID_ARG (null pointers, an output equal to an input,
+ * B, n_rows, n_free or max_ctx < 0), DFLASH_ERR_UNSUPPORTED_GEOM (B > 8192,
+ * n_rows >= 2^30, max_pages * page_size >= 2^31), DFLASH_ERR_CUDA.
+ * ------------------------------------------------------------------- */
+DFLASH_API int dflash_chunk_plan(const dflash_geom *g, int B, int n_rows, const int32_t *n_new,
+                                 const int32_t *ctx_len, const int32_t *n_pages,
+                                 int32_t *block_table, const int32_t *free_pages, int n_free,
+                                 const int32_t *free_range, const uint8_t *valid, int32_t max_ctx,
+                                 const dflash_chunk_outputs *out, int32_t *dev_status,
+                                 dflash_stream_t stream);
+
+/* ---------------------------------------------------------------------
+ * dflash_chunk_rope_store -- the chunk's q, k and v rows of one layer, as the
+ * projection leaves them: per-head RMSNorm (where a gain is given), rotary
+ * positions, keys and values into the paged pool.  GQA geometries.
+ *
+ * For row t at p = row_pos[t] and every head x of q (hq) and k (nkv):
+ *   x = x * gamma / sqrt(mean(x^2) + eps_k)          (gamma given)
+ *   (a, b) -> (a cos - b sin, b cos + a sin) for the rot_dim / 2 pairs of the
+ *   layout, angle p * f_j, f_j = rope_theta^(-2j/rot_dim); LINEAR: f_j /
+ *   factor; YARN: f_j (1 - u + u / factor), u = clamp((j - j0) / (j1 - j0)),
+ *   j(beta) = rot_dim ln(trained_ctx / (2 pi beta)) / (2 ln rope_theta),
+ *   j0 = max(0, floor(j(beta_fast))), j1 = min(rot_dim - 1,
+ *   ceil(j(beta_slow))) (j1 - j0 at least 0.001), cos and sin times the
+ *   magnitude.  Angles are reduced in 64-bit fixed point: positions up to
+ *   2^31 keep fp32's full accuracy.
+ * q goes to q_out, k and v (v unchanged) to (row_page, row_slot) of `layer`,
+ * each rounded to bf16 once.  A row with row_pos < 0 is passed over (q_out is
+ * left as it is); one with row_page < 0 is not stored; a page or slot outside
+ * the pool is not stored and flags DFLASH_DEV_BAD_PAGE.  Two rows must not
+ * share a slot.
+ *
+ * q, k, v      device bf16, row t at + t * stride elements, heads contiguous:
+ *              three views of a packed projection output, or dense tensors.
+ *              q may be NULL (then q_out too), k may be NULL (then v too).
+ * q_out        device bf16 rows of hq * head_dim at q_out_row_stride; may be q
+ *              itself (same pointer and stride), not overlap it otherwise.
+ * gamma_q, gamma_k  device bf16 [head_dim] or NULL.
+ * row_pos, row_page, row_slot  device int32 [n_rows] (dflash_chunk_plan).
+ * Errors: DFLASH_ERR_INVALID_ARG (null pointers, n_rows < 0, strides below the
+ * row widths, q / k / v / q_out / kv_pool not 16-byte aligned or strides not a
+ * multiple of 8, a bad spec: unknown layout or scaling, factor < 1, trained_ctx
+ * < 1, betas not positive and in order, values not finite),
+ * DFLASH_ERR_UNSUPPORTED_GEOM (MLA, head_dim not a multiple of 8 up to 256,
+ * rot_dim odd, < 2 or > head_dim, rope_theta <= 1 with YARN), DFLASH_ERR_CUDA.
+ * ------------------------------------------------------------------- */
+DFLASH_API int dflash_chunk_rope_store(const dflash_geom *g, int layer, int n_rows,
+                                       const dflash_rope_spec *rope, const void *q,
+                                       int64_t q_row_stride, const void *k, int64_t k_row_stride,
+                                       const void *v, int64_t v_row_stride, const void *gamma_q,
+                                       const void *gamma_k, const int32_t *row_pos,
+                                       const int32_t *row_page, const int32_t *row_slot,
+                                       void *q_out, int64_t q_out_row_stride, void *kv_pool,
+                                       int32_t *dev_status, dflash_stream_t stream);
+
+/* ---------------------------------------------------------------------
+ * dflash_chunk_attention -- attention of the chunk's rows over the paged
+ * cache, one layer, any number of rows per request.  GQA geometries.
+ *
+ * Row i of request r (chunk row cu_rows[r] + i) sits at p = ctx_len[r] + i and
+ * sees the keys j of its request with
+ *   lo <= j <= hi, hi = min(p, kv_len[r] - 1) (CAUSAL_TAIL) or kv_len[r] - 1
+ *   (BLOCK_BIDIR), lo = window > 0 ? max(0, p - window + 1) : 0,
+ * whose table entry is a page of the pool; with s_j = scale <q, k_j>,
+ * M = max(max_j s_j, sink_h):
+ *   out = sum_j e^(s_j-M) v_j / (sum_j e^(s_j-M) + e^(sink_h-M)),
+ * 0 where a row sees no key.  Softmax statistics and sums are fp32; the
+ * weights are rounded to bf16 for the second product, and out once.
+ * Slots that no row of the request sees are never used, whatever they hold
+ * (stale values, NaN); so are unmapped pages.  Within what some row of the
+ * request sees, values must be finite for other rows to be unaffected.
+ * Rows past cu_rows[B] and requests with no rows leave `out` as it is.
+ * kv_len outside [0, max_pages * P] is clamped and flags
+ * DFLASH_DEV_KV_LEN_RANGE; a visible key on a page outside the pool is masked
+ * and flags DFLASH_DEV_BAD_PAGE; ctx_len < 0 or cu_rows that do not ascend
+ * within [0, n_rows] give the request no rows and flag DFLASH_DEV_BAD_ROWS.
+ *
+ * q            device bf16, row t at + t * q_row_stride elements, [hq,
+ *              head_dim] contiguous.  out likewise with out_row_stride.
+ * block_table  device int32 [B, max_pages].  cu_rows  device int32 [B + 1].
+ * ctx_len      device int32 [B] (before the chunk); kv_len device int32 [B]
+ *              (after it: dflash_chunk_plan's seq_lens).
+ * sinks        device fp32 [hq] or NULL.  scale <= 0 selects 1/sqrt(head_dim).
+ * num_segments 0 = automatic; else >= 1, the number of slices each row tile's
+ *              keys are cut into (partials joined by a second launch).
+ * workspace    device scratch of dflash_chunk_attention_workspace_bytes(g, B,
+ *              n_rows, num_segments) bytes (0: none needed, may be NULL),
+ *              16-byte aligned, clobbered; calls whose GPU work overlaps need
+ *              one each.
+ * Errors: DFLASH_ERR_INVALID_ARG (null or misaligned pointers, strides below
+ * hq * head_dim or not a multiple of 8, bad indices, scale not finite, window
+ * < 0, unknown mask_mode), DFLASH_ERR_UNSUPPORTED_GEOM (MLA, head_dim not 64
+ * or 128, hq not a multiple of nkv, page_size not a multiple of 8 that divides
+ * 128 or is a multiple of 128, pool rows >= 2^31, max_pages * page_size >=
+ * 2^31, n_rows * hq >= 2^31), DFLASH_ERR_WORKSPACE_TOO_SMALL, DFLASH_ERR_CUDA.
+ * ------------------------------------------------------------------- */
+DFLASH_API int dflash_chunk_attention_num_segments(const dflash_geom *g, int B, int n_rows);
+DFLASH_API size_t dflash_chunk_attention_workspace_bytes(const dflash_geom *g, int B, int n_rows,
+                                                         int num_segments);
+DFLASH_API int dflash_chunk_attention(const dflash_geom *g, int B, int layer, int n_rows,
+                                      const void *q, int64_t q_row_stride, const void *kv_pool,
+                                      const int32_t *block_table, const int32_t *cu_rows,
+                                      const int32_t *ctx_len, const int32_t *kv_len,
+                                      int32_t window, const float *sinks, float scale,
+                                      int mask_mode, int num_segments, void *workspace,
+                                      size_t ws_bytes, void *out, int64_t out_row_stride,
+                                      int32_t *dev_status, dflash_stream_t stream);
 
 /* ---------------------------------------------------------------------
  * dflash_test_attention_skip_tile -- for tests of the bounded-wait path only.
