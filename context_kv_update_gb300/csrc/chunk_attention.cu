@@ -1,31 +1,680 @@
 // chunk_attention.cu -- attention of a ragged chunk's rows over the paged
-// cache: any number of rows per request, causal or bidirectional, sliding
-// window, sinks.
+// cache on the 5th-generation tensor cores: any number of rows per request,
+// causal or bidirectional, sliding window, sinks.
 //
-// Mathematics: softmax with one pass over the keys, a running maximum and sum
-// (fp32); the sink starts the sum as a logit without a value.
+// Mathematics: one pass over the keys in tiles of 128 with a running maximum
+// and sum per row (fp32); the reference maximum only moves when a tile exceeds
+// it by 2^8, so the accumulator in tensor memory is rarely rescaled; weights
+// are rounded to bf16 for the second product, as its operands must be.
+//
+// A work tile is up to 128 (or 256) flat rows (token, head of the KV head's
+// group) of one request, so the heads that share keys share their loads.
+// Ragged requests are mapped to tiles without a prefix sum: request r's tiles
+// start at floor(cu_r G / TR) + r, which leaves it room for ceil(rows G / TR).
+//
+// Three warpgroups a CTA, one CTA an SM: warps 0-3 and 4-7 are two softmax
+// groups (one thread a row, 128 rows), warp 8 issues every MMA, warp 9 the TMA
+// loads.  Each group has its own scores S (128 columns of tensor memory; its
+// weights P overwrite them) and accumulator O, so one group's softmax runs under
+// the other's two products:
+//   pair form (kPair): the groups hold two row tiles over the same key tiles;
+//   otherwise one row tile, the groups take the even and the odd key tiles and
+//   their halves are joined at the end (few rows: the key stream is the work).
+// K and V tiles come through one ring of 128-key slots in the order they are
+// used; products of one issuing thread execute in order, so the next scores may
+// be issued over the weights that the product before them reads.
+//
+// Few row tiles: the keys are cut into S segments (grid z), each writes (m, l,
+// O) to the workspace and chunk_merge_kernel joins them.
+//
+// Rows of K that no row of the tile sees are masked in the scores; such rows of
+// V are zeroed in shared memory before the product reads them, since a weight
+// of 0 does not silence a NaN.
+#include <cuda.h>
 #include <math.h>
+
+#include <algorithm>
 
 #include "dflash_internal.cuh"
 #include "sm100_ptx.cuh"
 
 namespace dflash {
+
+cudaError_t make_tmap_bf16_2d(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols,
+                              uint64_t row_stride_elems, uint32_t box_rows, uint32_t box_cols);
+
 namespace {
 
-struct ChunkAttnParams {
-  int B, n_rows, hq, nkv, G, hd, layer, NP, P, M, window, mask_mode;
-  float scale;
-  const uint16_t *q, *pool;
+constexpr int kKT = kAttnTileKeys;  // 128 keys per tile
+constexpr int kThreads = 384;
+// Registers: 384 threads launch with 168 each, 64512 in all; the softmax groups
+// take 216 (a row's 128 scores and 64 packed weights), the third group gives up
+// the difference: 2 x 128 x 216 + 128 x 72 = 64512.
+constexpr int kSoftmaxRegs = 216, kIssueRegs = 72;
+static_assert(256 * kSoftmaxRegs + 128 * kIssueRegs <= kThreads * 168, "register split");
+constexpr int kSmemMax = 227 * 1024;
+constexpr int kMaxSlots = 12;
+constexpr uint32_t kChunkBytes = kKT * 128;  // 64 dims of 128 rows, 128-byte swizzled
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 256;  // S of group g at 128 g, O at 256 + HD g
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct ChunkParams {
+  int B, n_rows, hq, nkv, G, layer, NP, P, M, window, mask_mode, S;
+  int box_rows, nst, skip_tile;
+  uint32_t ring_off, bar_off;
+  float scale_log2;
+  const uint16_t *q;
   int64_t qs, os;
   const int32_t *tbl, *cu, *ctx, *kv;
   const float *sinks;
+  float *ws_m, *ws_l, *ws_o;
   uint16_t *out;
   int32_t *st;
 };
 
-// One warp per (row, head); a lane holds hd / 32 dims.
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&r)[128]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, %64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, %96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+        "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
+        "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]),
+        "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]),
+        "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31]), "=f"(r[32]), "=f"(r[33]), "=f"(r[34]),
+        "=f"(r[35]), "=f"(r[36]), "=f"(r[37]), "=f"(r[38]), "=f"(r[39]), "=f"(r[40]), "=f"(r[41]),
+        "=f"(r[42]), "=f"(r[43]), "=f"(r[44]), "=f"(r[45]), "=f"(r[46]), "=f"(r[47]), "=f"(r[48]),
+        "=f"(r[49]), "=f"(r[50]), "=f"(r[51]), "=f"(r[52]), "=f"(r[53]), "=f"(r[54]), "=f"(r[55]),
+        "=f"(r[56]), "=f"(r[57]), "=f"(r[58]), "=f"(r[59]), "=f"(r[60]), "=f"(r[61]), "=f"(r[62]),
+        "=f"(r[63]), "=f"(r[64]), "=f"(r[65]), "=f"(r[66]), "=f"(r[67]), "=f"(r[68]), "=f"(r[69]),
+        "=f"(r[70]), "=f"(r[71]), "=f"(r[72]), "=f"(r[73]), "=f"(r[74]), "=f"(r[75]), "=f"(r[76]),
+        "=f"(r[77]), "=f"(r[78]), "=f"(r[79]), "=f"(r[80]), "=f"(r[81]), "=f"(r[82]), "=f"(r[83]),
+        "=f"(r[84]), "=f"(r[85]), "=f"(r[86]), "=f"(r[87]), "=f"(r[88]), "=f"(r[89]), "=f"(r[90]),
+        "=f"(r[91]), "=f"(r[92]), "=f"(r[93]), "=f"(r[94]), "=f"(r[95]), "=f"(r[96]), "=f"(r[97]),
+        "=f"(r[98]), "=f"(r[99]), "=f"(r[100]), "=f"(r[101]), "=f"(r[102]), "=f"(r[103]),
+        "=f"(r[104]), "=f"(r[105]), "=f"(r[106]), "=f"(r[107]), "=f"(r[108]), "=f"(r[109]),
+        "=f"(r[110]), "=f"(r[111]), "=f"(r[112]), "=f"(r[113]), "=f"(r[114]), "=f"(r[115]),
+        "=f"(r[116]), "=f"(r[117]), "=f"(r[118]), "=f"(r[119]), "=f"(r[120]), "=f"(r[121]),
+        "=f"(r[122]), "=f"(r[123]), "=f"(r[124]), "=f"(r[125]), "=f"(r[126]), "=f"(r[127])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+template <int N>
+__device__ __forceinline__ void regs_more() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_less() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// The request whose tiles hold work tile x (tiles of 2^shift flat rows), found
+// by the whole warp in a 32-ary search.
+__device__ __forceinline__ int64_t first_tile(const ChunkParams &p, int r, int shift) {
+  return ((static_cast<int64_t>(p.cu[r]) * p.G) >> shift) + r;
+}
+__device__ __forceinline__ int find_request(const ChunkParams &p, int64_t x, int shift, int lane) {
+  int lo = 0, n = p.B;
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const bool at = lane * step < n && first_tile(p, lo + lane * step, shift) <= x;
+    const int c = max(__popc(__ballot_sync(0xffffffffu, at)), 1) - 1;
+    lo += c * step;
+    n = min(step, n - c * step);
+  }
+  return lo;
+}
+
+// Chunk rows [a, b) of request r at positions from c over kv keys, or false
+// (flagged) where its offsets or length make no sense.
+struct Request {
+  int a, b, c, kv;
+};
+__device__ __forceinline__ bool load_request(const ChunkParams &p, int r, bool report, Request *q) {
+  q->a = p.cu[r];
+  q->b = p.cu[r + 1];
+  q->c = p.ctx[r];
+  q->kv = p.kv[r];
+  if (q->a < 0 || q->b < q->a || q->b > p.n_rows || q->c < 0 || q->c > INT32_MAX - p.n_rows) {
+    if (report) raise_status(p.st, DFLASH_DEV_BAD_ROWS);
+    return false;
+  }
+  const int cap = p.M * p.P;
+  if (q->kv < 0 || q->kv > cap) {
+    if (report) raise_status(p.st, DFLASH_DEV_KV_LEN_RANGE);
+    q->kv = q->kv < 0 ? 0 : cap;
+  }
+  return true;
+}
+
+// Keys [lo, hi] a row at position pos sees of kv.
+__device__ __forceinline__ void key_range(const ChunkParams &p, int pos, int kv, int *lo, int *hi) {
+  *hi = p.mask_mode == DFLASH_MASK_CAUSAL_TAIL ? min(pos, kv - 1) : kv - 1;
+  *lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+}
+
+// Position of a consumer or the producer in the slot ring.
+struct Ring {
+  int slot, nst;
+  uint32_t phase;
+  __device__ __forceinline__ void next() {
+    if (++slot == nst) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+template <int HD, bool kPair>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_attn_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ ChunkParams p) {
+  constexpr int kChunks = HD / 64;
+  constexpr int kShift = kPair ? 8 : 7;
+  constexpr uint32_t kSlotBytes = kChunks * kChunkBytes;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                            ~static_cast<uintptr_t>(1023));
+  uint8_t *ring = sm + p.ring_off;  // Q tiles come first
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + p.bar_off), *empty = full + kMaxSlots;
+  uint64_t *s_full = empty + kMaxSlots, *p_full = s_full + 2, *o_done = p_full + 2;
+  uint64_t *q_full = o_done + 2, *drain = q_full + 1;
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(drain + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.nst; ++i) {
+      ptx::mbar_init(ptx::smem_u32(&full[i]), 1);
+      ptx::mbar_init(ptx::smem_u32(&empty[i]), 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+      ptx::mbar_init(ptx::smem_u32(&s_full[g]), 1);
+      ptx::mbar_init(ptx::smem_u32(&p_full[g]), 4);  // one arrival per warp of the group
+      ptx::mbar_init(ptx::smem_u32(&o_done[g]), 1);
+    }
+    ptx::mbar_init(ptx::smem_u32(q_full), 8);
+    ptx::mbar_init(ptx::smem_u32(drain), 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&tm);
+  }
+  if (warp == 8) {
+    ptx::tmem_alloc(ptx::smem_u32(tslot), kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tslot;
+  ptx::griddep_launch();
+  ptx::griddep_wait();
+
+  // This CTA's rows [row0, row0 + nrow) of request r's flat rows, the keys
+  // [lo_min, hi_max] some of them sees, and its key tiles [t0, t0 + n).  Later
+  // rows see more keys: the last tiles go first.
+  const int64_t x = gridDim.x - 1 - blockIdx.x;
+  const int kvh = blockIdx.y, seg = blockIdx.z;
+  const int r = find_request(p, x, kShift, lane);
+  Request rq;
+  int row0 = 0, nrow = 0, lo_min = 0, hi_max = -1, t0 = 0, n = 0;
+  if (load_request(p, r, threadIdx.x == 0 && kvh == 0 && seg == 0, &rq)) {
+    const int64_t first = (x - first_tile(p, r, kShift)) << kShift;
+    const int total = (rq.b - rq.a) * p.G;
+    if (first >= 0 && first < total) {
+      row0 = static_cast<int>(first);
+      nrow = min(total - row0, 1 << kShift);
+      int lo, hi;
+      key_range(p, rq.c + row0 / p.G, rq.kv, &lo_min, &hi);
+      key_range(p, rq.c + (row0 + nrow - 1) / p.G, rq.kv, &lo, &hi_max);
+      if (lo_min <= hi_max) {
+        const int ta = lo_min / kKT, tb = hi_max / kKT + 1;
+        const int per = (tb - ta + p.S - 1) / p.S;
+        t0 = ta + seg * per;
+        n = max(min(tb - t0, per), 0);
+      }
+    }
+  }
+  const bool two = kPair && nrow > 128;  // both groups hold rows
+
+  if (warp >= 8) {
+    regs_less<kIssueRegs>();
+    if (n > 0 && warp == 9) {
+      // ---------------------------------------------- TMA producer
+      // A lane per box (page rows x 64 dims).  Boxes without a visible key and
+      // pages outside the pool are not loaded; their keys are masked below.
+      const int boxes = kKT / p.box_rows;
+      const uint64_t pol = (rq.b - rq.a) * p.G <= (1 << kShift) ? ptx::policy_evict_first()
+                                                                : ptx::policy_evict_normal();
+      auto fetch = [&](int t) {  // page of box `lane` of tile t, -1 where it is not loaded
+        int page = -1;
+        if (lane < boxes && t < n) {
+          const int key0 = (t0 + t) * kKT + lane * p.box_rows;
+          if (key0 <= hi_max && key0 + p.box_rows > lo_min) {
+            page = p.tbl[static_cast<int64_t>(r) * p.M + key0 / p.P];
+            if (page >= p.NP) page = -1;
+          }
+        }
+        return page;
+      };
+      Ring rg{0, p.nst, 0u};
+      bool ok = true, wrapped = false;
+      auto load = [&](int t, int kv, int page) {
+        if (!ok) return;
+        bool got = true;
+        if (lane == 0 && wrapped)
+          got = ptx::mbar_wait(ptx::smem_u32(&empty[rg.slot]), rg.phase ^ 1u, abort_flag);
+        ok = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
+        if (!ok) return;
+        const bool skip = t == p.skip_tile && kv == 0;
+        const uint32_t bar = ptx::smem_u32(&full[rg.slot]);
+        const uint32_t bytes =
+            __popc(__ballot_sync(0xffffffffu, page >= 0)) * kChunks * p.box_rows * 128u;
+        if (lane == 0 && !skip) ptx::mbar_arrive_expect_tx(bar, bytes);
+        __syncwarp();
+        const int b = lane / kChunks, c = lane % kChunks;
+        const int pg = __shfl_sync(0xffffffffu, page, b);
+        if (b < boxes && pg >= 0 && !skip) {
+          const int key0 = (t0 + t) * kKT + b * p.box_rows;
+          const int64_t row =
+              (((static_cast<int64_t>(p.layer) * p.NP + pg) * 2 + kv) * p.nkv + kvh) * p.P +
+              key0 % p.P;
+          ptx::tma_load_2d_hint(ptx::smem_u32(ring + rg.slot * kSlotBytes + c * kChunkBytes +
+                                              b * p.box_rows * 128),
+                                &tm, c * 64, static_cast<int32_t>(row), bar, pol);
+        }
+        rg.next();
+        if (rg.slot == 0) wrapped = true;
+      };
+      // a tile's pages are looked up at least one load ahead of their use
+      if constexpr (kPair) {
+        int cur = fetch(0);
+        for (int t = 0; t < n; ++t) {
+          const int nxt = fetch(t + 1);
+          load(t, 0, cur);
+          load(t, 1, cur);
+          cur = nxt;
+        }
+      } else {
+        int pa = fetch(0), pb = fetch(1);
+        load(0, 0, pa);
+        if (n > 1) load(1, 0, pb);
+        for (int t = 0; t < n; ++t) {
+          const int pc = fetch(t + 2);
+          load(t, 1, pa);
+          if (t + 2 < n) load(t + 2, 0, pc);
+          pa = pb;
+          pb = pc;
+        }
+      }
+      if (!ok && lane == 0) {  // wind down: the slots' last copies land before the CTA ends
+        for (int i = 0; i < p.nst; ++i) {
+          volatile int dummy = 0;
+          const bool later = i < rg.slot;  // filled in the current round of the ring
+          if (later || wrapped)
+            ptx::mbar_wait(ptx::smem_u32(&full[i]), later ? rg.phase : rg.phase ^ 1u, &dummy);
+        }
+      }
+    } else if (n > 0 && warp == 8 && lane == 0) {
+      // ---------------------------------------------- MMA issuer
+      constexpr uint32_t idesc_qk = ptx::idesc_bf16_f32(128, kKT, false);
+      constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, HD, true);
+      const uint64_t dq = ptx::desc_kmajor_sw128(ptx::smem_u32(sm), 0);
+      const uint64_t dk = ptx::desc_kmajor_sw128(ptx::smem_u32(ring), 0);
+      const uint64_t dv = ptx::smem_desc(ptx::smem_u32(ring), kChunkBytes, 1024, ptx::kSwizzle128B);
+      auto wait = [&](uint64_t *bar, uint32_t phase) {
+        const bool got = ptx::mbar_wait(ptx::smem_u32(bar), phase, abort_flag);
+        ptx::tc_fence_after();
+        return got;
+      };
+      auto qk = [&](int g, int slot) {  // S_g = Q K^T
+        const uint64_t a = dq + (((kPair ? g : 0) * kSlotBytes) >> 4);
+        const uint64_t b = dk + ((slot * kSlotBytes) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < HD / 16; ++ks) {
+          const uint32_t off = ((ks >> 2) * kChunkBytes + (ks & 3) * 32) >> 4;
+          ptx::mma_bf16(tmem + 128 * g, a + off, b + off, idesc_qk, ks > 0 ? 1u : 0u);
+        }
+        ptx::mma_commit(ptx::smem_u32(&s_full[g]));
+      };
+      auto pv = [&](int g, int slot, bool first) {  // O_g (+)= P V
+        const uint64_t b = dv + ((slot * kSlotBytes) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < kKT / 16; ++ks)
+          ptx::mma_bf16_ts(tmem + kColO + HD * g, tmem + 128 * g + ks * 8, b + ((ks * 2048) >> 4),
+                           idesc_pv, (!first || ks > 0) ? 1u : 0u);
+      };
+      Ring rg{0, p.nst, 0u};
+      auto release = [&](int slot) { ptx::mma_commit(ptx::smem_u32(&empty[slot])); };
+      bool ok = wait(q_full, 0u) && wait(&full[rg.slot], rg.phase);
+      if (ok) {
+        qk(0, rg.slot);
+        if (two) qk(1, rg.slot);
+        release(rg.slot);
+        rg.next();
+      }
+      if (!kPair && ok && n > 1) {
+        ok = wait(&full[rg.slot], rg.phase);
+        if (ok) {
+          qk(1, rg.slot);
+          release(rg.slot);
+          rg.next();
+        }
+      }
+      for (int t = 0; ok && t < n; ++t) {
+        const int vs = rg.slot;
+        ok = wait(&full[vs], rg.phase);
+        if (!ok) break;
+        rg.next();
+        const int ks = rg.slot;
+        const uint32_t kphase = rg.phase;
+        if constexpr (kPair) {
+          const bool more = t + 1 < n;
+          for (int g = 0; ok && g < (two ? 2 : 1); ++g) {
+            ok = wait(&p_full[g], static_cast<uint32_t>(t & 1));
+            if (!ok) break;
+            pv(g, vs, t == 0);
+            if (more) {
+              if (g == 0) ok = wait(&full[ks], kphase);
+              if (ok) qk(g, ks);
+            } else {
+              ptx::mma_commit(ptx::smem_u32(&o_done[g]));
+            }
+          }
+          if (!ok) break;
+          release(vs);
+          if (more) {
+            release(ks);
+            rg.next();
+          }
+        } else {
+          const int g = t & 1;
+          ok = wait(&p_full[g], static_cast<uint32_t>((t >> 1) & 1));
+          if (!ok) break;
+          pv(g, vs, t < 2);
+          release(vs);
+          if (t + 2 < n) {
+            ok = wait(&full[ks], kphase);
+            if (!ok) break;
+            qk(g, ks);
+            release(ks);
+            rg.next();
+          }
+          if (t + 1 == n) ptx::mma_commit(ptx::smem_u32(&o_done[0]));
+        }
+      }
+      if (!ok) {
+        ptx::mma_commit(ptx::smem_u32(drain));
+        volatile int dummy = 0;
+        ptx::mbar_wait(ptx::smem_u32(drain), 0u, &dummy);
+      }
+    }
+  } else {
+    regs_more<kSoftmaxRegs>();
+    if (nrow > 0) {
+      // ---------------------------------------------- softmax groups
+      const int g = warp >> 2;
+      const int tid = threadIdx.x & 127;  // TMEM lane = row of the group's tile
+      const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t tm_s = tmem + 128 * g + lane_off, tm_o = tmem + kColO + HD * g + lane_off;
+
+      if (n > 0) {
+        // Q rows -> shared memory, K-major, 128-byte swizzle (rows past the end: 0)
+        constexpr int kUnits = HD / 8;  // 16-byte units of a row
+        constexpr int kQRows = kPair ? 256 : 128;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < kQRows * kUnits; i += 256) {
+          const int row = i / kUnits, u = i % kUnits;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (row < nrow) {
+            const int R = row0 + row, tok = R / p.G;
+            v = reinterpret_cast<const uint4 *>(
+                p.q + (rq.a + tok) * p.qs + static_cast<int64_t>(kvh * p.G + R - tok * p.G) * HD)[u];
+          }
+          *reinterpret_cast<uint4 *>(sm + ((row >> 7) * kChunks + (u >> 3)) * kChunkBytes +
+                                     (row & 127) * 128 + (((u & 7) ^ (row & 7)) << 4)) = v;
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(q_full));
+      }
+
+      // this thread's row and the keys it sees
+      const int rt = (kPair ? 128 * g : 0) + tid;
+      const bool real = rt < nrow;
+      const int tok = (row0 + (real ? rt : 0)) / p.G;
+      const int h = kvh * p.G + (row0 + (real ? rt : 0)) - tok * p.G;
+      int lo = 0, hi = -1;
+      if (real) key_range(p, rq.c + tok, rq.kv, &lo, &hi);
+
+      // pages of the segment outside the pool: none, as a rule
+      bool bad_pages = false;
+      if (n > 0) {
+        const int ka = max(lo_min, t0 * kKT), kb = min(hi_max, (t0 + n) * kKT - 1);
+        for (int lp = ka / p.P + static_cast<int>(threadIdx.x); lp <= kb / p.P; lp += 256) {
+          const int page = p.tbl[static_cast<int64_t>(r) * p.M + lp];
+          bad_pages |= page < 0 || page >= p.NP;
+        }
+        bad_pages = ptx::bar_or(1, 256, bad_pages);
+        if (bad_pages && threadIdx.x == 0) raise_status(p.st, DFLASH_DEV_BAD_PAGE);
+      }
+
+      float m_ref = -INFINITY, l = 0.f;
+      bool ok = true;
+      int u = 0;
+      for (int t = kPair ? 0 : g; t < n && (!kPair || g == 0 || two); t += kPair ? 1 : 2, ++u) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(ptx::smem_u32(&s_full[g]),
+                                                    static_cast<uint32_t>(u & 1), abort_flag));
+        if (!ok) break;
+        ptx::tc_fence_after();
+        float sv[128];
+        tmem_ld128(tm_s, sv);
+        const int kb = (t0 + t) * kKT;
+        // the tile holds keys that some row of the CTA does not see, or bad pages
+        const bool edge = bad_pages || kb < lo_min || kb + kKT - 1 > hi_max;
+        if (edge) {
+          uint32_t okm[4] = {~0u, ~0u, ~0u, ~0u};  // keys on pages of the pool
+          if (bad_pages) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int lp = (kb + 32 * w + lane) / p.P;
+              const int page = lp < p.M ? p.tbl[static_cast<int64_t>(r) * p.M + lp] : -1;
+              okm[w] = __ballot_sync(0xffffffffu, page >= 0 && page < p.NP);
+            }
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (!((okm[c >> 5] >> (c & 31)) & 1u)) sv[c] = -INFINITY;
+          }
+          // V rows no row of this tile sees: zero, before P is handed over
+          const int at = kPair ? 2 * t + 1 : min(t + 2, n) + t;  // V's place in the ring's order
+          const int slot = at % p.nst;
+          ok = __all_sync(0xffffffffu,
+                          ptx::mbar_wait(ptx::smem_u32(&full[slot]),
+                                         static_cast<uint32_t>((at / p.nst) & 1), abort_flag));
+          if (!ok) break;
+          const int key = kb + tid, w4 = warp & 3;
+          const uint32_t mine = w4 == 0 ? okm[0] : w4 == 1 ? okm[1] : w4 == 2 ? okm[2] : okm[3];
+          if (key < lo_min || key > hi_max || !((mine >> lane) & 1u)) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+              uint4 *v = reinterpret_cast<uint4 *>(ring + slot * kSlotBytes + c * kChunkBytes +
+                                                   tid * 128);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[(e + tid) & 7] = make_uint4(0, 0, 0, 0);
+            }
+          }
+          ptx::fence_proxy_async_smem();
+        }
+        if (!(lo <= kb && hi >= kb + kKT - 1)) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (kb + c < lo || kb + c > hi) sv[c] = -INFINITY;
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mx[c] = sv[c];
+#pragma unroll
+        for (int c = 4; c < 128; c += 8) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c + e + 4 < 128) mx[e] = fmaxf(fmaxf(mx[e], sv[c + e]), sv[c + e + 4]);
+            else mx[e] = fmaxf(mx[e], sv[c + e]);
+        }
+        const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        float corr = 1.f;
+        bool need = false;
+        if (m_ref == -INFINITY) {
+          m_ref = tmax;
+        } else if (tmax > m_ref + 8.f) {
+          corr = ptx::ex2(m_ref - tmax);
+          m_ref = tmax;
+          need = true;
+        }
+        // the group's previous product completed before this S did
+        if (__any_sync(0xffffffffu, need)) {
+          for (int c = 0; c < HD; c += 16) {
+            uint32_t ov[16];
+            ptx::tmem_ld16_sync(tm_o + c, ov);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * corr);
+            ptx::tmem_st16(tm_o + c, ov);
+          }
+        }
+        const float nm = m_ref == -INFINITY ? 0.f : -m_ref;  // nothing seen yet: weights 2^-inf
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float a = ptx::ex2(fmaf(sv[64 * c + 2 * e], p.scale_log2, nm));
+            const float b = ptx::ex2(fmaf(sv[64 * c + 2 * e + 1], p.scale_log2, nm));
+            sum[(2 * e) & 3] += a;
+            sum[(2 * e + 1) & 3] += b;
+            pk[e] = ptx::pack_bf16x2(a, b);
+          }
+          tmem_st32(tm_s + 32 * c, pk);
+        }
+        l = l * corr + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&p_full[g]));
+      }
+      // ---------------------------------------------- epilogue
+      const bool mine = kPair ? u > 0 : n > 0;  // a product to wait for
+      if (mine && ok) {
+        ok = __all_sync(0xffffffffu,
+                        ptx::mbar_wait(ptx::smem_u32(&o_done[kPair ? g : 0]), 0u, abort_flag));
+        ptx::tc_fence_after();
+      }
+      // the row's state over both groups, and this thread's share of its dims
+      constexpr int kDims = kPair ? HD : HD / 2;
+      const int d0 = kPair ? 0 : g * kDims;
+      float m = ok ? m_ref : -INFINITY, own = 1.f, other = 0.f;
+      const float *xo = nullptr;
+      if constexpr (!kPair) {
+        // the other group's half of the dims goes through the idle ring
+        float *sx = reinterpret_cast<float *>(ring);  // [2][HD / 2][128], then m and l [2][128]
+        float *smx = sx + HD * 128;
+        smx[g * 128 + tid] = m;
+        smx[256 + g * 128 + tid] = l;
+        if (u > 0 && ok) {
+          for (int c = 0; c < kDims; c += 16) {
+            uint32_t ov[16];
+            ptx::tmem_ld16_sync(tm_o + (g ^ 1) * kDims + c, ov);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              sx[(g * kDims + c + e) * 128 + tid] = __uint_as_float(ov[e]);
+          }
+        }
+        const bool bad = ptx::bar_or(1, 256, !ok);
+        const float m2 = smx[(g ^ 1) * 128 + tid], l2 = smx[256 + (g ^ 1) * 128 + tid];
+        m = bad ? -INFINITY : fmaxf(m_ref, m2);
+        own = bad || m_ref == -INFINITY ? 0.f : ptx::ex2(m_ref - m);
+        other = bad || m2 == -INFINITY ? 0.f : ptx::ex2(m2 - m);
+        l = l * own + l2 * other;
+        xo = sx + (g ^ 1) * kDims * 128 + tid;
+      }
+      const bool any = real && m != -INFINITY;  // the row saw a key
+      const int64_t orow = static_cast<int64_t>(rq.a) + tok;
+      float gain = 1.f;
+      if (p.S == 1) {
+        float top = m, den = l;
+        if (p.sinks && any) {
+          const float sk = p.sinks[h] * kLog2e;
+          top = fmaxf(m, sk);
+          den = l * ptx::ex2(m - top) + ptx::ex2(sk - top);
+        }
+        gain = any ? ptx::ex2(m - top) / den : 0.f;
+      } else if (real && (kPair || g == 0)) {
+        const int64_t w = (orow * p.hq + h) * p.S + seg;
+        p.ws_m[w] = m;
+        p.ws_l[w] = any ? l : 0.f;
+      }
+      own *= gain;
+      other *= gain;
+      const bool has = u > 0 && ok;  // this group's accumulator was written
+#pragma unroll
+      for (int c = 0; c < kDims; c += 16) {
+        float o[16];
+        if (has) {  // warp-uniform: tensor memory loads take the whole warp
+          uint32_t ov[16];
+          ptx::tmem_ld16_sync(tm_o + d0 + c, ov);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = own != 0.f ? __uint_as_float(ov[e]) * own : 0.f;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = 0.f;
+        }
+        if constexpr (!kPair) {
+          if (other != 0.f) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] += xo[(c + e) * 128] * other;
+          }
+        }
+        if (!real) continue;
+        if (p.S == 1) {
+          uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * p.os +
+                                                 static_cast<int64_t>(h) * HD + d0 + c);
+          uint32_t w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = ptx::pack_bf16x2(o[2 * e], o[2 * e + 1]);
+          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        } else if (any) {
+          float4 *dst = reinterpret_cast<float4 *>(
+              p.ws_o + ((orow * p.hq + h) * p.S + seg) * HD + d0 + c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+      }
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) raise_status(p.st, DFLASH_DEV_WAIT_TIMEOUT);
+  if (warp == 8) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the S partial states of a row: one warp per (row, head), HD / 32 dims a
+// lane.  Rows of no request are passed over, as the main kernel passes them.
 template <int HD>
-__global__ void __launch_bounds__(128) chunk_attn_rows_kernel(const ChunkAttnParams p) {
+__global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkParams p) {
   constexpr int E = HD / 32;
   ptx::griddep_launch();
   ptx::griddep_wait();
@@ -33,77 +682,97 @@ __global__ void __launch_bounds__(128) chunk_attn_rows_kernel(const ChunkAttnPar
   const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int t = static_cast<int>(w / p.hq), h = static_cast<int>(w % p.hq);
   if (t >= p.n_rows) return;
-  int lo = 0, hi = p.B - 1;  // the last request whose first row is <= t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.cu[mid] <= t) lo = mid; else hi = mid - 1;
+  int lo = 0, n = p.B;  // the last request whose first row is <= t
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const bool at = lane * step < n && p.cu[lo + lane * step] <= t;
+    const int c = max(__popc(__ballot_sync(0xffffffffu, at)), 1) - 1;
+    lo += c * step;
+    n = min(step, n - c * step);
   }
-  const int r = lo, a = p.cu[r], b = p.cu[r + 1];
-  if (t < a || t >= b) return;
-  const int c = p.ctx[r];
-  if (a < 0 || b > p.n_rows || c < 0) {
-    if (lane == 0) raise_status(p.st, DFLASH_DEV_BAD_ROWS);
-    return;
-  }
-  int kv = p.kv[r];
-  const int cap = p.M * p.P;
-  if (kv < 0 || kv > cap) {
-    if (lane == 0) raise_status(p.st, DFLASH_DEV_KV_LEN_RANGE);
-    kv = kv < 0 ? 0 : cap;
-  }
-  const int pos = c + (t - a);
-  const int last = p.mask_mode == DFLASH_MASK_CAUSAL_TAIL ? min(pos, kv - 1) : kv - 1;
-  const int first = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-  float qv[E], acc[E];
-  const uint16_t *q = p.q + t * p.qs + static_cast<int64_t>(h) * HD + lane * E;
+  Request rq;
+  if (!load_request(p, lo, false, &rq) || t < rq.a || t >= rq.b) return;
+  const float *o = p.ws_o + w * p.S * HD + lane * E;
+  float m = p.sinks ? p.sinks[h] * kLog2e : -INFINITY, l = p.sinks ? 1.f : 0.f;
+  float acc[E] = {};
+  for (int s0 = 0; s0 < p.S; s0 += 32) {
+    const bool in = s0 + lane < p.S;
+    const float mj = in ? p.ws_m[w * p.S + s0 + lane] : -INFINITY;
+    const float lj = in ? p.ws_l[w * p.S + s0 + lane] : 0.f;
+    const float mn = fmaxf(m, warp_max(mj));
+    if (mn == -INFINITY) continue;
+    const float sc = m == -INFINITY ? 0.f : ptx::ex2(m - mn);
+    const float wj = mj == -INFINITY ? 0.f : ptx::ex2(mj - mn);
+    l = l * sc + warp_sum(wj * lj);
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    qv[e] = bf16_to_f32(q[e]) * p.scale;
-    acc[e] = 0.f;
-  }
-  float m = p.sinks ? p.sinks[h] : -INFINITY, l = p.sinks ? 1.f : 0.f;
-  for (int j = first; j <= last; ++j) {
-    const int page = p.tbl[static_cast<int64_t>(r) * p.M + j / p.P];
-    if (page < 0 || page >= p.NP) {
-      if (lane == 0) raise_status(p.st, DFLASH_DEV_BAD_PAGE);
-      continue;
+    for (int e = 0; e < E; ++e) acc[e] *= sc;
+    for (int j = 0; j < min(32, p.S - s0); ++j) {
+      const float ws = __shfl_sync(0xffffffffu, wj, j);
+      if (ws == 0.f) continue;  // also a segment without keys, whose O is not written
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += ws * o[static_cast<int64_t>(s0 + j) * HD + e];
     }
-    const size_t row = ((static_cast<size_t>(p.layer) * p.NP + page) * 2 * p.nkv + h / p.G) * p.P +
-                       j % p.P;
-    const uint16_t *k = p.pool + row * HD + lane * E;
-    const uint16_t *v = k + static_cast<size_t>(p.nkv) * p.P * HD;
-    float d = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) d += qv[e] * bf16_to_f32(k[e]);
-    d = warp_sum(d);
-    const float mn = fmaxf(m, d);
-    const float sc = m == -INFINITY ? 0.f : __expf(m - mn), w1 = __expf(d - mn);
-    l = l * sc + w1;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * sc + w1 * bf16_to_f32(v[e]);
     m = mn;
   }
-  uint16_t *o = p.out + t * p.os + static_cast<int64_t>(h) * HD + lane * E;
+  uint16_t *dst = p.out + t * p.os + static_cast<int64_t>(h) * HD + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = f32_to_bf16_rn(l > 0.f ? acc[e] / l : 0.f);
+  for (int e = 0; e < E; ++e) dst[e] = f32_to_bf16_rn(l > 0.f ? acc[e] / l : 0.f);
+}
+
+// Pair form where the mean request fills more than one 128-row tile.
+bool pair_form(const dflash_geom &g, int B, int n_rows) {
+  return static_cast<int64_t>(n_rows) * (g.hq / g.nkv) > 128LL * B;
+}
+
+// Work tiles of a chunk, at most.
+int64_t chunk_tiles(const dflash_geom &g, int B, int n_rows) {
+  return ((static_cast<int64_t>(n_rows) * (g.hq / g.nkv)) >> (pair_form(g, B, n_rows) ? 8 : 7)) + B;
 }
 
 }  // namespace
 
 int chunk_attention_num_segments(const dflash_geom &g, int B, int n_rows) {
-  (void)g;
-  (void)B;
-  (void)n_rows;
-  return 1;
+  const int64_t ctas = chunk_tiles(g, B, n_rows) * g.nkv;
+  int64_t S = device_sm_count() / ctas;
+  const int64_t most = (static_cast<int64_t>(g.max_pages) * g.page_size + kKT - 1) / kKT;
+  S = S > most ? most : S;
+  return static_cast<int>(S < 1 ? 1 : S);
 }
 
 size_t chunk_attention_workspace_bytes(const dflash_geom &g, int B, int n_rows, int S) {
-  (void)g;
-  (void)B;
-  (void)n_rows;
-  (void)S;
-  return 0;
+  if (B < 1 || n_rows < 1) return 0;
+  if (S <= 0) S = chunk_attention_num_segments(g, B, n_rows);
+  if (S == 1) return 0;
+  const size_t rows = static_cast<size_t>(n_rows) * g.hq * S;
+  return 2 * align_up(rows * sizeof(float), 256) + rows * g.head_dim * sizeof(float);
 }
+
+namespace {
+
+template <int HD, bool kPair>
+cudaError_t launch_main(const CUtensorMap &tm, ChunkParams p, dim3 grid, cudaStream_t s) {
+  constexpr uint32_t slot = HD / 64 * kChunkBytes, q_bytes = (kPair ? 2 : 1) * slot;
+  constexpr uint32_t bars = (2 * kMaxSlots + 8) * 8 + 16;
+  // the epilogue's exchange (128 rows x HD floats, 4 KB of states... in the ring)
+  p.nst = std::min<int>(kMaxSlots, (kSmemMax - 1024 - bars - q_bytes) / slot);
+  p.ring_off = q_bytes;
+  p.bar_off = q_bytes + p.nst * slot;
+  const cudaError_t e = ensure_smem_limit<chunk_attn_kernel<HD, kPair>>(kSmemMax);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = 1024 + p.bar_off + bars;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_attn_kernel<HD, kPair>, tm, p);
+}
+
+}  // namespace
 
 cudaError_t launch_chunk_attention(const dflash_geom &g, int B, int layer, int n_rows,
                                    const void *q, int64_t q_stride, const void *pool,
@@ -111,24 +780,23 @@ cudaError_t launch_chunk_attention(const dflash_geom &g, int B, int layer, int n
                                    const int32_t *kv, int32_t window, const float *sinks,
                                    float scale, int mask_mode, int S, void *ws, void *out,
                                    int64_t out_stride, int32_t *st, cudaStream_t s) {
-  (void)S;
-  (void)ws;
-  ChunkAttnParams p;
+  ChunkParams p = {};
   p.B = B;
   p.n_rows = n_rows;
   p.hq = g.hq;
   p.nkv = g.nkv;
   p.G = g.hq / g.nkv;
-  p.hd = g.head_dim;
   p.layer = layer;
   p.NP = g.num_pool_pages;
   p.P = g.page_size;
   p.M = g.max_pages;
   p.window = window;
   p.mask_mode = mask_mode;
-  p.scale = scale;
+  p.S = S;
+  p.box_rows = std::min(p.P, kKT);
+  p.skip_tile = attention_test_skip_tile_value();
+  p.scale_log2 = scale * kLog2e;  // scale > 0 (validated by the caller)
   p.q = static_cast<const uint16_t *>(q);
-  p.pool = static_cast<const uint16_t *>(pool);
   p.qs = q_stride;
   p.os = out_stride;
   p.tbl = tbl;
@@ -136,8 +804,25 @@ cudaError_t launch_chunk_attention(const dflash_geom &g, int B, int layer, int n
   p.ctx = ctx;
   p.kv = kv;
   p.sinks = sinks;
+  const size_t rows = static_cast<size_t>(n_rows) * g.hq * S;
+  char *w = static_cast<char *>(ws);
+  p.ws_m = reinterpret_cast<float *>(w);
+  p.ws_l = reinterpret_cast<float *>(w + align_up(rows * sizeof(float), 256));
+  p.ws_o = reinterpret_cast<float *>(w + 2 * align_up(rows * sizeof(float), 256));
   p.out = static_cast<uint16_t *>(out);
   p.st = st;
+  CUtensorMap tm;
+  const uint64_t pool_rows = static_cast<uint64_t>(g.num_layers) * g.num_pool_pages * 2 * g.nkv *
+                             static_cast<uint64_t>(g.page_size);
+  cudaError_t e = make_tmap_bf16_2d(&tm, pool, pool_rows, g.head_dim, g.head_dim, p.box_rows, 64);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(chunk_tiles(g, B, n_rows)), g.nkv, S);
+  const bool pair = pair_form(g, B, n_rows);
+  if (g.head_dim == 64)
+    e = pair ? launch_main<64, true>(tm, p, grid, s) : launch_main<64, false>(tm, p, grid, s);
+  else
+    e = pair ? launch_main<128, true>(tm, p, grid, s) : launch_main<128, false>(tm, p, grid, s);
+  if (e != cudaSuccess || S == 1) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(n_rows) * g.hq + 3) / 4));
@@ -147,8 +832,8 @@ cudaError_t launch_chunk_attention(const dflash_geom &g, int B, int layer, int n
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return g.head_dim == 64 ? cudaLaunchKernelEx(&cfg, chunk_attn_rows_kernel<64>, p)
-                          : cudaLaunchKernelEx(&cfg, chunk_attn_rows_kernel<128>, p);
+  return g.head_dim == 64 ? cudaLaunchKernelEx(&cfg, chunk_merge_kernel<64>, p)
+                          : cudaLaunchKernelEx(&cfg, chunk_merge_kernel<128>, p);
 }
 
 }  // namespace dflash

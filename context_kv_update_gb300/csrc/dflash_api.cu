@@ -450,7 +450,7 @@ int chunk_attention_geom_status(const dflash_geom *g, int B, int n_rows) {
   // 32-bit
   const long long pool_rows =
       2LL * g->num_layers * g->num_pool_pages * P * static_cast<long long>(g->nkv);
-  if (pool_rows >= (1LL << 31) || static_cast<long long>(g->max_pages) * P >= (1LL << 31) ||
+  if (pool_rows >= (1LL << 31) || static_cast<long long>(g->max_pages) * P > (1LL << 31) - 2 * kAttnTileKeys ||
       static_cast<long long>(n_rows) * g->hq >= (1LL << 31) || B >= (1 << 24))
     return DFLASH_ERR_UNSUPPORTED_GEOM;
   return DFLASH_OK;

@@ -731,8 +731,8 @@ DFLASH_API int dflash_chunk_rope_store(const dflash_geom *g, int layer, int n_ro
  * hq * head_dim or not a multiple of 8, bad indices, scale not finite, window
  * < 0, unknown mask_mode), DFLASH_ERR_UNSUPPORTED_GEOM (MLA, head_dim not 64
  * or 128, hq not a multiple of nkv, page_size not a multiple of 8 that divides
- * 128 or is a multiple of 128, pool rows >= 2^31, max_pages * page_size >=
- * 2^31, n_rows * hq >= 2^31), DFLASH_ERR_WORKSPACE_TOO_SMALL, DFLASH_ERR_CUDA.
+ * 128 or is a multiple of 128, pool rows >= 2^31, max_pages * page_size >
+ * 2^31 - 256, n_rows * hq >= 2^31), DFLASH_ERR_WORKSPACE_TOO_SMALL, DFLASH_ERR_CUDA.
  * ------------------------------------------------------------------- */
 DFLASH_API int dflash_chunk_attention_num_segments(const dflash_geom *g, int B, int n_rows);
 DFLASH_API size_t dflash_chunk_attention_workspace_bytes(const dflash_geom *g, int B, int n_rows,
@@ -748,9 +748,10 @@ DFLASH_API int dflash_chunk_attention(const dflash_geom *g, int B, int layer, in
 
 /* ---------------------------------------------------------------------
  * dflash_test_attention_skip_tile -- for tests of the bounded-wait path only.
- * While set (tile >= 0), every dflash_block_attention launched from the
- * calling host thread leaves key tile `tile` of each CTA's segment unloaded
- * (MLA: the first 64-key half of it): the wait for it runs out (about 2 s),
+ * While set (tile >= 0), every dflash_block_attention and
+ * dflash_chunk_attention launched from the calling host thread leaves key tile
+ * `tile` of each CTA's segment unloaded (MLA: the first 64-key half of it;
+ * chunks: its keys, not its values): the wait for it runs out (about 2 s),
  * the kernel winds down, ORs
  * DFLASH_DEV_WAIT_TIMEOUT into *dev_status and the context stays usable.
  * tile < 0 turns it off (the default).  Never set it in production.

@@ -119,11 +119,13 @@ def test_attention_refusals(lib):
                dict(mask=2), dict(S=-1), dict(scale=float("inf")), dict(scale=float("nan")),
                dict(q=None), dict(pool=None), dict(tbl=None), dict(cu=None), dict(ctx=None),
                dict(kv=None), dict(out=None), dict(q=ODD), dict(out=ODD), dict(pool=ODD),
-               dict(qs=248), dict(qs=260), dict(os=0), dict(os=257)):
+               dict(qs=248), dict(qs=260), dict(os=0), dict(os=257), dict(S=3, ws=None),
+               dict(S=3, ws=ODD)):
         assert _attn(lib, **kw) == bad, kw
+    assert _attn(lib, S=3, nb=64) == _lib.DFLASH_ERR_WORKSPACE_TOO_SMALL
     for kw in (dict(g=_geom(kind="mla")), dict(g=_geom(hd=96)), dict(g=_geom(P=12)),
                dict(g=_geom(P=48)), dict(g=_geom(P=192)), dict(g=_geom(num_pool_pages=1 << 25)),
-               dict(g=_geom(max_pages=1 << 27)), dict(n_rows=1 << 29)):
+               dict(g=_geom(max_pages=(1 << 27) - 15)), dict(n_rows=1 << 29)):
         assert _attn(lib, **kw) == geo, kw
 
 
@@ -132,6 +134,7 @@ def test_attention_workspace(lib):
     G = ctypes.byref(g)
     ws = lib.dflash_chunk_attention_workspace_bytes
     assert ws(G, 2, 6, 1) == 0            # one segment writes out directly
+    assert ws(G, 2, 6, 3) >= 3 * 6 * 4 * (64 + 2) * 4
     assert ws(G, 2, 6, -1) == ws(None, 2, 6, 3) == 0
     assert lib.dflash_chunk_attention_num_segments(G, 2, 6) >= 1
     assert lib.dflash_chunk_attention_num_segments(G, 0, 6) == 0

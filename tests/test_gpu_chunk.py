@@ -489,6 +489,21 @@ def test_attention_long_cache(dl):
     np.testing.assert_array_equal(bf16_f64(bits(out)).reshape(near.shape), near)
 
 
+@pytest.mark.parametrize("rows", [1, 90])
+def test_attention_unloaded_tile_times_out_cleanly(dl, rows):
+    """The bounded waits: the producer leaves one key tile unloaded, the kernel
+    winds down and sets its status, and the next call is right."""
+    rng = np.random.default_rng(22)
+    kw = dict(hq=4, nkv=2, hd=64, P=16)
+    pb = attn_problem(rng, [rows], [1000], **kw)
+    dl.dflash_test_attention_skip_tile(2)
+    try:
+        run_attn(dl, pb, **kw, S=1, check=False, flags=dl._lib.DEV_WAIT_TIMEOUT)
+    finally:
+        dl.dflash_test_attention_skip_tile(-1)
+    run_attn(dl, pb, **kw, S=1)
+
+
 # ------------------------------------------------------------------ together
 
 
