@@ -14,9 +14,9 @@
 //
 // Three warpgroups a CTA, one CTA an SM: warps 0-3 and 4-7 are two softmax
 // groups (one thread a row, 128 rows), warp 8 issues every MMA, warp 9 the TMA
-// loads.  Each group has its own scores S (128 columns of tensor memory; its
-// weights P overwrite them) and accumulator O, so one group's softmax runs under
-// the other's two products:
+// loads.  Each group has its own scores S (128 columns of tensor
+// memory; its weights P overwrite them) and accumulator O, so one group's softmax
+// runs under the other's two products:
 //   pair form (kPair): the groups hold two row tiles over the same key tiles;
 //   otherwise one row tile, the groups take the even and the odd key tiles and
 //   their halves are joined at the end (few rows: the key stream is the work).
@@ -53,7 +53,7 @@ constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 216, kIssueRegs = 72;
 static_assert(256 * kSoftmaxRegs + 128 * kIssueRegs <= kThreads * 168, "register split");
 constexpr int kSmemMax = 227 * 1024;
-constexpr int kMaxSlots = 12;
+constexpr int kDone = 8;  // barriers of the iterations in flight (more than half the slots + 1)
 constexpr uint32_t kChunkBytes = kKT * 128;  // 64 dims of 128 rows, 128-byte swizzled
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;  // S of group g at 128 g, O at 256 + HD g
@@ -61,8 +61,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 struct ChunkParams {
   int B, n_rows, hq, nkv, G, layer, NP, P, M, window, mask_mode, S;
-  int box_rows, nst, skip_tile;
-  uint32_t ring_off, bar_off;
+  int box_rows, skip_tile;
   float scale_log2;
   const uint16_t *q;
   int64_t qs, os;
@@ -109,6 +108,25 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[30]), "r"(r[31])
       : "memory");
 }
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 template <int N>
 __device__ __forceinline__ void regs_more() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -116,6 +134,42 @@ __device__ __forceinline__ void regs_more() {
 template <int N>
 __device__ __forceinline__ void regs_less() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Wait on phase `parity` of `bar`, bounded by the SM clock (a read of the
+// global timer costs more than most of these waits): false, with *abort set,
+// after about two seconds, or once another thread has set *abort.  kSpin: with
+// the probe that does not suspend the thread (waking up takes longer than the
+// wait does), for the waits between the products and the softmax.
+template <bool kSpin>
+__device__ __forceinline__ bool chunk_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+  constexpr long long kLimit = 4000000000ll;  // cycles
+  auto probe = [&] { return kSpin ? ptx::mbar_test(bar, parity) : ptx::mbar_try_wait(bar, parity); };
+  if (probe()) return true;
+  const long long t0 = clock64();
+  for (uint32_t n = 1;; ++n) {
+    if (probe()) return true;
+    if ((n & 255u) == 0) {
+      if (*abort) return false;
+      if (clock64() - t0 > kLimit) {
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// One lane of a converged warp, the same one at every call.  Issuing under it
+// with warp-uniform operands lets the compiler keep descriptors in uniform
+// registers: a lane-0 branch needs several times the instructions for each MMA,
+// and they wait for the softmax warps that share the scheduler (measured with
+// fma-bound neighbours: 262 cycles an MMA against 134; 64 without any).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
 }
 
 // The request whose tiles hold work tile x (tiles of 2^shift flat rows), found
@@ -163,16 +217,17 @@ __device__ __forceinline__ void key_range(const ChunkParams &p, int pos, int kv,
   *lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
 }
 
-// Position of a consumer or the producer in the slot ring.
-struct Ring {
-  int slot, nst;
-  uint32_t phase;
-  __device__ __forceinline__ void next() {
-    if (++slot == nst) {
-      slot = 0;
-      phase ^= 1u;
-    }
-  }
+// Shared memory: Q tiles, the slot ring, barriers.
+template <int HD, bool kPair>
+struct Layout {
+  static constexpr uint32_t kSlotBytes = HD / 64 * kChunkBytes;
+  static constexpr uint32_t kRing = (kPair ? 2 : 1) * kSlotBytes;
+  static constexpr uint32_t kBarBytes = (12 + kDone + 12) * 8;
+  static constexpr int kFit = (kSmemMax - 1024 - kBarBytes - kRing) / kSlotBytes;
+  static constexpr int kSlots = kFit < 12 ? kFit : 12;
+  static constexpr uint32_t kBars = kRing + kSlots * kSlotBytes;
+  static constexpr uint32_t kBytes = 1024 + kBars + kBarBytes;
+  static_assert(kSlots >= 5 && kDone > kSlots / 2 + 1, "");
 };
 
 template <int HD, bool kPair>
@@ -180,23 +235,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ ChunkParams p) {
   constexpr int kChunks = HD / 64;
   constexpr int kShift = kPair ? 8 : 7;
-  constexpr uint32_t kSlotBytes = kChunks * kChunkBytes;
+  using Lay = Layout<HD, kPair>;
+  constexpr uint32_t kSlotBytes = Lay::kSlotBytes;
+  constexpr int kSlots = Lay::kSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                             ~static_cast<uintptr_t>(1023));
-  uint8_t *ring = sm + p.ring_off;  // Q tiles come first
-  uint64_t *full = reinterpret_cast<uint64_t *>(sm + p.bar_off), *empty = full + kMaxSlots;
-  uint64_t *s_full = empty + kMaxSlots, *p_full = s_full + 2, *o_done = p_full + 2;
+  uint8_t *ring = sm + Lay::kRing;  // Q tiles come first
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + Lay::kBars), *done = full + 12;
+  uint64_t *s_full = done + kDone, *p_full = s_full + 2, *o_done = p_full + 2;
   uint64_t *q_full = o_done + 2, *drain = q_full + 1;
   uint32_t *tslot = reinterpret_cast<uint32_t *>(drain + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < p.nst; ++i) {
-      ptx::mbar_init(ptx::smem_u32(&full[i]), 1);
-      ptx::mbar_init(ptx::smem_u32(&empty[i]), 1);
-    }
+    for (int i = 0; i < kSlots; ++i) ptx::mbar_init(ptx::smem_u32(&full[i]), 1);
+    for (int i = 0; i < kDone; ++i) ptx::mbar_init(ptx::smem_u32(&done[i]), 1);
     for (int g = 0; g < 2; ++g) {
       ptx::mbar_init(ptx::smem_u32(&s_full[g]), 1);
       ptx::mbar_init(ptx::smem_u32(&p_full[g]), 4);  // one arrival per warp of the group
@@ -221,9 +276,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // This CTA's rows [row0, row0 + nrow) of request r's flat rows, the keys
   // [lo_min, hi_max] some of them sees, and its key tiles [t0, t0 + n).  Later
-  // rows see more keys: the last tiles go first.
-  const int64_t x = gridDim.x - 1 - blockIdx.x;
-  const int kvh = blockIdx.y, seg = blockIdx.z;
+  // rows see more keys, so the last tiles of all heads go first (heads one after
+  // the other leave a head's longest tiles for the end).
+  const int kvh = blockIdx.x % p.nkv, seg = blockIdx.z;
+  const int64_t x = gridDim.x / p.nkv - 1 - blockIdx.x / p.nkv;
   const int r = find_request(p, x, kShift, lane);
   Request rq;
   int row0 = 0, nrow = 0, lo_min = 0, hi_max = -1, t0 = 0, n = 0;
@@ -248,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 8) {
     regs_less<kIssueRegs>();
-    if (n > 0 && warp == 9) {
+    if (n > 0 && warp == 10) {
       // ---------------------------------------------- TMA producer
       // A lane per box (page rows x 64 dims).  Boxes without a visible key and
       // pages outside the pool are not loaded; their keys are masked below.
@@ -266,34 +322,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return page;
       };
-      Ring rg{0, p.nst, 0u};
-      bool ok = true, wrapped = false;
+      int at = 0;  // place of the next load in the ring's order
+      bool ok = true;
       auto load = [&](int t, int kv, int page) {
         if (!ok) return;
         bool got = true;
-        if (lane == 0 && wrapped)
-          got = ptx::mbar_wait(ptx::smem_u32(&empty[rg.slot]), rg.phase ^ 1u, abort_flag);
+        if (lane == 0 && at >= kSlots) {
+          // the iteration that used this slot's last tile: pair form K0 | V0 K1 |
+          // V1 K2 | ..., else K0 | K1 | V0 K2 | V1 K3 | ...
+          const int old = at - kSlots;
+          const int e = kPair ? (old + 1) / 2 : (old < 2 ? old : old / 2 + 1);
+          got = chunk_wait<false>(ptx::smem_u32(&done[e % kDone]),
+                           static_cast<uint32_t>((e / kDone) & 1), abort_flag);
+        }
         ok = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
         if (!ok) return;
         const bool skip = t == p.skip_tile && kv == 0;
-        const uint32_t bar = ptx::smem_u32(&full[rg.slot]);
+        const int slot = at % kSlots;
+        const uint32_t bar = ptx::smem_u32(&full[slot]);
         const uint32_t bytes =
             __popc(__ballot_sync(0xffffffffu, page >= 0)) * kChunks * p.box_rows * 128u;
         if (lane == 0 && !skip) ptx::mbar_arrive_expect_tx(bar, bytes);
         __syncwarp();
-        const int b = lane / kChunks, c = lane % kChunks;
-        const int pg = __shfl_sync(0xffffffffu, page, b);
+        // other lanes for each load: one thread's copies complete one after another
+        const int j = (lane - at * boxes * kChunks) & 31, b = j / kChunks, c = j % kChunks;
+        const int pg = __shfl_sync(0xffffffffu, page, b & 31);
         if (b < boxes && pg >= 0 && !skip) {
           const int key0 = (t0 + t) * kKT + b * p.box_rows;
           const int64_t row =
               (((static_cast<int64_t>(p.layer) * p.NP + pg) * 2 + kv) * p.nkv + kvh) * p.P +
               key0 % p.P;
-          ptx::tma_load_2d_hint(ptx::smem_u32(ring + rg.slot * kSlotBytes + c * kChunkBytes +
+          ptx::tma_load_2d_hint(ptx::smem_u32(ring + slot * kSlotBytes + c * kChunkBytes +
                                               b * p.box_rows * 128),
                                 &tm, c * 64, static_cast<int32_t>(row), bar, pol);
         }
-        rg.next();
-        if (rg.slot == 0) wrapped = true;
+        ++at;
       };
       // a tile's pages are looked up at least one load ahead of their use
       if constexpr (kPair) {
@@ -317,105 +380,107 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok && lane == 0) {  // wind down: the slots' last copies land before the CTA ends
-        for (int i = 0; i < p.nst; ++i) {
+        for (int i = max(at - kSlots, 0); i < at; ++i) {
           volatile int dummy = 0;
-          const bool later = i < rg.slot;  // filled in the current round of the ring
-          if (later || wrapped)
-            ptx::mbar_wait(ptx::smem_u32(&full[i]), later ? rg.phase : rg.phase ^ 1u, &dummy);
+          chunk_wait<false>(ptx::smem_u32(&full[i % kSlots]), static_cast<uint32_t>((i / kSlots) & 1),
+                     &dummy);
         }
       }
-    } else if (n > 0 && warp == 8 && lane == 0) {
+    } else if (n > 0 && warp == 11) {
       // ---------------------------------------------- MMA issuer
+      // One thread for both groups: their blocks of products go into the pipe in
+      // turn (mixed by two issuers, both groups wait for the pipe and then leave
+      // it idle together: 570 us where one issuer takes 434).
       constexpr uint32_t idesc_qk = ptx::idesc_bf16_f32(128, kKT, false);
       constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, HD, true);
-      const uint64_t dq = ptx::desc_kmajor_sw128(ptx::smem_u32(sm), 0);
-      const uint64_t dk = ptx::desc_kmajor_sw128(ptx::smem_u32(ring), 0);
-      const uint64_t dv = ptx::smem_desc(ptx::smem_u32(ring), kChunkBytes, 1024, ptx::kSwizzle128B);
-      auto wait = [&](uint64_t *bar, uint32_t phase) {
-        const bool got = ptx::mbar_wait(ptx::smem_u32(bar), phase, abort_flag);
+      // warp-uniform copies
+      const int tiles = __shfl_sync(0xffffffffu, n, 0);
+      const int groups = __shfl_sync(0xffffffffu, two ? 2 : 1, 0);
+      const uint32_t tm0 = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t qbase = __shfl_sync(0xffffffffu, ptx::smem_u32(sm), 0);
+      const uint32_t rbase = __shfl_sync(0xffffffffu, ptx::smem_u32(ring), 0);
+      const uint64_t dq = ptx::desc_kmajor_sw128(qbase, 0);
+      const uint64_t dk = ptx::desc_kmajor_sw128(rbase, 0);
+      const uint64_t dv = ptx::smem_desc(rbase, kChunkBytes, 1024, ptx::kSwizzle128B);
+      const uint32_t full0 = ptx::smem_u32(full);
+      // Waits on up to three barriers at the cost of one: each is polled by lanes
+      // of its own.  A slot in the ring's order, or a barrier and its phase.
+      struct At {
+        uint32_t bar, phase;
+      };
+      auto slot = [&](int at) {
+        return At{full0 + 8u * (at % kSlots), static_cast<uint32_t>((at / kSlots) & 1)};
+      };
+      auto wait = [&](At a, At b, At c) {
+        const At x = lane == 1 ? b : lane == 2 ? c : a;
+        const bool got = __all_sync(0xffffffffu, chunk_wait<true>(x.bar, x.phase, abort_flag));
         ptx::tc_fence_after();
         return got;
       };
-      auto qk = [&](int g, int slot) {  // S_g = Q K^T
+      auto qk = [&](int g, int at) {  // S_g = Q K^T
         const uint64_t a = dq + (((kPair ? g : 0) * kSlotBytes) >> 4);
-        const uint64_t b = dk + ((slot * kSlotBytes) >> 4);
+        const uint64_t b = dk + (((at % kSlots) * kSlotBytes) >> 4);
 #pragma unroll
         for (int ks = 0; ks < HD / 16; ++ks) {
           const uint32_t off = ((ks >> 2) * kChunkBytes + (ks & 3) * 32) >> 4;
-          ptx::mma_bf16(tmem + 128 * g, a + off, b + off, idesc_qk, ks > 0 ? 1u : 0u);
+          ptx::mma_bf16(tm0 + 128 * g, a + off, b + off, idesc_qk, ks > 0 ? 1u : 0u);
         }
         ptx::mma_commit(ptx::smem_u32(&s_full[g]));
       };
-      auto pv = [&](int g, int slot, bool first) {  // O_g (+)= P V
-        const uint64_t b = dv + ((slot * kSlotBytes) >> 4);
+      auto pv = [&](int g, int at, int k0, int k1, bool first) {  // O_g (+)= P V
+        const uint64_t b = dv + (((at % kSlots) * kSlotBytes) >> 4);
 #pragma unroll
-        for (int ks = 0; ks < kKT / 16; ++ks)
-          ptx::mma_bf16_ts(tmem + kColO + HD * g, tmem + 128 * g + ks * 8, b + ((ks * 2048) >> 4),
+        for (int ks = k0; ks < k1; ++ks)
+          ptx::mma_bf16_ts(tm0 + kColO + HD * g, tm0 + 128 * g + ks * 8, b + ((ks * 2048) >> 4),
                            idesc_pv, (!first || ks > 0) ? 1u : 0u);
       };
-      Ring rg{0, p.nst, 0u};
-      auto release = [&](int slot) { ptx::mma_commit(ptx::smem_u32(&empty[slot])); };
-      bool ok = wait(q_full, 0u) && wait(&full[rg.slot], rg.phase);
-      if (ok) {
-        qk(0, rg.slot);
-        if (two) qk(1, rg.slot);
-        release(rg.slot);
-        rg.next();
-      }
-      if (!kPair && ok && n > 1) {
-        ok = wait(&full[rg.slot], rg.phase);
-        if (ok) {
-          qk(1, rg.slot);
-          release(rg.slot);
-          rg.next();
+      // pair form: event 0 is the first scores, 1 + t tile t's values and tile
+      // t + 1's scores; else events 0 and 1 the first scores, 2 + t tile t's
+      // values and tile t + 2's scores
+      auto event = [&](int e) { ptx::mma_commit(ptx::smem_u32(&done[e % kDone])); };
+      const At qf{ptx::smem_u32(q_full), 0u};
+      bool ok = wait(qf, slot(0), slot(!kPair && tiles > 1 ? 1 : 0));
+      if (ok && elect_one()) {
+        qk(0, 0);
+        if (kPair) {
+          if (groups > 1) qk(1, 0);
+          event(0);
+        } else {
+          event(0);
+          if (tiles > 1) {
+            qk(1, 1);
+            event(1);
+          }
         }
       }
-      for (int t = 0; ok && t < n; ++t) {
-        const int vs = rg.slot;
-        ok = wait(&full[vs], rg.phase);
-        if (!ok) break;
-        rg.next();
-        const int ks = rg.slot;
-        const uint32_t kphase = rg.phase;
-        if constexpr (kPair) {
-          const bool more = t + 1 < n;
-          for (int g = 0; ok && g < (two ? 2 : 1); ++g) {
-            ok = wait(&p_full[g], static_cast<uint32_t>(t & 1));
-            if (!ok) break;
-            pv(g, vs, t == 0);
+      __syncwarp();
+      constexpr int kStep = kPair ? 1 : 2;
+      for (int t = 0; ok && t < tiles; ++t) {
+        const int av = kPair ? 2 * t + 1 : min(t + 2, tiles) + t;  // V's place in the ring's order
+        const bool more = t + kStep < tiles;
+        for (int i = 0; ok && i < (kPair ? groups : 1); ++i) {
+          const int g = kPair ? i : t & 1;
+          const uint32_t ph = static_cast<uint32_t>((kPair ? t : t >> 1) & 1);
+          const At k = slot(more ? av + 1 : av);
+          ok = wait(At{ptx::smem_u32(&p_full[g]), ph}, slot(av), k);
+          if (!ok) break;
+          if (elect_one()) {
+            pv(g, av, 0, 8, t < kStep);
             if (more) {
-              if (g == 0) ok = wait(&full[ks], kphase);
-              if (ok) qk(g, ks);
+              qk(g, av + 1);
+              if (!kPair || i + 1 == groups) event(t + kStep);
             } else {
               ptx::mma_commit(ptx::smem_u32(&o_done[g]));
             }
           }
-          if (!ok) break;
-          release(vs);
-          if (more) {
-            release(ks);
-            rg.next();
-          }
-        } else {
-          const int g = t & 1;
-          ok = wait(&p_full[g], static_cast<uint32_t>((t >> 1) & 1));
-          if (!ok) break;
-          pv(g, vs, t < 2);
-          release(vs);
-          if (t + 2 < n) {
-            ok = wait(&full[ks], kphase);
-            if (!ok) break;
-            qk(g, ks);
-            release(ks);
-            rg.next();
-          }
-          if (t + 1 == n) ptx::mma_commit(ptx::smem_u32(&o_done[0]));
+          __syncwarp();
         }
       }
       if (!ok) {
-        ptx::mma_commit(ptx::smem_u32(drain));
+        if (elect_one()) ptx::mma_commit(ptx::smem_u32(drain));
+        __syncwarp();
         volatile int dummy = 0;
-        ptx::mbar_wait(ptx::smem_u32(drain), 0u, &dummy);
+        chunk_wait<false>(ptx::smem_u32(drain), 0u, &dummy);
       }
     }
   } else {
@@ -468,11 +533,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (bad_pages && threadIdx.x == 0) raise_status(p.st, DFLASH_DEV_BAD_PAGE);
       }
 
+      const bool active = (kPair ? 128 * g : 0) + (warp & 3) * 32 < nrow;  // the warp holds rows
       float m_ref = -INFINITY, l = 0.f;
       bool ok = true;
       int u = 0;
       for (int t = kPair ? 0 : g; t < n && (!kPair || g == 0 || two); t += kPair ? 1 : 2, ++u) {
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(ptx::smem_u32(&s_full[g]),
+        ok = __all_sync(0xffffffffu, chunk_wait<false>(ptx::smem_u32(&s_full[g]),
                                                     static_cast<uint32_t>(u & 1), abort_flag));
         if (!ok) break;
         ptx::tc_fence_after();
@@ -496,10 +562,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // V rows no row of this tile sees: zero, before P is handed over
           const int at = kPair ? 2 * t + 1 : min(t + 2, n) + t;  // V's place in the ring's order
-          const int slot = at % p.nst;
+          const int slot = at % kSlots;
           ok = __all_sync(0xffffffffu,
-                          ptx::mbar_wait(ptx::smem_u32(&full[slot]),
-                                         static_cast<uint32_t>((at / p.nst) & 1), abort_flag));
+                          chunk_wait<false>(ptx::smem_u32(&full[slot]),
+                                         static_cast<uint32_t>((at / kSlots) & 1), abort_flag));
           if (!ok) break;
           const int key = kb + tid, w4 = warp & 3;
           const uint32_t mine = w4 == 0 ? okm[0] : w4 == 1 ? okm[1] : w4 == 2 ? okm[2] : okm[3];
@@ -513,6 +579,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           ptx::fence_proxy_async_smem();
+        }
+        if (!active) {  // its rows of P may hold anything: they reach no other row
+          ptx::tc_fence_before();
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&p_full[g]));
+          continue;
         }
         if (!(lo <= kb && hi >= kb + kKT - 1)) {
 #pragma unroll
@@ -550,33 +621,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float nm = m_ref == -INFINITY ? 0.f : -m_ref;  // nothing seen yet: weights 2^-inf
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(nm, nm);
+        float2 sum[2] = {};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t pk[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float a = ptx::ex2(fmaf(sv[64 * c + 2 * e], p.scale_log2, nm));
-            const float b = ptx::ex2(fmaf(sv[64 * c + 2 * e + 1], p.scale_log2, nm));
-            sum[(2 * e) & 3] += a;
-            sum[(2 * e + 1) & 3] += b;
-            pk[e] = ptx::pack_bf16x2(a, b);
+            float2 w = fma2(make_float2(sv[64 * c + 2 * e], sv[64 * c + 2 * e + 1]), sc2, nm2);
+            w.x = ptx::ex2(w.x);
+            w.y = ptx::ex2(w.y);
+            sum[e & 1] = add2(sum[e & 1], w);
+            pk[e] = ptx::pack_bf16x2(w.x, w.y);
           }
           tmem_st32(tm_s + 32 * c, pk);
         }
-        l = l * corr + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        sum[0] = add2(sum[0], sum[1]);
+        l = l * corr + (sum[0].x + sum[0].y);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&p_full[g]));
       }
       // ---------------------------------------------- epilogue
-      const bool mine = kPair ? u > 0 : n > 0;  // a product to wait for
-      if (mine && ok) {
-        ok = __all_sync(0xffffffffu,
-                        ptx::mbar_wait(ptx::smem_u32(&o_done[kPair ? g : 0]), 0u, abort_flag));
+      if (u > 0 && ok) {
+        ok = __all_sync(0xffffffffu, chunk_wait<false>(ptx::smem_u32(&o_done[g]), 0u, abort_flag));
         ptx::tc_fence_after();
       }
+      if (!kPair && ok && n > 1 - g)  // the other group's products: the ring is idle after them
+        ok = __all_sync(0xffffffffu, chunk_wait<false>(ptx::smem_u32(&o_done[g ^ 1]), 0u, abort_flag));
       // the row's state over both groups, and this thread's share of its dims
       constexpr int kDims = kPair ? HD : HD / 2;
       const int d0 = kPair ? 0 : g * kDims;
@@ -750,20 +823,14 @@ size_t chunk_attention_workspace_bytes(const dflash_geom &g, int B, int n_rows, 
 namespace {
 
 template <int HD, bool kPair>
-cudaError_t launch_main(const CUtensorMap &tm, ChunkParams p, dim3 grid, cudaStream_t s) {
-  constexpr uint32_t slot = HD / 64 * kChunkBytes, q_bytes = (kPair ? 2 : 1) * slot;
-  constexpr uint32_t bars = (2 * kMaxSlots + 8) * 8 + 16;
-  // the epilogue's exchange (128 rows x HD floats, 4 KB of states... in the ring)
-  p.nst = std::min<int>(kMaxSlots, (kSmemMax - 1024 - bars - q_bytes) / slot);
-  p.ring_off = q_bytes;
-  p.bar_off = q_bytes + p.nst * slot;
+cudaError_t launch_main(const CUtensorMap &tm, const ChunkParams &p, dim3 grid, cudaStream_t s) {
   const cudaError_t e = ensure_smem_limit<chunk_attn_kernel<HD, kPair>>(kSmemMax);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = 1024 + p.bar_off + bars;
+  cfg.dynamicSmemBytes = Layout<HD, kPair>::kBytes;
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -816,7 +883,7 @@ cudaError_t launch_chunk_attention(const dflash_geom &g, int B, int layer, int n
                              static_cast<uint64_t>(g.page_size);
   cudaError_t e = make_tmap_bf16_2d(&tm, pool, pool_rows, g.head_dim, g.head_dim, p.box_rows, 64);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(chunk_tiles(g, B, n_rows)), g.nkv, S);
+  const dim3 grid(static_cast<unsigned>(chunk_tiles(g, B, n_rows) * g.nkv), 1, S);
   const bool pair = pair_form(g, B, n_rows);
   if (g.head_dim == 64)
     e = pair ? launch_main<64, true>(tm, p, grid, s) : launch_main<64, false>(tm, p, grid, s);
