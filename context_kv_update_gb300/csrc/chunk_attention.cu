@@ -727,16 +727,58 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the S partial states of a row: one warp per (row, head), HD / 32 dims a
-// lane.  Rows of no request are passed over, as the main kernel passes them.
+// lane.  All of a batch's loads are issued before any is used (one memory round
+// trip for up to 20 segments).  Rows of no request are passed over, as the main
+// kernel passes them; O of a segment without keys is not written, so what is read
+// there is selected away.
 template <int HD>
 __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkParams p) {
-  constexpr int E = HD / 32;
+  constexpr int E = HD / 32, kBatch = 20;
   ptx::griddep_launch();
   ptx::griddep_wait();
   const int lane = threadIdx.x & 31;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int t = static_cast<int>(w / p.hq), h = static_cast<int>(w % p.hq);
   if (t >= p.n_rows) return;
+  const float *o = p.ws_o + w * p.S * HD + lane * E;
+  float m = p.sinks ? p.sinks[h] * kLog2e : -INFINITY, l = p.sinks ? 1.f : 0.f;
+  float acc[E] = {};
+  for (int s0 = 0; s0 < p.S; s0 += kBatch) {
+    const bool in = lane < kBatch && s0 + lane < p.S;
+    const float mj = in ? __ldcg(p.ws_m + w * p.S + s0 + lane) : -INFINITY;
+    const float lj = in ? __ldcg(p.ws_l + w * p.S + s0 + lane) : 0.f;
+    float ov[kBatch][E];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const float *from = o + static_cast<int64_t>(min(s0 + j, p.S - 1)) * HD;
+      if constexpr (E == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(from));
+        ov[j][0] = v.x;
+        ov[j][1] = v.y;
+        ov[j][2] = v.z;
+        ov[j][3] = v.w;
+      } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2 *>(from));
+        ov[j][0] = v.x;
+        ov[j][1] = v.y;
+      }
+    }
+    const float mn = fmaxf(m, warp_max(mj));
+    if (mn == -INFINITY) continue;
+    const float sc = m == -INFINITY ? 0.f : ptx::ex2(m - mn);
+    const float wj = mj == -INFINITY ? 0.f : ptx::ex2(mj - mn);
+    l = l * sc + warp_sum(wj * lj);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= sc;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const float ws = __shfl_sync(0xffffffffu, wj, j);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += ws != 0.f ? ws * ov[j][e] : 0.f;
+    }
+    m = mn;
+  }
+  // the row's request
   int lo = 0, n = p.B;  // the last request whose first row is <= t
   while (n > 1) {
     const int step = (n + 31) / 32;
@@ -747,31 +789,15 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkParams p) {
   }
   Request rq;
   if (!load_request(p, lo, false, &rq) || t < rq.a || t >= rq.b) return;
-  const float *o = p.ws_o + w * p.S * HD + lane * E;
-  float m = p.sinks ? p.sinks[h] * kLog2e : -INFINITY, l = p.sinks ? 1.f : 0.f;
-  float acc[E] = {};
-  for (int s0 = 0; s0 < p.S; s0 += 32) {
-    const bool in = s0 + lane < p.S;
-    const float mj = in ? p.ws_m[w * p.S + s0 + lane] : -INFINITY;
-    const float lj = in ? p.ws_l[w * p.S + s0 + lane] : 0.f;
-    const float mn = fmaxf(m, warp_max(mj));
-    if (mn == -INFINITY) continue;
-    const float sc = m == -INFINITY ? 0.f : ptx::ex2(m - mn);
-    const float wj = mj == -INFINITY ? 0.f : ptx::ex2(mj - mn);
-    l = l * sc + warp_sum(wj * lj);
+  float f[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= sc;
-    for (int j = 0; j < min(32, p.S - s0); ++j) {
-      const float ws = __shfl_sync(0xffffffffu, wj, j);
-      if (ws == 0.f) continue;  // also a segment without keys, whose O is not written
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += ws * o[static_cast<int64_t>(s0 + j) * HD + e];
-    }
-    m = mn;
-  }
+  for (int e = 0; e < E; ++e) f[e] = l > 0.f ? acc[e] / l : 0.f;
   uint16_t *dst = p.out + t * p.os + static_cast<int64_t>(h) * HD + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; ++e) dst[e] = f32_to_bf16_rn(l > 0.f ? acc[e] / l : 0.f);
+  const uint32_t a = ptx::pack_bf16x2(f[0], f[1]);
+  if constexpr (E == 4)
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(a, ptx::pack_bf16x2(f[2], f[3]));
+  else
+    *reinterpret_cast<uint32_t *>(dst) = a;
 }
 
 // Pair form where the mean request fills more than one 128-row tile.
@@ -786,10 +812,12 @@ int64_t chunk_tiles(const dflash_geom &g, int B, int n_rows) {
 
 }  // namespace
 
+// Segments: as many as fill the GPU's SMs once, but each of 4 tiles at least of the
+// longest cache the table holds, since a second launch joins them.
 int chunk_attention_num_segments(const dflash_geom &g, int B, int n_rows) {
   const int64_t ctas = chunk_tiles(g, B, n_rows) * g.nkv;
   int64_t S = device_sm_count() / ctas;
-  const int64_t most = (static_cast<int64_t>(g.max_pages) * g.page_size + kKT - 1) / kKT;
+  const int64_t most = (static_cast<int64_t>(g.max_pages) * g.page_size + kKT - 1) / kKT / 4;
   S = S > most ? most : S;
   return static_cast<int>(S < 1 ? 1 : S);
 }
