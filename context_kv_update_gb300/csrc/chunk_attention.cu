@@ -61,8 +61,9 @@ constexpr uint32_t kColO = 256;  // S of group g at 128 g, O at 256 + HD g
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct ChunkParams {
-  int B, n_rows, hq, nkv, G, layer, NP, P, M, window, mask_mode, S;
+  int B, n_rows, hq, nkv, G, wide_out, layer, NP, P, M, window, mask_mode, S;
   int box_rows, skip_tile;
+  uint32_t g_inv;  // ceil(2^32 / G), for G > 1
   float scale_log2;
   const uint16_t *q;
   int64_t qs, os;
@@ -108,6 +109,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
       "r"(r[30]), "r"(r[31])
       : "memory");
+}
+// 32 bytes in one store, 32-byte aligned.
+__device__ __forceinline__ void store_32b(void *p, const uint32_t *w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 template <int N>
 __device__ __forceinline__ void regs_more() {
@@ -474,21 +481,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t tm_s = tmem + 128 * g + lane_off, tm_o = tmem + kColO + HD * g + lane_off;
 
+      // pages of the segment outside the pool: none, as a rule.  The first look-ups
+      // go out before Q's loads.
+      const int32_t *pages = p.tbl + static_cast<int64_t>(r) * p.M;
+      const int last_page = min(hi_max, (t0 + n) * kKT - 1) / p.P;
+      const int first_page = max(lo_min, t0 * kKT) / p.P + static_cast<int>(threadIdx.x);
+      const int page0 = n > 0 && first_page <= last_page ? pages[first_page] : 0;
+
       if (n > 0) {
-        // Q rows -> shared memory, K-major, 128-byte swizzle (rows past the end: 0)
-        constexpr int kUnits = HD / 8;  // 16-byte units of a row
-        constexpr int kQRows = kPair ? 256 : 128;
-#pragma unroll 4
-        for (int i = threadIdx.x; i < kQRows * kUnits; i += 256) {
-          const int row = i / kUnits, u = i % kUnits;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (row < nrow) {
-            const int R = row0 + row, tok = R / p.G;
-            v = reinterpret_cast<const uint4 *>(
-                p.q + (rq.a + tok) * p.qs + static_cast<int64_t>(kvh * p.G + R - tok * p.G) * HD)[u];
-          }
+        // Q rows -> shared memory, K-major, 128-byte swizzle (rows past the end: 0).
+        // Every load of a thread is issued before any is stored: in batches of four
+        // they took 5.7 us of a CTA.
+        constexpr int kUnits = HD / 8, kAtOnce = 256 / kUnits;  // 16-byte units of a row
+        constexpr int kEach = (kPair ? 256 : 128) / kAtOnce;
+        const int u = threadIdx.x % kUnits, tok0 = row0 / p.G, rem0 = row0 - tok0 * p.G;
+        uint4 v[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+          const int row = threadIdx.x / kUnits + k * kAtOnce, x = rem0 + row;
+          // x / G by the reciprocal, exact for x G < 2^32
+          const int tok = p.G == 1 ? x : static_cast<int>(__umulhi(x, p.g_inv));
+          v[k] = make_uint4(0, 0, 0, 0);
+          if (row < nrow)
+            v[k] = reinterpret_cast<const uint4 *>(
+                p.q + (rq.a + tok0 + tok) * p.qs +
+                static_cast<int64_t>(kvh * p.G + x - tok * p.G) * HD)[u];
+        }
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+          const int row = threadIdx.x / kUnits + k * kAtOnce;
           *reinterpret_cast<uint4 *>(sm + ((row >> 7) * kChunks + (u >> 3)) * kChunkBytes +
-                                     (row & 127) * 128 + (((u & 7) ^ (row & 7)) << 4)) = v;
+                                     (row & 127) * 128 + (((u & 7) ^ (row & 7)) << 4)) = v[k];
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
@@ -503,14 +526,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int lo = 0, hi = -1;
       if (real) key_range(p, rq.c + tok, rq.kv, &lo, &hi);
 
-      // pages of the segment outside the pool: none, as a rule
-      bool bad_pages = false;
+      bool bad_pages = page0 < 0 || page0 >= p.NP;
       if (n > 0) {
-        const int ka = max(lo_min, t0 * kKT), kb = min(hi_max, (t0 + n) * kKT - 1);
-        for (int lp = ka / p.P + static_cast<int>(threadIdx.x); lp <= kb / p.P; lp += 256) {
-          const int page = p.tbl[static_cast<int64_t>(r) * p.M + lp];
-          bad_pages |= page < 0 || page >= p.NP;
-        }
+        for (int lp = first_page + 256; lp <= last_page; lp += 256)
+          bad_pages |= pages[lp] < 0 || pages[lp] >= p.NP;
         bad_pages = ptx::bar_or(1, 256, bad_pages);
         if (bad_pages && threadIdx.x == 0) raise_status(p.st, DFLASH_DEV_BAD_PAGE);
       }
@@ -643,13 +662,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         float *smx = sx + HD * 128;
         smx[g * 128 + tid] = m;
         smx[256 + g * 128 + tid] = l;
-        if (u > 0 && ok) {
-          for (int c = 0; c < kDims; c += 16) {
-            uint32_t ov[16];
-            ptx::tmem_ld16_sync(tm_o + (g ^ 1) * kDims + c, ov);
+        if (u > 0 && ok && active) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              sx[(g * kDims + c + e) * 128 + tid] = __uint_as_float(ov[e]);
+          for (int c = 0; c < kDims; c += 32) {
+            float ov[32];
+            ptx::tmem_ld32f_sync(tm_o + (g ^ 1) * kDims + c, ov);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) sx[(g * kDims + c + e) * 128 + tid] = ov[e];
           }
         }
         const bool bad = ptx::bar_or(1, 256, !ok);
@@ -680,37 +699,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       other *= gain;
       const bool has = u > 0 && ok;  // this group's accumulator was written
 #pragma unroll
-      for (int c = 0; c < kDims; c += 16) {
-        float o[16];
+      for (int c = 0; c < kDims && active; c += 32) {
+        float o[32];
         if (has) {  // warp-uniform: tensor memory loads take the whole warp
-          uint32_t ov[16];
-          ptx::tmem_ld16_sync(tm_o + d0 + c, ov);
+          ptx::tmem_ld32f_sync(tm_o + d0 + c, o);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = own != 0.f ? __uint_as_float(ov[e]) * own : 0.f;
+          for (int e = 0; e < 32; ++e) o[e] = own != 0.f ? o[e] * own : 0.f;
         } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = 0.f;
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
         if constexpr (!kPair) {
           if (other != 0.f) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] += xo[(c + e) * 128] * other;
+            for (int e = 0; e < 32; ++e) o[e] += xo[(c + e) * 128] * other;
           }
         }
         if (!real) continue;
         if (p.S == 1) {
-          uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * p.os +
-                                                 static_cast<int64_t>(h) * HD + d0 + c);
-          uint32_t w[8];
+          uint16_t *dst = p.out + orow * p.os + static_cast<int64_t>(h) * HD + d0 + c;
+          uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = ptx::pack_bf16x2(o[2 * e], o[2 * e + 1]);
-          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          for (int e = 0; e < 16; ++e) w[e] = ptx::pack_bf16x2(o[2 * e], o[2 * e + 1]);
+          if (p.wide_out) {  // whole sectors: half the write requests
+            store_32b(dst, w);
+            store_32b(dst + 16, w + 8);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              reinterpret_cast<uint4 *>(dst)[e] =
+                  make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+          }
         } else if (any) {
           float4 *dst = reinterpret_cast<float4 *>(
               p.ws_o + ((orow * p.hq + h) * p.S + seg) * HD + d0 + c);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
+          for (int e = 0; e < 8; ++e)
             dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       }
@@ -863,6 +887,8 @@ cudaError_t launch_chunk_attention(const dflash_geom &g, int B, int layer, int n
   p.hq = g.hq;
   p.nkv = g.nkv;
   p.G = g.hq / g.nkv;
+  p.g_inv = p.G > 1 ? 0xffffffffu / p.G + 1u : 0u;
+  p.wide_out = ((reinterpret_cast<uintptr_t>(out) | (2 * out_stride)) & 31u) == 0;
   p.layer = layer;
   p.NP = g.num_pool_pages;
   p.P = g.page_size;
