@@ -17,9 +17,10 @@
 // loads.  Each group has its own scores S (128 columns of tensor
 // memory; its weights P overwrite them) and accumulator O, so one group's softmax
 // runs under the other's two products:
-//   pair form (kPair): the groups hold two row tiles over the same key tiles;
-//   otherwise one row tile, the groups take the even and the odd key tiles and
-//   their halves are joined at the end (few rows: the key stream is the work).
+//   more than 128 rows: the groups hold two row tiles over the same key tiles;
+//   otherwise the groups take the even and the odd key tiles of the one row tile
+//   and their halves are joined at the end (few rows: the key stream is the work).
+// kPair: work tiles of 256 rows; otherwise of 128, with more room for keys.
 // K and V tiles come through one ring of 128-key slots in the order they are
 // used; products of one issuing thread execute in order, so the next scores may
 // be issued over the weights that the product before them reads.
@@ -289,7 +290,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
-  const bool two = kPair && nrow > 128;  // both groups hold rows
+  // one row tile: the groups take its even and its odd key tiles
+  const bool split = !kPair || nrow <= 128;
 
   if (warp >= 8) {
     regs_less<kIssueRegs>();
@@ -317,10 +319,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) return;
         bool got = true;
         if (lane == 0 && at >= kSlots) {
-          // the iteration that used this slot's last tile: pair form K0 | V0 K1 |
-          // V1 K2 | ..., else K0 | K1 | V0 K2 | V1 K3 | ...
+          // the iteration that used this slot's last tile: two row tiles K0 | V0 K1 |
+          // V1 K2 | ..., one K0 | K1 | V0 K2 | V1 K3 | ...
           const int old = at - kSlots;
-          const int e = kPair ? (old + 1) / 2 : (old < 2 ? old : old / 2 + 1);
+          const int e = !split ? (old + 1) / 2 : (old < 2 ? old : old / 2 + 1);
           got = chunk_wait<false>(ptx::smem_u32(&done[e % kDone]),
                            static_cast<uint32_t>((e / kDone) & 1), abort_flag);
         }
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++at;
       };
       // a tile's pages are looked up at least one load ahead of their use
-      if constexpr (kPair) {
+      if (!split) {
         int cur = fetch(0);
         for (int t = 0; t < n; ++t) {
           const int nxt = fetch(t + 1);
@@ -384,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, HD, true);
       // warp-uniform copies
       const int tiles = __shfl_sync(0xffffffffu, n, 0);
-      const int groups = __shfl_sync(0xffffffffu, two ? 2 : 1, 0);
+      const bool pairs = kPair && __shfl_sync(0xffffffffu, split ? 0 : 1, 0) != 0;
       const uint32_t tm0 = __shfl_sync(0xffffffffu, tmem, 0);
       const uint32_t qbase = __shfl_sync(0xffffffffu, ptx::smem_u32(sm), 0);
       const uint32_t rbase = __shfl_sync(0xffffffffu, ptx::smem_u32(ring), 0);
@@ -407,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return got;
       };
       auto qk = [&](int g, int at) {  // S_g = Q K^T
-        const uint64_t a = dq + (((kPair ? g : 0) * kSlotBytes) >> 4);
+        const uint64_t a = dq + (((pairs ? g : 0) * kSlotBytes) >> 4);
         const uint64_t b = dk + (((at % kSlots) * kSlotBytes) >> 4);
 #pragma unroll
         for (int ks = 0; ks < HD / 16; ++ks) {
@@ -416,23 +418,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::mma_commit(ptx::smem_u32(&s_full[g]));
       };
-      auto pv = [&](int g, int at, int k0, int k1, bool first) {  // O_g (+)= P V
+      auto pv = [&](int g, int at, bool first) {  // O_g (+)= P V
         const uint64_t b = dv + (((at % kSlots) * kSlotBytes) >> 4);
 #pragma unroll
-        for (int ks = k0; ks < k1; ++ks)
+        for (int ks = 0; ks < kKT / 16; ++ks)
           ptx::mma_bf16_ts(tm0 + kColO + HD * g, tm0 + 128 * g + ks * 8, b + ((ks * 2048) >> 4),
                            idesc_pv, (!first || ks > 0) ? 1u : 0u);
       };
-      // pair form: event 0 is the first scores, 1 + t tile t's values and tile
-      // t + 1's scores; else events 0 and 1 the first scores, 2 + t tile t's
+      // two row tiles: event 0 is the first scores, 1 + t tile t's values and tile
+      // t + 1's scores; one: events 0 and 1 the first scores, 2 + t tile t's
       // values and tile t + 2's scores
       auto event = [&](int e) { ptx::mma_commit(ptx::smem_u32(&done[e % kDone])); };
       const At qf{ptx::smem_u32(q_full), 0u};
-      bool ok = wait(qf, slot(0), slot(!kPair && tiles > 1 ? 1 : 0));
+      bool ok = wait(qf, slot(0), slot(!pairs && tiles > 1 ? 1 : 0));
       if (ok && elect_one()) {
         qk(0, 0);
-        if (kPair) {
-          if (groups > 1) qk(1, 0);
+        if (pairs) {
+          qk(1, 0);
           event(0);
         } else {
           event(0);
@@ -443,21 +445,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      constexpr int kStep = kPair ? 1 : 2;
+      const int step = pairs ? 1 : 2;
       for (int t = 0; ok && t < tiles; ++t) {
-        const int av = kPair ? 2 * t + 1 : min(t + 2, tiles) + t;  // V's place in the ring's order
-        const bool more = t + kStep < tiles;
-        for (int i = 0; ok && i < (kPair ? groups : 1); ++i) {
-          const int g = kPair ? i : t & 1;
-          const uint32_t ph = static_cast<uint32_t>((kPair ? t : t >> 1) & 1);
+        const int av = pairs ? 2 * t + 1 : min(t + 2, tiles) + t;  // V's place in the ring's order
+        const bool more = t + step < tiles;
+        for (int i = 0; ok && i < (pairs ? 2 : 1); ++i) {
+          const int g = pairs ? i : t & 1;
+          const uint32_t ph = static_cast<uint32_t>((pairs ? t : t >> 1) & 1);
           const At k = slot(more ? av + 1 : av);
           ok = wait(At{ptx::smem_u32(&p_full[g]), ph}, slot(av), k);
           if (!ok) break;
           if (elect_one()) {
-            pv(g, av, 0, 8, t < kStep);
+            pv(g, av, t < step);
             if (more) {
               qk(g, av + 1);
-              if (!kPair || i + 1 == groups) event(t + kStep);
+              if (!pairs || i == 1) event(t + step);
             } else {
               ptx::mma_commit(ptx::smem_u32(&o_done[g]));
             }
@@ -519,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       // this thread's row and the keys it sees
-      const int rt = (kPair ? 128 * g : 0) + tid;
+      const int rt = (split ? 0 : 128 * g) + tid;
       const bool real = rt < nrow;
       const int tok = (row0 + (real ? rt : 0)) / p.G;
       const int h = kvh * p.G + (row0 + (real ? rt : 0)) - tok * p.G;
@@ -534,11 +536,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (bad_pages && threadIdx.x == 0) raise_status(p.st, DFLASH_DEV_BAD_PAGE);
       }
 
-      const bool active = (kPair ? 128 * g : 0) + (warp & 3) * 32 < nrow;  // the warp holds rows
+      const bool active = (split ? 0 : 128 * g) + (warp & 3) * 32 < nrow;  // the warp holds rows
       float m_ref = -INFINITY, l = 0.f;
       bool ok = true;
       int u = 0;
-      for (int t = kPair ? 0 : g; t < n && (!kPair || g == 0 || two); t += kPair ? 1 : 2, ++u) {
+      for (int t = split ? g : 0; t < n; t += split ? 2 : 1, ++u) {
         ok = __all_sync(0xffffffffu, chunk_wait<false>(ptx::smem_u32(&s_full[g]),
                                                     static_cast<uint32_t>(u & 1), abort_flag));
         if (!ok) break;
@@ -562,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!((okm[c >> 5] >> (c & 31)) & 1u)) sv[c] = -INFINITY;
           }
           // V rows no row of this tile sees: zero, before P is handed over
-          const int at = kPair ? 2 * t + 1 : min(t + 2, n) + t;  // V's place in the ring's order
+          const int at = split ? min(t + 2, n) + t : 2 * t + 1;  // V's place in the ring's order
           const int slot = at % kSlots;
           ok = __all_sync(0xffffffffu,
                           chunk_wait<false>(ptx::smem_u32(&full[slot]),
@@ -649,14 +651,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, chunk_wait<false>(ptx::smem_u32(&o_done[g]), 0u, abort_flag));
         ptx::tc_fence_after();
       }
-      if (!kPair && ok && n > 1 - g)  // the other group's products: the ring is idle after them
+      if (split && ok && n > 1 - g)  // the other group's products: the ring is idle after them
         ok = __all_sync(0xffffffffu, chunk_wait<false>(ptx::smem_u32(&o_done[g ^ 1]), 0u, abort_flag));
       // the row's state over both groups, and this thread's share of its dims
-      constexpr int kDims = kPair ? HD : HD / 2;
-      const int d0 = kPair ? 0 : g * kDims;
+      const int dims = split ? HD / 2 : HD, d0 = split ? g * (HD / 2) : 0;
       float m = ok ? m_ref : -INFINITY, own = 1.f, other = 0.f;
       const float *xo = nullptr;
-      if constexpr (!kPair) {
+      if (split) {
         // the other group's half of the dims goes through the idle ring
         float *sx = reinterpret_cast<float *>(ring);  // [2][HD / 2][128], then m and l [2][128]
         float *smx = sx + HD * 128;
@@ -664,11 +665,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         smx[256 + g * 128 + tid] = l;
         if (u > 0 && ok && active) {
 #pragma unroll
-          for (int c = 0; c < kDims; c += 32) {
+          for (int c = 0; c < HD / 2; c += 32) {
             float ov[32];
-            ptx::tmem_ld32f_sync(tm_o + (g ^ 1) * kDims + c, ov);
+            ptx::tmem_ld32f_sync(tm_o + (g ^ 1) * (HD / 2) + c, ov);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) sx[(g * kDims + c + e) * 128 + tid] = ov[e];
+            for (int e = 0; e < 32; ++e) sx[(g * (HD / 2) + c + e) * 128 + tid] = ov[e];
           }
         }
         const bool bad = ptx::bar_or(1, 256, !ok);
@@ -677,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         own = bad || m_ref == -INFINITY ? 0.f : ptx::ex2(m_ref - m);
         other = bad || m2 == -INFINITY ? 0.f : ptx::ex2(m2 - m);
         l = l * own + l2 * other;
-        xo = sx + (g ^ 1) * kDims * 128 + tid;
+        xo = sx + (g ^ 1) * (HD / 2) * 128 + tid;
       }
       const bool any = real && m != -INFINITY;  // the row saw a key
       const int64_t orow = static_cast<int64_t>(rq.a) + tok;
@@ -690,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           den = l * ptx::ex2(m - top) + ptx::ex2(sk - top);
         }
         gain = any ? ptx::ex2(m - top) / den : 0.f;
-      } else if (real && (kPair || g == 0)) {
+      } else if (real && (!split || g == 0)) {
         const int64_t w = (orow * p.hq + h) * p.S + seg;
         p.ws_m[w] = m;
         p.ws_l[w] = any ? l : 0.f;
@@ -699,7 +700,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       other *= gain;
       const bool has = u > 0 && ok;  // this group's accumulator was written
 #pragma unroll
-      for (int c = 0; c < kDims && active; c += 32) {
+      for (int c = 0; c < HD; c += 32) {
+        if (c >= dims || !active) break;
         float o[32];
         if (has) {  // warp-uniform: tensor memory loads take the whole warp
           ptx::tmem_ld32f_sync(tm_o + d0 + c, o);
@@ -709,11 +711,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
-        if constexpr (!kPair) {
-          if (other != 0.f) {
+        if (other != 0.f) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] += xo[(c + e) * 128] * other;
-          }
+          for (int e = 0; e < 32; ++e) o[e] += xo[(c + e) * 128] * other;
         }
         if (!real) continue;
         if (p.S == 1) {
