@@ -1,11 +1,11 @@
 """ctypes binding of ``libdflash.so`` (include/dflash.h).
 
-Argument marshalling only: every function here validates nothing beyond what
-ctypes needs, converts torch tensors to device pointers and the current torch
-stream to a ``cudaStream_t``, calls the C entry point of the same name and
-raises ``DflashError`` on a non-zero status.  All arithmetic runs in the CUDA
-kernels of the library; there is no CPU or PyTorch fallback.  Loading fails
-loudly when the library is missing.
+Argument marshalling only (that of the ragged-chunk calls is in csrc/calls.c):
+every function here validates nothing beyond what ctypes needs, converts torch
+tensors to device pointers and the current torch stream to a ``cudaStream_t``,
+calls the C entry point of the same name and raises ``DflashError`` on a non-zero
+status.  All arithmetic runs in the CUDA kernels of the library; there is no CPU
+or PyTorch fallback.  Loading fails loudly when the library is missing.
 """
 from __future__ import annotations
 
@@ -110,12 +110,13 @@ class RopeSpec(ctypes.Structure):
                 ("beta_slow", ctypes.c_double), ("magnitude", ctypes.c_double)]
 
 _lib = None
+_calls = None  # the module that marshals the ragged-chunk calls (csrc/calls.c)
 _raw_stream = _current_device = None  # of torch, set with the library
 
 
 def load():
     """Load libdflash.so (raises when it has not been built)."""
-    global _lib, _raw_stream, _current_device
+    global _lib, _calls, _raw_stream, _current_device
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -195,6 +196,11 @@ def load():
     import torch
     _raw_stream = torch._C._cuda_getCurrentRawStream
     _current_device = torch._C._cuda_getDevice
+    from . import _calls as calls
+    calls.bind(*[ctypes.cast(f, vp).value for f in (
+        lib.dflash_chunk_plan, lib.dflash_chunk_rope_store, lib.dflash_chunk_attention)],
+        _current_device, _raw_stream)
+    _calls = calls
     _lib = lib
     return lib
 
@@ -224,20 +230,6 @@ def _stream(stream):
         # (3.3 us a call against 0.3)
         return _raw_stream(_current_device())
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _rows(t):
-    """Address of a row-strided view and the elements between two rows: any step
-    between rows, the rest of a row contiguous."""
-    if t is None:
-        return None, 0
-    st = t.stride()
-    assert st[-1] == 1 and (len(st) < 3 or st[1] == t.shape[2])
-    return t.data_ptr(), st[0]
 
 
 def _check(fn, code):
@@ -462,18 +454,10 @@ def dflash_chunk_plan(geom, n_new, ctx_len, n_pages, block_table, free_pages, fr
     are written), free_pages int32, free_range int32 [2] CUDA tensors, valid
     uint8 [B] or None; out: dict of the dflash_chunk_outputs fields ->
     preallocated int32 CUDA tensors (n_rows = length of row_req)."""
-    lib = _lib or load()
-    assert block_table.is_contiguous()
-    row_req = out["row_req"]
-    o = ChunkOutputs(out["cu_rows"].data_ptr(), out["n_pages"].data_ptr(),
-                     out["alloc_limit"].data_ptr(), out["seq_lens"].data_ptr(),
-                     out["free_head"].data_ptr(), row_req.data_ptr(), out["row_pos"].data_ptr(),
-                     out["row_page"].data_ptr(), out["row_slot"].data_ptr())
-    rc = lib.dflash_chunk_plan(
-        ctypes.byref(geom), n_new.shape[0], row_req.shape[0], n_new.data_ptr(), ctx_len.data_ptr(),
-        n_pages.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), free_pages.shape[0],
-        free_range.data_ptr(), _addr(valid), max_ctx, ctypes.byref(o), _addr(dev_status),
-        _stream(stream))
+    if _calls is None:
+        load()
+    rc = _calls.chunk_plan(geom, n_new, ctx_len, n_pages, block_table, free_pages, free_range,
+                           valid, max_ctx, out, dev_status, stream)
     if rc:
         _check("dflash_chunk_plan", rc)
 
@@ -484,16 +468,10 @@ def dflash_chunk_rope_store(geom, layer, rope, q, k, v, row_pos, row_page, row_s
     head_dim] bf16 CUDA tensors (row-strided views of a packed projection output
     allowed, also as [n_rows, heads, head_dim]); q_out like q.  q and q_out, or
     k and v, may be None."""
-    lib = _lib or load()
-    assert kv_pool is None or kv_pool.is_contiguous()
-    qp, qs = _rows(q)
-    kp, ks = _rows(k)
-    vp, vs = _rows(v)
-    op, os_ = _rows(q_out)
-    rc = lib.dflash_chunk_rope_store(
-        ctypes.byref(geom), layer, row_pos.shape[0], ctypes.byref(rope), qp, qs, kp, ks, vp, vs,
-        _addr(gamma_q), _addr(gamma_k), row_pos.data_ptr(), _addr(row_page), _addr(row_slot), op,
-        os_, _addr(kv_pool), _addr(dev_status), _stream(stream))
+    if _calls is None:
+        load()
+    rc = _calls.chunk_rope_store(geom, layer, rope, q, k, v, row_pos, row_page, row_slot, q_out,
+                                 kv_pool, gamma_q, gamma_k, dev_status, stream)
     if rc:
         _check("dflash_chunk_rope_store", rc)
 
@@ -515,15 +493,11 @@ def dflash_chunk_attention(geom, layer, q, kv_pool, block_table, cu_rows, ctx_le
     allowed); block_table int32 [B, M], cu_rows int32 [B + 1], ctx_len and kv_len
     int32 [B]; workspace: uint8 tensor of dflash_chunk_attention_workspace_bytes
     bytes (None where that is 0)."""
-    lib = _lib or load()
-    assert kv_pool.is_contiguous() and block_table.is_contiguous()
-    qp, qs = _rows(q)
-    op, os_ = _rows(out)
-    rc = lib.dflash_chunk_attention(
-        ctypes.byref(geom), kv_len.shape[0], layer, q.shape[0], qp, qs, kv_pool.data_ptr(),
-        block_table.data_ptr(), cu_rows.data_ptr(), ctx_len.data_ptr(), kv_len.data_ptr(), window,
-        _addr(sinks), 0.0 if scale is None else scale, mask_mode, num_segments, _addr(workspace),
-        0 if workspace is None else workspace.nbytes, op, os_, _addr(dev_status), _stream(stream))
+    if _calls is None:
+        load()
+    rc = _calls.chunk_attention(geom, layer, q, kv_pool, block_table, cu_rows, ctx_len, kv_len,
+                                out, workspace, window, sinks, scale, mask_mode, num_segments,
+                                dev_status, stream)
     if rc:
         _check("dflash_chunk_attention", rc)
 

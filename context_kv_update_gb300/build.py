@@ -2,7 +2,9 @@
 
 Each translation unit under ``csrc/`` compiles in parallel with nvcc; the
 objects link into one shared library next to this file.  The CUDA runtime is
-linked statically, so the library depends only on the driver.
+linked statically, so the library depends only on the driver.  ``csrc/calls.c``,
+the CPython module that marshals the ragged-chunk calls, compiles beside it with
+gcc.
 
     python -m context_kv_update_gb300.build            # build if stale
     python -m context_kv_update_gb300.build --force
@@ -15,12 +17,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libdflash.so")
+CALLS_SRC = os.path.join(CSRC, "calls.c")
+CALLS_PATH = os.path.join(HERE, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -41,13 +46,14 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "dflash.h"),
+                                                                  CALLS_SRC,
                                                                   os.path.abspath(__file__)]
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
         return True
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
@@ -60,6 +66,16 @@ def _compile(src: str, extra=()) -> str:
     if extra:
         sys.stderr.write(r.stderr)
     return obj
+
+
+def _build_calls() -> None:
+    tmp = CALLS_PATH + ".tmp"
+    cmd = [shutil.which("gcc") or "cc", "-O2", "-Wall", "-Werror", "-fPIC", "-shared",
+           "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"], CALLS_SRC, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on calls.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS_PATH)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -76,6 +92,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    _build_calls()
     return LIB_PATH
 
 
