@@ -426,12 +426,14 @@ extern "C" int dflash_block_scatter_attention(
 
 namespace {
 
-// Device memory of two int32 arrays overlaps.
-bool overlap(const int32_t *a, int64_t na, const int32_t *b, int64_t nb) {
+// Two pieces of device memory overlap (sizes in bytes).
+bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return na > 0 && nb > 0 && x < y + static_cast<uintptr_t>(nb) * 4 &&
-         y < x + static_cast<uintptr_t>(na) * 4;
+  return na > 0 && nb > 0 && x < y + static_cast<uintptr_t>(nb) &&
+         y < x + static_cast<uintptr_t>(na);
 }
+
+constexpr int kMaxChunkSegments = 65535;  // a grid's depth
 
 bool rows_ok(const void *p, int64_t stride, int64_t width) {
   return aligned16(p) && stride >= width && stride % 8 == 0;
@@ -451,7 +453,8 @@ int chunk_attention_geom_status(const dflash_geom *g, int B, int n_rows) {
   const long long pool_rows =
       2LL * g->num_layers * g->num_pool_pages * P * static_cast<long long>(g->nkv);
   if (pool_rows >= (1LL << 31) || static_cast<long long>(g->max_pages) * P > (1LL << 31) - 2 * kAttnTileKeys ||
-      static_cast<long long>(n_rows) * g->hq >= (1LL << 31) || B >= (1 << 24))
+      static_cast<long long>(n_rows) * g->hq >= (1LL << 31) ||
+      static_cast<long long>(B) * g->nkv >= (1LL << 30))
     return DFLASH_ERR_UNSUPPORTED_GEOM;
   return DFLASH_OK;
 }
@@ -477,11 +480,13 @@ extern "C" int dflash_chunk_plan(const dflash_geom *g, int B, int n_rows, const 
   if (n_free > 0 && !free_pages) return DFLASH_ERR_INVALID_ARG;
   if (n_rows > 0 && (!o.row_req || !o.row_pos || !o.row_page || !o.row_slot))
     return DFLASH_ERR_INVALID_ARG;
-  const struct { const int32_t *p; int64_t n; } outs[] = {
-      {o.cu_rows, B + 1LL}, {o.n_pages, B}, {o.alloc_limit, B}, {o.seq_lens, B}, {o.free_head, 1},
-      {o.row_req, n_rows}, {o.row_pos, n_rows}, {o.row_page, n_rows}, {o.row_slot, n_rows},
-      {block_table, static_cast<int64_t>(B) * g->max_pages}},
-      ins[] = {{n_new, B}, {ctx_len, B}, {n_pages, B}, {free_pages, n_free}, {free_range, 2}};
+  const int64_t b4 = 4LL * B, r4 = 4LL * n_rows;
+  const struct { const void *p; int64_t n; } outs[] = {
+      {o.cu_rows, b4 + 4}, {o.n_pages, b4}, {o.alloc_limit, b4}, {o.seq_lens, b4},
+      {o.free_head, 4}, {o.row_req, r4}, {o.row_pos, r4}, {o.row_page, r4}, {o.row_slot, r4},
+      {block_table, b4 * g->max_pages}},
+      ins[] = {{n_new, b4}, {ctx_len, b4}, {n_pages, b4}, {free_pages, 4LL * n_free},
+               {free_range, 8}, {valid, valid ? B : 0}};
   for (const auto &a : outs)
     for (const auto &b : ins)
       if (overlap(a.p, a.n, b.p, b.n)) return DFLASH_ERR_INVALID_ARG;
@@ -500,7 +505,8 @@ extern "C" int dflash_chunk_rope_store(const dflash_geom *g, int layer, int n_ro
                                        int32_t *dev_status, dflash_stream_t stream) {
   if (!geom_ok(g) || !rope || layer < 0 || layer >= g->num_layers || n_rows < 0)
     return DFLASH_ERR_INVALID_ARG;
-  if (g->kind != DFLASH_KIND_GQA || g->head_dim % 8 != 0 || g->head_dim > kMaxHeadDim)
+  if (g->kind != DFLASH_KIND_GQA || g->head_dim % 8 != 0 || g->head_dim > kMaxHeadDim ||
+      n_rows >= (1 << 30))
     return DFLASH_ERR_UNSUPPORTED_GEOM;
   const dflash_rope_spec &r = *rope;
   if (r.layout != DFLASH_ROPE_HALF && r.layout != DFLASH_ROPE_PAIRS) return DFLASH_ERR_INVALID_ARG;
@@ -548,7 +554,7 @@ extern "C" int dflash_chunk_attention_num_segments(const dflash_geom *g, int B, 
 extern "C" size_t dflash_chunk_attention_workspace_bytes(const dflash_geom *g, int B, int n_rows,
                                                          int num_segments) {
   if (!geom_ok(g) || B < 0 || n_rows < 0 || num_segments < 0 ||
-      chunk_attention_geom_status(g, B, n_rows))
+      num_segments > kMaxChunkSegments || chunk_attention_geom_status(g, B, n_rows))
     return 0;
   return chunk_attention_workspace_bytes(*g, B, n_rows, num_segments);
 }
@@ -562,7 +568,7 @@ extern "C" int dflash_chunk_attention(const dflash_geom *g, int B, int layer, in
                                       size_t ws_bytes, void *out, int64_t out_row_stride,
                                       int32_t *dev_status, dflash_stream_t stream) {
   if (!geom_ok(g) || B < 0 || n_rows < 0 || layer < 0 || layer >= g->num_layers || window < 0 ||
-      num_segments < 0 || !std::isfinite(scale))
+      num_segments < 0 || num_segments > kMaxChunkSegments || !std::isfinite(scale))
     return DFLASH_ERR_INVALID_ARG;
   if (mask_mode != DFLASH_MASK_CAUSAL_TAIL && mask_mode != DFLASH_MASK_BLOCK_BIDIR)
     return DFLASH_ERR_INVALID_ARG;

@@ -9,6 +9,9 @@
  *   2. the context-KV update itself (fc -> hidden RMSNorm -> stacked per-layer
  *      K/V or latent projection -> k RMSNorm + RoPE -> masked paged store);
  *   3. the block-KV scatter and the decode-shaped split-KV block attention.
+ * Beside them, a layer over a ragged chunk of new tokens (any number of rows per
+ * request): its page and slot plan, its rotary positions and paged store, and its
+ * attention.
  *
  * Conventions shared by every call
  *  - All pointers named as device buffers are device pointers the caller owns
@@ -682,7 +685,8 @@ DFLASH_API int dflash_chunk_plan(const dflash_geom *g, int B, int n_rows, const 
  * multiple of 8, a bad spec: unknown layout or scaling, factor < 1, trained_ctx
  * < 1, betas not positive and in order, values not finite),
  * DFLASH_ERR_UNSUPPORTED_GEOM (MLA, head_dim not a multiple of 8 up to 256,
- * rot_dim odd, < 2 or > head_dim, rope_theta <= 1 with YARN), DFLASH_ERR_CUDA.
+ * rot_dim odd, < 2 or > head_dim, rope_theta <= 1 with YARN, n_rows >= 2^30),
+ * DFLASH_ERR_CUDA.
  * ------------------------------------------------------------------- */
 DFLASH_API int dflash_chunk_rope_store(const dflash_geom *g, int layer, int n_rows,
                                        const dflash_rope_spec *rope, const void *q,
@@ -729,10 +733,10 @@ DFLASH_API int dflash_chunk_rope_store(const dflash_geom *g, int layer, int n_ro
  *              one each.
  * Errors: DFLASH_ERR_INVALID_ARG (null or misaligned pointers, strides below
  * hq * head_dim or not a multiple of 8, bad indices, scale not finite, window
- * < 0, unknown mask_mode), DFLASH_ERR_UNSUPPORTED_GEOM (MLA, head_dim not 64
+ * < 0, unknown mask_mode, num_segments > 65535), DFLASH_ERR_UNSUPPORTED_GEOM (MLA, head_dim not 64
  * or 128, hq not a multiple of nkv, page_size not a multiple of 8 that divides
  * 128 or is a multiple of 128, pool rows >= 2^31, max_pages * page_size >
- * 2^31 - 256, n_rows * hq >= 2^31), DFLASH_ERR_WORKSPACE_TOO_SMALL, DFLASH_ERR_CUDA.
+ * 2^31 - 256, n_rows * hq >= 2^31, B * nkv >= 2^30), DFLASH_ERR_WORKSPACE_TOO_SMALL, DFLASH_ERR_CUDA.
  * ------------------------------------------------------------------- */
 DFLASH_API int dflash_chunk_attention_num_segments(const dflash_geom *g, int B, int n_rows);
 DFLASH_API size_t dflash_chunk_attention_workspace_bytes(const dflash_geom *g, int B, int n_rows,

@@ -23,7 +23,7 @@ def _geom(**over):
     return make_geom(g)
 
 
-def _plan(lib, B=2, n_rows=6, n_free=4, max_ctx=100, g=None, drop=None, alias=None, **ptr):
+def _plan(lib, B=2, n_rows=6, n_free=4, max_ctx=100, g=None, drop=None, alias=None, valid=None):
     """Every pointer distinct and far apart unless named; never reaches a launch
     in these tests."""
     from context_kv_update_gb300 import _lib
@@ -38,7 +38,7 @@ def _plan(lib, B=2, n_rows=6, n_free=4, max_ctx=100, g=None, drop=None, alias=No
     g = g or _geom()
     return lib.dflash_chunk_plan(ctypes.byref(g), B, n_rows, a["n_new"], a["ctx_len"],
                                  a["n_pages"], a["block_table"], a["free_pages"], n_free,
-                                 a["free_range"], None, max_ctx, ctypes.byref(out), None, None)
+                                 a["free_range"], valid, max_ctx, ctypes.byref(out), None, None)
 
 
 def test_struct_sizes(lib):
@@ -63,6 +63,7 @@ def test_plan_refusals(lib):
         assert _plan(lib, alias={o: i}) == bad, (o, i)
     assert _plan(lib, B=8193) == geo
     assert _plan(lib, n_rows=1 << 30) == geo
+    assert _plan(lib, valid=0x1000000) == bad   # the memory of cu_rows
     assert _plan(lib, g=_geom(max_pages=1 << 27, P=16)) == geo
 
 
@@ -98,7 +99,7 @@ def test_rope_refusals(lib):
         assert _rope(lib, **kw) == bad, kw
     for kw in (dict(spec=dict(rot_dim=0)), dict(spec=dict(rot_dim=7)), dict(spec=dict(rot_dim=66)),
                dict(g=_geom(hd=60)), dict(g=_geom(hd=264)), dict(g=_geom(kind="mla")),
-               dict(spec=yarn, g=_geom(rope_theta=1.0))):
+               dict(spec=yarn, g=_geom(rope_theta=1.0)), dict(n_rows=1 << 30)):
         assert _rope(lib, **kw) == geo, kw
 
 
@@ -119,13 +120,13 @@ def test_attention_refusals(lib):
                dict(mask=2), dict(S=-1), dict(scale=float("inf")), dict(scale=float("nan")),
                dict(q=None), dict(pool=None), dict(tbl=None), dict(cu=None), dict(ctx=None),
                dict(kv=None), dict(out=None), dict(q=ODD), dict(out=ODD), dict(pool=ODD),
-               dict(qs=248), dict(qs=260), dict(os=0), dict(os=257), dict(S=3, ws=None),
+               dict(qs=248), dict(qs=260), dict(os=0), dict(os=257), dict(S=65536), dict(S=3, ws=None),
                dict(S=3, ws=ODD)):
         assert _attn(lib, **kw) == bad, kw
     assert _attn(lib, S=3, nb=64) == _lib.DFLASH_ERR_WORKSPACE_TOO_SMALL
     for kw in (dict(g=_geom(kind="mla")), dict(g=_geom(hd=96)), dict(g=_geom(P=12)),
                dict(g=_geom(P=48)), dict(g=_geom(P=192)), dict(g=_geom(num_pool_pages=1 << 25)),
-               dict(g=_geom(max_pages=(1 << 27) - 15)), dict(n_rows=1 << 29)):
+               dict(g=_geom(max_pages=(1 << 27) - 15)), dict(n_rows=1 << 29), dict(B=1 << 29)):
         assert _attn(lib, **kw) == geo, kw
 
 
@@ -139,3 +140,43 @@ def test_attention_workspace(lib):
     assert lib.dflash_chunk_attention_num_segments(G, 2, 6) >= 1
     assert lib.dflash_chunk_attention_num_segments(G, 0, 6) == 0
     assert lib.dflash_chunk_attention_num_segments(None, 1, 6) == 0
+
+
+def test_binding_refuses_what_it_cannot_pass_on(lib):
+    """Arguments the marshalling itself turns away: tensors that are not on the
+    current device (a CPU pointer would reach a kernel), views whose rows are not
+    contiguous, structures of another type, counts past 32 bits."""
+    import torch
+
+    import context_kv_update_gb300 as dl
+    from context_kv_update_gb300 import _lib
+    g = _geom()
+    i32 = torch.zeros(4, dtype=torch.int32)
+    q = torch.zeros((4, 4, 64), dtype=torch.bfloat16)
+    pool = torch.zeros((2, 32, 2, 2, 16, 64), dtype=torch.bfloat16)
+    out = {k: i32 for k in dl.CHUNK_OUTPUT_FIELDS}
+    tbl = torch.zeros((4, 8), dtype=torch.int32)
+    spec = dl.RopeSpec(rot_dim=64)
+    plan = lambda **kw: dl.dflash_chunk_plan(*[kw.get(k, d) for k, d in (  # noqa: E731
+        ("g", g), ("n", i32), ("ctx", i32), ("have", i32), ("tbl", tbl), ("free", i32),
+        ("range", i32), ("valid", None), ("max_ctx", 100), ("out", out))])
+    rope = lambda **kw: dl.dflash_chunk_rope_store(  # noqa: E731
+        kw.get("g", g), 0, kw.get("spec", spec), kw.get("q", q), None, None, i32, None, None, q,
+        kw.get("pool"))
+    attn = lambda **kw: dl.dflash_chunk_attention(  # noqa: E731
+        g, kw.get("layer", 0), kw.get("q", q), pool, tbl, i32, i32, i32, q)
+    # no CUDA device here, or tensors that are not on it
+    for f in (plan, rope, attn):
+        with pytest.raises((ValueError, RuntimeError, AssertionError)):
+            f()
+    for f, kw in ((plan, dict(tbl=tbl[:, ::2])), (rope, dict(q=q.transpose(0, 1))),
+                  (rope, dict(q=q[:, ::2])), (rope, dict(pool=pool[:, :, :1])),
+                  (attn, dict(q=q[:, :, ::2]))):
+        with pytest.raises(AssertionError):
+            f(**kw)
+    with pytest.raises(KeyError):
+        plan(out={})
+    with pytest.raises(OverflowError):
+        attn(layer=1 << 40)
+    with pytest.raises(TypeError):
+        _lib._calls.chunk_plan(g)

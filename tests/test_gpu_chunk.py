@@ -489,6 +489,116 @@ def test_attention_long_cache(dl):
     np.testing.assert_array_equal(bf16_f64(bits(out)).reshape(near.shape), near)
 
 
+# Work tiles of 256 rows (the mean request fills more than one tile of 128), with a
+# remainder of each kind, and requests of a few rows among them.
+WIDE = {"full_and_rest": ([130, 3], [0, 700]), "one_over": ([65], [500]),
+        "half": ([96, 64], [40, 0]), "long": ([200, 1, 0, 70], [129, 1000, 9, 3])}
+
+
+@pytest.mark.parametrize("shape", WIDE)
+@pytest.mark.parametrize("window,sinks,causal", [(0, False, True), (150, True, True),
+                                                 (1, False, True), (40, True, False)])
+def test_attention_wide_tiles(dl, shape, window, sinks, causal):
+    rng = np.random.default_rng(23)
+    n, ctx = WIDE[shape]
+    kw = dict(hq=4, nkv=1, hd=128, P=16)
+    pb = attn_problem(rng, n, ctx, **kw)
+    run_attn(dl, pb, **kw, window=window, causal=causal, pad_rows=1,
+             sinks=rng.standard_normal(4) if sinks else None)
+
+
+@pytest.mark.parametrize("S", [2, 5])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attention_wide_tiles_in_segments(dl, S, hd):
+    rng = np.random.default_rng(24)
+    kw = dict(hq=8, nkv=1, hd=hd, P=64)
+    pb = attn_problem(rng, [70, 1, 5], [600, 300, 0], **kw)
+    for sinks in (None, rng.standard_normal(8)):
+        run_attn(dl, pb, **kw, S=S, sinks=sinks, pad_rows=2)
+        run_attn(dl, pb, **kw, S=S, sinks=sinks, window=130)
+
+
+def test_attention_wide_tiles_bad_pages_and_cut_cache(dl):
+    rng = np.random.default_rng(25)
+    kw = dict(hq=8, nkv=2, hd=64, P=16)
+    pb = attn_problem(rng, [90, 40], [200, 150], **kw)
+    pb["table"][0, 3], pb["table"][0, 15], pb["table"][1, 9] = -1, pb["NP"] + 5, -7
+    run_attn(dl, pb, **kw, flags=8)
+    run_attn(dl, pb, **kw, flags=8, S=3)
+    pb = attn_problem(rng, [90, 40], [200, 150], **kw)
+    pb["kv"] = np.array([250, 0], np.int32)
+    for S in (1, 3):
+        got = run_attn(dl, pb, **kw, window=20, S=S)
+        assert np.all(got[69:] == 0)   # rows at 269 on see keys 250 on; the second request none
+
+
+def test_attention_many_requests(dl):
+    """More requests than a warp searches at once, some empty, tiles of each."""
+    rng = np.random.default_rng(26)
+    kw = dict(hq=2, nkv=1, hd=64, P=16)
+    n = [int(x) for x in rng.integers(0, 4, 1100)]
+    n[500] = 150
+    pb = attn_problem(rng, n, [int(x) for x in rng.integers(0, 30, 1100)], **kw)
+    run_attn(dl, pb, **kw)
+    run_attn(dl, pb, **kw, S=2)
+
+
+def test_attention_calls_at_once(dl):
+    """Two calls on two streams with a workspace each, many times over, give what
+    each gives alone."""
+    import torch
+    rng = np.random.default_rng(27)
+    kw = dict(hq=8, nkv=2, hd=128, P=64)
+    pbs = [attn_problem(rng, [1, 2], [900, 1500], **kw), attn_problem(rng, [40, 3], [300, 64], **kw)]
+    want = [run_attn(dl, pb, **kw, S=4) for pb in pbs]
+    streams, outs, keep = [torch.cuda.Stream() for _ in pbs], [], []
+    for s, pb in zip(streams, pbs):
+        g = geom(dl, P=64, hq=8, nkv=2, hd=128, M=pb["M"], NP=pb["NP"])
+        n = pb["q"].shape[0]
+        a = [bf16(pb["q"])[0], bf16(pb["pool"])[0], *(dev(pb[k]) for k in ("table", "cu", "ctx", "kv"))]
+        ws = torch.empty(dl.dflash_chunk_attention_workspace_bytes(g, 2, n, 4), dtype=torch.uint8,
+                         device="cuda")
+        outs.append([torch.empty_like(a[0]) for _ in range(20)])
+        keep.append((g, a, ws))
+    torch.cuda.synchronize()
+    for i in range(20):
+        for s, o, (g, a, ws) in zip(streams, outs, keep):
+            dl.dflash_chunk_attention(g, 0, *a, o[i], ws, num_segments=4, stream=s)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        for x in o:
+            np.testing.assert_array_equal(bf16_f64(bits(x)).reshape(w.shape), w)
+
+
+def test_a_workspace_serves_captured_graphs_in_turn(dl):
+    """Two graphs captured on one workspace and replayed one after the other: each
+    leaves nothing there that the other needs."""
+    import torch
+    rng = np.random.default_rng(28)
+    kw = dict(hq=8, nkv=2, hd=64, P=16)
+    pbs = [attn_problem(rng, [1, 1], [500, 800], **kw), attn_problem(rng, [2], [300], **kw)]
+    want = [run_attn(dl, pb, **kw, S=3) for pb in pbs]
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    graphs, outs, keep = [], [], []
+    for pb in pbs:
+        g = geom(dl, P=16, hq=8, nkv=2, hd=64, M=pb["M"], NP=pb["NP"])
+        a = [bf16(pb["q"])[0], bf16(pb["pool"])[0], *(dev(pb[k]) for k in ("table", "cu", "ctx", "kv"))]
+        o = torch.empty_like(a[0])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            dl.dflash_chunk_attention(g, 0, *a, o, ws, num_segments=3)
+        graphs.append(graph)
+        outs.append(o)
+        keep.append((g, a))
+    for _ in range(3):
+        for graph, o, w in zip(graphs, outs, want):
+            o.fill_(7.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            np.testing.assert_array_equal(bf16_f64(bits(o)).reshape(w.shape), w)
+
+
 @pytest.mark.parametrize("rows", [1, 90])
 def test_attention_unloaded_tile_times_out_cleanly(dl, rows):
     """The bounded waits: the producer leaves one key tile unloaded, the kernel
