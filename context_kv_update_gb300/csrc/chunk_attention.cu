@@ -651,34 +651,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, chunk_wait<false>(ptx::smem_u32(&o_done[g]), 0u, abort_flag));
         ptx::tc_fence_after();
       }
-      if (split && ok && n > 1 - g)  // the other group's products: the ring is idle after them
+      if (split && ok && n > 1 - g) {  // the other group's products
         ok = __all_sync(0xffffffffu, chunk_wait<false>(ptx::smem_u32(&o_done[g ^ 1]), 0u, abort_flag));
+        ptx::tc_fence_after();
+      }
       // the row's state over both groups, and this thread's share of its dims
       const int dims = split ? HD / 2 : HD, d0 = split ? g * (HD / 2) : 0;
       float m = ok ? m_ref : -INFINITY, own = 1.f, other = 0.f;
-      const float *xo = nullptr;
       if (split) {
-        // the other group's half of the dims goes through the idle ring
-        float *sx = reinterpret_cast<float *>(ring);  // [2][HD / 2][128], then m and l [2][128]
-        float *smx = sx + HD * 128;
-        smx[g * 128 + tid] = m;
-        smx[256 + g * 128 + tid] = l;
-        if (u > 0 && ok && active) {
-#pragma unroll
-          for (int c = 0; c < HD / 2; c += 32) {
-            float ov[32];
-            ptx::tmem_ld32f_sync(tm_o + (g ^ 1) * (HD / 2) + c, ov);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) sx[(g * (HD / 2) + c + e) * 128 + tid] = ov[e];
-          }
-        }
+        // Both groups hold the row in the same TMEM lane: the states go through shared
+        // memory (the idle ring), the other accumulator is read where it is.
+        float *sx = reinterpret_cast<float *>(ring);  // m and l [2][128]
+        sx[g * 128 + tid] = m;
+        sx[256 + g * 128 + tid] = l;
         const bool bad = ptx::bar_or(1, 256, !ok);
-        const float m2 = smx[(g ^ 1) * 128 + tid], l2 = smx[256 + (g ^ 1) * 128 + tid];
+        const float m2 = sx[(g ^ 1) * 128 + tid], l2 = sx[256 + (g ^ 1) * 128 + tid];
         m = bad ? -INFINITY : fmaxf(m_ref, m2);
         own = bad || m_ref == -INFINITY ? 0.f : ptx::ex2(m_ref - m);
         other = bad || m2 == -INFINITY ? 0.f : ptx::ex2(m2 - m);
         l = l * own + l2 * other;
-        xo = sx + (g ^ 1) * (HD / 2) * 128 + tid;
       }
       const bool any = real && m != -INFINITY;  // the row saw a key
       const int64_t orow = static_cast<int64_t>(rq.a) + tok;
@@ -711,9 +702,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
-        if (other != 0.f) {
+        if (split && ok && n > 1 - g) {
+          float x[32];
+          ptx::tmem_ld32f_sync(tmem + kColO + HD * (g ^ 1) + lane_off + d0 + c, x);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] += xo[(c + e) * 128] * other;
+          for (int e = 0; e < 32; ++e) o[e] += other != 0.f ? x[e] * other : 0.f;
         }
         if (!real) continue;
         if (p.S == 1) {
