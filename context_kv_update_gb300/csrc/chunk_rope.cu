@@ -8,8 +8,9 @@
 // rotation are fp32, rounded to bf16 once at the store (nearest even).
 //
 // Bound by HBM: 8192 rows of 32 + 8 + 8 heads of 128 (201 MB) take 40 us, 5.0 TB/s,
-// where a plain copy of as many bytes takes 33; a few rows are bound by latency
-// (16 rows: 4 us on the device).
+// where a plain copy of as many bytes takes 33; 40000 rows of 24 + 4 + 4 heads of 64
+// take 53, 6.2 TB/s (65 with groups of at most four rows); a few rows are bound
+// by latency (16 rows: 4 us on the device).
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -93,7 +94,7 @@ __device__ __forceinline__ Chunk<VW> pack(const float2 *x) {
 }
 
 constexpr int kRopeWarps = 8;    // of a CTA
-constexpr int kMaxRopeRows = 4;  // rows of a CTA
+constexpr int kMaxRopeRows = 8;  // rows of a group, at most: a warp each
 constexpr int kRopeSmem = 208 * 1024;
 
 // Bulk copy of `bytes` (a multiple of 16) from global to shared memory.
