@@ -13,10 +13,10 @@
 // start at floor(cu_r G / TR) + r, which leaves it room for ceil(rows G / TR).
 //
 // Three warpgroups a CTA, one CTA an SM: warps 0-3 and 4-7 are two softmax
-// groups (one thread a row, 128 rows), warp 8 issues every MMA, warp 9 the TMA
-// loads.  Each group has its own scores S (128 columns of tensor
-// memory; its weights P overwrite them) and accumulator O, so one group's softmax
-// runs under the other's two products:
+// groups (one thread a row, 128 rows), warp 8 finds the CTA's next work tile and brings
+// its Q with warp 9, warp 10 issues the loads of K and V, warp 11 every MMA.  Each group
+// has its own scores S (128 columns of tensor memory; its weights P overwrite them) and
+// accumulator O, so one group's softmax runs under the other's two products:
 //   more than 128 rows: the groups hold two row tiles over the same key tiles;
 //   otherwise the groups take the even and the odd key tiles of the one row tile
 //   and their halves are joined at the end (few rows: the key stream is the work).
@@ -24,6 +24,12 @@
 // K and V tiles come through one ring of 128-key slots in the order they are
 // used; products of one issuing thread execute in order, so the next scores may
 // be issued over the weights that the product before them reads.
+//
+// Where the grid has more work tiles than there are SMs, a CTA claims blocks that have
+// not started (cluster launch control) and goes through its work tiles without a break
+// between them: loads, Q and first scores of the next run under the end of the last (4096
+// rows of a prompt 131 us with a CTA for each tile, 118 so; 2311 rows of 16 requests,
+// window 1024: 75 and 66).
 //
 // Few row tiles: the keys are cut into S segments (grid z), each writes (m, l,
 // O) to the workspace and chunk_merge_kernel joins them.
@@ -34,13 +40,13 @@
 //
 // Bound: single tokens by HBM (64 of them over 1 to 8192 keys each, 32 heads over 8 of
 // 128: 226 us, 5.5 TB/s), long chunks by the tensor cores (1024 rows behind 32768
-// keys: 430 us, 1.30 PFLOP/s with 128 of the 152 SMs at work; 16384 rows of one
-// prompt: 1.47 PFLOP/s).  In the 256-row form a key tile takes ~3250 cycles for 2048 of
+// keys: 420 us, 1.33 PFLOP/s with 128 of the 152 SMs at work; 16384 rows of one
+// prompt: 1.55 PFLOP/s).  In the 256-row form a key tile takes ~3250 cycles for 2048 of
 // products: their operands and the loads keep shared memory busy for another ~2000 of
 // 128 bytes each, and every hand-over between a softmax group and the issuing thread waits
-// behind them.  A work tile's start and end (finding its request, Q, the first
-// scores, the output) are ~14000 cycles more, which bounds short key spans (2311 rows, a
-// window of 1024: 75 us).
+// behind them.  A work tile ends with ~7000 cycles in which a group has no scores to
+// work on (its last product, its output, the next tile's row ranges), which bounds short key
+// spans (the 2311 rows: 9 key tiles each).
 #include <cuda.h>
 #include <math.h>
 
@@ -54,6 +60,11 @@ namespace dflash {
 
 cudaError_t make_tmap_bf16_2d(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols,
                               uint64_t row_stride_elems, uint32_t box_rows, uint32_t box_cols);
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled_fn();
 
 namespace {
 
@@ -65,7 +76,9 @@ constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 216, kIssueRegs = 72;
 static_assert(256 * kSoftmaxRegs + 128 * kIssueRegs <= kThreads * 168, "register split");
 constexpr int kSmemMax = 227 * 1024;
-constexpr int kDone = 8;  // barriers of the iterations in flight (more than half the slots + 1)
+// Barriers of the events that free ring slots, more than can be between a slot's use
+// and its next: each event frees a slot or two, of at most 12.
+constexpr int kDone = 16;
 constexpr uint32_t kChunkBytes = kKT * 128;  // 64 dims of 128 rows, 128-byte swizzled
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;  // S of group g at 128 g, O at 256 + HD g
@@ -73,7 +86,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 struct ChunkParams {
   int B, n_rows, hq, nkv, G, wide_out, layer, NP, P, M, window, mask_mode, S;
-  int box_rows, skip_tile;
+  int box_rows, skip_tile, q_boxes, claims;
   uint32_t g_inv;  // ceil(2^32 / G), for G > 1
   float scale_log2;
   const uint16_t *q;
@@ -141,9 +154,9 @@ __device__ __forceinline__ void regs_less() {
 // after about two seconds, or once another thread has set *abort.  kSpin: with
 // the probe that does not suspend the thread (waking up takes longer than the
 // wait does), for the waits between the products and the softmax.
-template <bool kSpin>
+template <bool kSpin, int kTimes = 1>
 __device__ __forceinline__ bool chunk_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
-  constexpr long long kLimit = 4000000000ll;  // cycles
+  constexpr long long kLimit = kTimes * 4000000000ll;  // cycles
   auto probe = [&] { return kSpin ? ptx::mbar_test(bar, parity) : ptx::mbar_try_wait(bar, parity); };
   if (probe()) return true;
   const long long t0 = clock64();
@@ -194,11 +207,13 @@ __device__ __forceinline__ int find_request(const ChunkParams &p, int64_t x, int
 struct Request {
   int a, b, c, kv;
 };
-__device__ __forceinline__ bool load_request(const ChunkParams &p, int r, bool report, Request *q) {
+__device__ __forceinline__ void load_request(const ChunkParams &p, int r, Request *q) {
   q->a = p.cu[r];
   q->b = p.cu[r + 1];
   q->c = p.ctx[r];
   q->kv = p.kv[r];
+}
+__device__ __forceinline__ bool check_request(const ChunkParams &p, bool report, Request *q) {
   if (q->a < 0 || q->b < q->a || q->b > p.n_rows || q->c < 0 || q->c > INT32_MAX - p.n_rows) {
     if (report) raise_status(p.st, DFLASH_DEV_BAD_ROWS);
     return false;
@@ -217,22 +232,121 @@ __device__ __forceinline__ void key_range(const ChunkParams &p, int pos, int kv,
   *lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
 }
 
-// Shared memory: Q tiles, the slot ring, barriers.
+// A work tile's rows [row0, row0 + nrow) of request r's flat rows, the keys
+// [lo_min, hi_max] some of them sees, and its key tiles [t0, t0 + n).
+struct __align__(16) Work {
+  int r, kvh, seg, a, c, kv, total;  // chunk rows from a, positions from c, flat rows in all
+  int row0, nrow, lo_min, hi_max, t0, n;
+  int pad[3];
+};
+
+// Work tile (x, seg) of the grid; nrow 0 where it holds no rows.  The whole warp.
+// Later rows see more keys, so the last tiles of all heads go first (heads one
+// after the other leave a head's longest tiles for the end).
+__device__ __forceinline__ Work describe(const ChunkParams &p, int block, int seg, int shift,
+                                         int lane) {
+  Work w = {};
+  w.kvh = block % p.nkv;
+  w.seg = seg;
+  const int64_t x = gridDim.x / p.nkv - 1 - block / p.nkv;
+  Request q;
+  if (p.B <= 32) {  // in one memory round trip: a request a lane
+    const int i = min(lane, p.B - 1);
+    q.a = p.cu[i];
+    q.b = p.cu[i + 1];
+    q.c = p.ctx[i];
+    q.kv = p.kv[i];
+    const int64_t tile = ((static_cast<int64_t>(q.a) * p.G) >> shift) + i;
+    w.r = max(__popc(__ballot_sync(0xffffffffu, lane < p.B && tile <= x)), 1) - 1;
+    q.a = __shfl_sync(0xffffffffu, q.a, w.r);
+    q.b = __shfl_sync(0xffffffffu, q.b, w.r);
+    q.c = __shfl_sync(0xffffffffu, q.c, w.r);
+    q.kv = __shfl_sync(0xffffffffu, q.kv, w.r);
+  } else {
+    w.r = find_request(p, x, shift, lane);
+    load_request(p, w.r, &q);
+  }
+  if (!check_request(p, lane == 0 && w.kvh == 0 && seg == 0, &q)) return w;
+  const int64_t first = (x - (((static_cast<int64_t>(q.a) * p.G) >> shift) + w.r)) << shift;
+  w.a = q.a;
+  w.c = q.c;
+  w.kv = q.kv;
+  w.total = (q.b - q.a) * p.G;
+  if (first < 0 || first >= w.total) return w;
+  w.row0 = static_cast<int>(first);
+  w.nrow = min(w.total - w.row0, 1 << shift);
+  int lo, hi;
+  key_range(p, w.c + w.row0 / p.G, w.kv, &w.lo_min, &hi);
+  key_range(p, w.c + (w.row0 + w.nrow - 1) / p.G, w.kv, &lo, &w.hi_max);
+  if (w.lo_min <= w.hi_max) {
+    const int ta = w.lo_min / kKT, tb = w.hi_max / kKT + 1;
+    const int per = (tb - ta + p.S - 1) / p.S;
+    w.t0 = ta + seg * per;
+    w.n = max(min(tb - w.t0, per), 0);
+  }
+  return w;
+}
+
+// Ask for a block of the grid that has not started, to do its work here; the
+// answer (16 bytes) arrives on `bar`.
+__device__ __forceinline__ void claim_block(uint32_t answer, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], "
+      "[%1];" ::"r"(answer),
+      "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ bool claimed_block(uint32_t answer, int *x, int *z) {
+  uint32_t got;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t"
+      "ld.shared.b128 a, [%3];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::z.b32.b128 %2, a;\n\t}"
+      : "=&r"(got), "=&r"(*x), "=&r"(*z)
+      : "r"(answer)
+      : "memory");
+  return got != 0;
+}
+// Box of a [tokens][heads][dims] tensor.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, int32_t c0,
+                                            int32_t c1, int32_t c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src))
+               : "memory");
+}
+
+// Shared memory: Q tiles, the slot ring, barriers, the work in hand.
 template <int HD, bool kPair>
 struct Layout {
   static constexpr uint32_t kSlotBytes = HD / 64 * kChunkBytes;
   static constexpr uint32_t kRing = (kPair ? 2 : 1) * kSlotBytes;
-  static constexpr uint32_t kBarBytes = (12 + kDone + 12) * 8;
+  static constexpr uint32_t kWords = (12 + kDone + 13) * 8;  // barriers, then three words
+  static constexpr uint32_t kWork = (kWords + 12 + 15) / 16 * 16;
+  static constexpr uint32_t kAnswer = kWork + 2 * sizeof(Work);
+  static constexpr uint32_t kJoin = kAnswer + 16;  // m, then l, of a split tile [256]
+  static constexpr uint32_t kBarBytes = kJoin + 1024;
   static constexpr int kFit = (kSmemMax - 1024 - kBarBytes - kRing) / kSlotBytes;
   static constexpr int kSlots = kFit < 12 ? kFit : 12;
   static constexpr uint32_t kBars = kRing + kSlots * kSlotBytes;
   static constexpr uint32_t kBytes = 1024 + kBars + kBarBytes;
-  static_assert(kSlots >= 5 && kDone > kSlots / 2 + 1, "");
+  static_assert(kSlots >= 5, "");
 };
 
 template <int HD, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
-    chunk_attn_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ ChunkParams p) {
+    chunk_attn_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tq,
+                      const __grid_constant__ ChunkParams p) {
   constexpr int kChunks = HD / 64;
   constexpr int kShift = kPair ? 8 : 7;
   using Lay = Layout<HD, kPair>;
@@ -244,9 +358,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *ring = sm + Lay::kRing;  // Q tiles come first
   uint64_t *full = reinterpret_cast<uint64_t *>(sm + Lay::kBars), *done = full + 12;
   uint64_t *s_full = done + kDone, *p_full = s_full + 2, *o_done = p_full + 2;
-  uint64_t *q_full = o_done + 2, *drain = q_full + 1;
-  uint32_t *tslot = reinterpret_cast<uint32_t *>(drain + 1);
+  uint64_t *q_full = o_done + 2, *q_empty = q_full + 1, *drain = q_empty + 1;
+  uint64_t *work_full = drain + 1, *work_read = work_full + 1, *claim = work_read + 1;
+  uint64_t *pages_seen = claim + 1;
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Lay::kBars + Lay::kWords);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
+  volatile int *bad_flag = abort_flag + 1;  // the work's segment has pages outside the pool
+  Work *shared_work = reinterpret_cast<Work *>(sm + Lay::kBars + Lay::kWork);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -257,7 +375,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(ptx::smem_u32(&p_full[g]), 4);  // one arrival per warp of the group
       ptx::mbar_init(ptx::smem_u32(&o_done[g]), 1);
     }
-    ptx::mbar_init(ptx::smem_u32(q_full), 8);
+    ptx::mbar_init(ptx::smem_u32(q_full), 2);  // the loading warps
+    ptx::mbar_init(ptx::smem_u32(q_empty), 1);
+    ptx::mbar_init(ptx::smem_u32(work_full), 1);
+    ptx::mbar_init(ptx::smem_u32(work_read), 11);  // every other warp
+    ptx::mbar_init(ptx::smem_u32(claim), 1);
+    ptx::mbar_init(ptx::smem_u32(pages_seen), 1);
     ptx::mbar_init(ptx::smem_u32(drain), 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
@@ -274,129 +397,256 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::griddep_launch();
   ptx::griddep_wait();
 
-  // This CTA's rows [row0, row0 + nrow) of request r's flat rows, the keys
-  // [lo_min, hi_max] some of them sees, and its key tiles [t0, t0 + n).  Later
-  // rows see more keys, so the last tiles of all heads go first (heads one after
-  // the other leave a head's longest tiles for the end).
-  const int kvh = blockIdx.x % p.nkv, seg = blockIdx.z;
-  const int64_t x = gridDim.x / p.nkv - 1 - blockIdx.x / p.nkv;
-  const int r = find_request(p, x, kShift, lane);
-  Request rq;
-  int row0 = 0, nrow = 0, lo_min = 0, hi_max = -1, t0 = 0, n = 0;
-  if (load_request(p, r, threadIdx.x == 0 && kvh == 0 && seg == 0, &rq)) {
-    const int64_t first = (x - first_tile(p, r, kShift)) << kShift;
-    const int total = (rq.b - rq.a) * p.G;
-    if (first >= 0 && first < total) {
-      row0 = static_cast<int>(first);
-      nrow = min(total - row0, 1 << kShift);
-      int lo, hi;
-      key_range(p, rq.c + row0 / p.G, rq.kv, &lo_min, &hi);
-      key_range(p, rq.c + (row0 + nrow - 1) / p.G, rq.kv, &lo, &hi_max);
-      if (lo_min <= hi_max) {
-        const int ta = lo_min / kKT, tb = hi_max / kKT + 1;
-        const int per = (tb - ta + p.S - 1) / p.S;
-        t0 = ta + seg * per;
-        n = max(min(tb - t0, per), 0);
+  // The CTA's works, one after the other: its own block of the grid, then blocks that
+  // have not started (there are none where the grid fits the SMs).  The next one is
+  // claimed when the loads come to this one's last key tiles, so its own loads and first
+  // scores run under the last values and the output of this one; claimed as this
+  // one begins, long works pile up on some SMs (64 single tokens over up to 8192 keys 258 us
+  // instead of 226).  Every warp sees every work; wound down, it passes over them.
+  // (Its wait for one is longer than all that the scheduler can spend before it
+  // announces one, so no warp of the softmax groups gives up alone and leaves the others in
+  // a barrier.)
+  auto next_work = [&](uint32_t w) {
+    volatile int dummy = 0;
+    Work d = {};
+    if (__all_sync(0xffffffffu,
+                   chunk_wait<false, 16>(ptx::smem_u32(work_full), w & 1, &dummy)))
+      d = shared_work[w & 1];
+    else
+      *abort_flag = 1;
+    return d;
+  };
+  auto have_read = [&] {
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(work_read));
+  };
+  // A work's Q rows into shared memory, K-major, 128-byte swizzle, once the scores of
+  // the work before are done.  Many rows whose tiles begin with a token (the
+  // group's heads divide 128) come as tensor boxes: 64 KB took two warps of 16-byte
+  // copies 8000 to 12000 cycles, in the way of the next work.  Otherwise each of two warps
+  // copies half of them.  Rows past the end are left as they are: they reach no other
+  // row.
+  auto q_in_boxes = [&](const Work &d) { return p.q_boxes && d.nrow > 64; };
+  auto load_q = [&](const Work &d, int half, uint32_t count) {
+    bool ok = true;
+    if (count > 0)
+      ok = __all_sync(0xffffffffu,
+                      chunk_wait<false>(ptx::smem_u32(q_empty), (count - 1) & 1, abort_flag));
+    if (!ok) return false;
+    if (q_in_boxes(d)) {
+      if (half == 0 && lane == 0) {
+        const int tiles = kPair && d.nrow > 128 ? 2 : 1, tok0 = d.row0 / p.G;
+        ptx::mbar_arrive_expect_tx(ptx::smem_u32(q_full), tiles * kSlotBytes);
+        for (int t = 0; t < tiles; ++t)
+          for (int c = 0; c < kChunks; ++c)
+            tma_load_3d(ptx::smem_u32(sm) + t * kSlotBytes + c * kChunkBytes, &tq, 64 * c,
+                        d.kvh * p.G, d.a + tok0 + t * (128 / p.G), ptx::smem_u32(q_full));
       }
+      __syncwarp();
+      return true;
     }
-  }
-  // one row tile: the groups take its even and its odd key tiles
-  const bool split = !kPair || nrow <= 128;
+    constexpr int kUnits = HD / 8, kAtOnce = 64 / kUnits;  // 16-byte units of a row
+    const int u = lane % kUnits, tok0 = d.row0 / p.G, rem0 = d.row0 - tok0 * p.G;
+    const uint32_t base = ptx::smem_u32(sm) + (u >> 3) * kChunkBytes;
+    for (int row = half * (kAtOnce / 2) + lane / kUnits; row < d.nrow; row += kAtOnce) {
+      const int x = rem0 + row;
+      // x / G by the reciprocal, exact for x G < 2^32
+      const int tok = p.G == 1 ? x : static_cast<int>(__umulhi(x, p.g_inv));
+      const uint16_t *from = p.q + (d.a + tok0 + tok) * p.qs +
+                             static_cast<int64_t>(d.kvh * p.G + x - tok * p.G) * HD;
+      copy_async16(base + (row >> 7) * kSlotBytes + (row & 127) * 128 +
+                       (((u & 7) ^ (row & 7)) << 4),
+                   from + 8 * u);
+    }
+    return true;
+  };
+  auto q_copied = [&] {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(q_full));
+  };
 
   if (warp >= 8) {
     regs_less<kIssueRegs>();
-    if (n > 0 && warp == 10) {
+    if (warp == 8) {
+      // ---------------------------------------------- scheduler, half of Q
+      int block = blockIdx.x, seg = blockIdx.z;
+      bool have = true, last = !p.claims;
+      uint32_t claims = 0, loads = 0;
+      for (uint32_t w = 0;; ++w) {
+        Work d = {};
+        while (true) {
+          if (have) {
+            d = describe(p, block, seg, kShift, lane);
+            have = false;
+            if (d.nrow > 0) break;
+          }
+          if (last) break;
+          const uint32_t answer = ptx::smem_u32(sm) + Lay::kBars + Lay::kAnswer;
+          if (lane == 0) {
+            ptx::fence_proxy_async_smem();
+            ptx::mbar_arrive_expect_tx(ptx::smem_u32(claim), 16);
+            claim_block(answer, ptx::smem_u32(claim));
+          }
+          __syncwarp();
+          volatile int dummy = 0;
+          have = __all_sync(0xffffffffu,
+                            chunk_wait<false, 4>(ptx::smem_u32(claim), claims & 1, &dummy)) &&
+                 claimed_block(answer, &block, &seg);
+          __syncwarp();
+          ++claims;
+          last = !have;  // none left: not to be asked again
+        }
+        if (lane == 0) {
+          shared_work[w & 1] = d;
+          ptx::mbar_arrive(ptx::smem_u32(work_full));
+        }
+        __syncwarp();
+        if (d.nrow == 0) break;
+        if (d.n > 0 && load_q(d, 0, loads++) && !q_in_boxes(d)) q_copied();
+        if (!p.claims) break;
+        volatile int dummy = 0;
+        if (!__all_sync(0xffffffffu,
+                        chunk_wait<false, 4>(ptx::smem_u32(work_read), w & 1, &dummy)) ||
+            *abort_flag)
+          last = true;
+      }
+      if (*abort_flag && loads > 0) {  // wind down: Q's last boxes land before the CTA ends
+        volatile int dummy = 0;
+        chunk_wait<false>(ptx::smem_u32(q_full), (loads - 1) & 1, &dummy);
+      }
+    } else if (warp == 9) {
+      // ---------------------------------------------- half of Q, the pages' check
+      uint32_t loads = 0;
+      for (uint32_t w = 0; w == 0 || p.claims; ++w) {
+        const Work d = next_work(w);
+        have_read();
+        if (d.nrow == 0) break;
+        if (d.n == 0) continue;
+        // pages of the segment outside the pool: none, as a rule
+        const int32_t *pages = p.tbl + static_cast<int64_t>(d.r) * p.M;
+        const int last_page = min(d.hi_max, (d.t0 + d.n) * kKT - 1) / p.P;
+        int lp = max(d.lo_min, d.t0 * kKT) / p.P + lane;
+        const int first = lp <= last_page ? pages[lp] : 0;
+        if (load_q(d, 1, loads++)) q_copied();
+        bool bad = first < 0 || first >= p.NP;
+        while ((lp += 32) <= last_page) bad |= pages[lp] < 0 || pages[lp] >= p.NP;
+        bad = __any_sync(0xffffffffu, bad);
+        if (lane == 0) {
+          *bad_flag = bad;
+          if (bad) raise_status(p.st, DFLASH_DEV_BAD_PAGE);
+          ptx::mbar_arrive(ptx::smem_u32(pages_seen));
+        }
+        __syncwarp();
+      }
+    } else if (warp == 10) {
       // ---------------------------------------------- TMA producer
       // A lane per box (page rows x 64 dims).  Boxes without a visible key and
       // pages outside the pool are not loaded; their keys are masked below.
+      // The next work is claimed once the loads come to the last kAhead tiles.
+      constexpr int kAhead = 3;
       const int boxes = kKT / p.box_rows;
-      const uint64_t pol = (rq.b - rq.a) * p.G <= (1 << kShift) ? ptx::policy_evict_first()
-                                                                : ptx::policy_evict_normal();
-      auto fetch = [&](int t) {  // page of box `lane` of tile t, -1 where it is not loaded
-        int page = -1;
-        if (lane < boxes && t < n) {
-          const int key0 = (t0 + t) * kKT + lane * p.box_rows;
-          if (key0 <= hi_max && key0 + p.box_rows > lo_min) {
-            page = p.tbl[static_cast<int64_t>(r) * p.M + key0 / p.P];
-            if (page >= p.NP) page = -1;
+      int at = 0;  // place of the next load in the ring's order
+      // The events that free slots, counted over all works.  Two row tiles: the
+      // work's event 0 is the first scores, 1 + t tile t's values and tile t + 1's
+      // scores; one: events 0 and 1 (with one key tile 0) the first scores, then one for tile
+      // t's values and tile t + 2's scores.  Lane s keeps the one that frees slot s.
+      int events = 0, freed_by = 0;
+      bool ok = true;
+      for (uint32_t w = 0; w == 0 || p.claims; ++w) {
+        const Work d = next_work(w);
+        if (d.nrow == 0 || d.n == 0 || !ok) {
+          have_read();
+          if (d.nrow == 0) break;
+          continue;
+        }
+        const int n = d.n, t0 = d.t0, lo_min = d.lo_min, hi_max = d.hi_max;
+        const int first = kPair && d.nrow > 128 ? 1 : min(n, 2);  // events before V 0's
+        const uint64_t pol =
+            d.total <= (1 << kShift) ? ptx::policy_evict_first() : ptx::policy_evict_normal();
+        auto fetch = [&](int t) {  // page of box `lane` of tile t, -1 where it is not loaded
+          int page = -1;
+          if (lane < boxes && t < n) {
+            const int key0 = (t0 + t) * kKT + lane * p.box_rows;
+            if (key0 <= hi_max && key0 + p.box_rows > lo_min) {
+              page = p.tbl[static_cast<int64_t>(d.r) * p.M + key0 / p.P];
+              if (page >= p.NP) page = -1;
+            }
+          }
+          return page;
+        };
+        auto load = [&](int t, int kv, int page) {
+          if (!ok) return;
+          bool got = true;
+          const int last = __shfl_sync(0xffffffffu, freed_by, at % kSlots);
+          if (lane == 0 && at >= kSlots)
+            got = chunk_wait<false>(ptx::smem_u32(&done[last % kDone]),
+                                    static_cast<uint32_t>((last / kDone) & 1), abort_flag);
+          ok = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
+          if (!ok) return;
+          const bool skip = t == p.skip_tile && kv == 0;
+          const int slot = at % kSlots;
+          if (lane == slot) freed_by = events + t + (kv ? first : 0);
+          const uint32_t bar = ptx::smem_u32(&full[slot]);
+          const uint32_t bytes =
+              __popc(__ballot_sync(0xffffffffu, page >= 0)) * kChunks * p.box_rows * 128u;
+          if (lane == 0 && !skip) ptx::mbar_arrive_expect_tx(bar, bytes);
+          __syncwarp();
+          // other lanes for each load: one thread's copies complete one after another
+          const int j = (lane - at * boxes * kChunks) & 31, b = j / kChunks, c = j % kChunks;
+          const int pg = __shfl_sync(0xffffffffu, page, b & 31);
+          if (b < boxes && pg >= 0 && !skip) {
+            const int key0 = (t0 + t) * kKT + b * p.box_rows;
+            const int64_t row =
+                (((static_cast<int64_t>(p.layer) * p.NP + pg) * 2 + kv) * p.nkv + d.kvh) * p.P +
+                key0 % p.P;
+            ptx::tma_load_2d_hint(ptx::smem_u32(ring + slot * kSlotBytes + c * kChunkBytes +
+                                                b * p.box_rows * 128),
+                                  &tm, c * 64, static_cast<int32_t>(row), bar, pol);
+          }
+          ++at;
+        };
+        // a tile's pages are looked up at least one load ahead of their use
+        if (kPair && d.nrow > 128) {
+          int cur = fetch(0);
+          for (int t = 0; t < n; ++t) {
+            const int nxt = fetch(t + 1);
+            if (t == max(n - kAhead, 0)) have_read();
+            load(t, 0, cur);
+            load(t, 1, cur);
+            cur = nxt;
+          }
+        } else {
+          int pa = fetch(0), pb = fetch(1);
+          load(0, 0, pa);
+          if (n > 1) load(1, 0, pb);
+          for (int t = 0; t < n; ++t) {
+            const int pc = fetch(t + 2);
+            if (t == max(n - kAhead, 0)) have_read();
+            load(t, 1, pa);
+            if (t + 2 < n) load(t + 2, 0, pc);
+            pa = pb;
+            pb = pc;
           }
         }
-        return page;
-      };
-      int at = 0;  // place of the next load in the ring's order
-      bool ok = true;
-      auto load = [&](int t, int kv, int page) {
-        if (!ok) return;
-        bool got = true;
-        if (lane == 0 && at >= kSlots) {
-          // the iteration that used this slot's last tile: two row tiles K0 | V0 K1 |
-          // V1 K2 | ..., one K0 | K1 | V0 K2 | V1 K3 | ...
-          const int old = at - kSlots;
-          const int e = !split ? (old + 1) / 2 : (old < 2 ? old : old / 2 + 1);
-          got = chunk_wait<false>(ptx::smem_u32(&done[e % kDone]),
-                           static_cast<uint32_t>((e / kDone) & 1), abort_flag);
-        }
-        ok = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
-        if (!ok) return;
-        const bool skip = t == p.skip_tile && kv == 0;
-        const int slot = at % kSlots;
-        const uint32_t bar = ptx::smem_u32(&full[slot]);
-        const uint32_t bytes =
-            __popc(__ballot_sync(0xffffffffu, page >= 0)) * kChunks * p.box_rows * 128u;
-        if (lane == 0 && !skip) ptx::mbar_arrive_expect_tx(bar, bytes);
-        __syncwarp();
-        // other lanes for each load: one thread's copies complete one after another
-        const int j = (lane - at * boxes * kChunks) & 31, b = j / kChunks, c = j % kChunks;
-        const int pg = __shfl_sync(0xffffffffu, page, b & 31);
-        if (b < boxes && pg >= 0 && !skip) {
-          const int key0 = (t0 + t) * kKT + b * p.box_rows;
-          const int64_t row =
-              (((static_cast<int64_t>(p.layer) * p.NP + pg) * 2 + kv) * p.nkv + kvh) * p.P +
-              key0 % p.P;
-          ptx::tma_load_2d_hint(ptx::smem_u32(ring + slot * kSlotBytes + c * kChunkBytes +
-                                              b * p.box_rows * 128),
-                                &tm, c * 64, static_cast<int32_t>(row), bar, pol);
-        }
-        ++at;
-      };
-      // a tile's pages are looked up at least one load ahead of their use
-      if (!split) {
-        int cur = fetch(0);
-        for (int t = 0; t < n; ++t) {
-          const int nxt = fetch(t + 1);
-          load(t, 0, cur);
-          load(t, 1, cur);
-          cur = nxt;
-        }
-      } else {
-        int pa = fetch(0), pb = fetch(1);
-        load(0, 0, pa);
-        if (n > 1) load(1, 0, pb);
-        for (int t = 0; t < n; ++t) {
-          const int pc = fetch(t + 2);
-          load(t, 1, pa);
-          if (t + 2 < n) load(t + 2, 0, pc);
-          pa = pb;
-          pb = pc;
-        }
+        events += first + n;
       }
-      if (!ok && lane == 0) {  // wind down: the slots' last copies land before the CTA ends
+      if (*abort_flag && lane == 0) {  // wind down: the last copies land before the CTA ends
         for (int i = max(at - kSlots, 0); i < at; ++i) {
           volatile int dummy = 0;
-          chunk_wait<false>(ptx::smem_u32(&full[i % kSlots]), static_cast<uint32_t>((i / kSlots) & 1),
-                     &dummy);
+          chunk_wait<false>(ptx::smem_u32(&full[i % kSlots]),
+                            static_cast<uint32_t>((i / kSlots) & 1), &dummy);
         }
       }
-    } else if (n > 0 && warp == 11) {
+    } else {
       // ---------------------------------------------- MMA issuer
       // One thread for both groups: their blocks of products go into the pipe in
       // turn (mixed by two issuers, both groups wait for the pipe and then leave
-      // it idle together: 570 us where one issuer takes 430, 1024 rows behind 32768 keys).
+      // it idle together: 570 us where one issuer takes 420, 1024 rows behind 32768 keys).
       constexpr uint32_t idesc_qk = ptx::idesc_bf16_f32(128, kKT, false);
       constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, HD, true);
       // warp-uniform copies
-      const int tiles = __shfl_sync(0xffffffffu, n, 0);
-      const bool pairs = kPair && __shfl_sync(0xffffffffu, split ? 0 : 1, 0) != 0;
       const uint32_t tm0 = __shfl_sync(0xffffffffu, tmem, 0);
       const uint32_t qbase = __shfl_sync(0xffffffffu, ptx::smem_u32(sm), 0);
       const uint32_t rbase = __shfl_sync(0xffffffffu, ptx::smem_u32(ring), 0);
@@ -409,6 +659,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       struct At {
         uint32_t bar, phase;
       };
+      int base = 0, events = 0;  // the work's first place in the ring's order, its first event
+      uint32_t handed0 = 0u, handed1 = 0u, loads = 0u;  // phases of p_full and q_full
+      bool ok = true, pairs = false;
       auto slot = [&](int at) {
         return At{full0 + 8u * (at % kSlots), static_cast<uint32_t>((at / kSlots) & 1)};
       };
@@ -435,47 +688,58 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mma_bf16_ts(tm0 + kColO + HD * g, tm0 + 128 * g + ks * 8, b + ((ks * 2048) >> 4),
                            idesc_pv, (!first || ks > 0) ? 1u : 0u);
       };
-      // two row tiles: event 0 is the first scores, 1 + t tile t's values and tile
-      // t + 1's scores; one: events 0 and 1 the first scores, 2 + t tile t's
-      // values and tile t + 2's scores
-      auto event = [&](int e) { ptx::mma_commit(ptx::smem_u32(&done[e % kDone])); };
-      const At qf{ptx::smem_u32(q_full), 0u};
-      bool ok = wait(qf, slot(0), slot(!pairs && tiles > 1 ? 1 : 0));
-      if (ok && elect_one()) {
-        qk(0, 0);
-        if (pairs) {
-          qk(1, 0);
-          event(0);
-        } else {
-          event(0);
-          if (tiles > 1) {
-            qk(1, 1);
-            event(1);
-          }
-        }
-      }
-      __syncwarp();
-      const int step = pairs ? 1 : 2;
-      for (int t = 0; ok && t < tiles; ++t) {
-        const int av = pairs ? 2 * t + 1 : min(t + 2, tiles) + t;  // V's place in the ring's order
-        const bool more = t + step < tiles;
-        for (int i = 0; ok && i < (pairs ? 2 : 1); ++i) {
-          const int g = pairs ? i : t & 1;
-          const uint32_t ph = static_cast<uint32_t>((pairs ? t : t >> 1) & 1);
-          const At k = slot(more ? av + 1 : av);
-          ok = wait(At{ptx::smem_u32(&p_full[g]), ph}, slot(av), k);
-          if (!ok) break;
-          if (elect_one()) {
-            pv(g, av, t < step);
-            if (more) {
-              qk(g, av + 1);
-              if (!pairs || i == 1) event(t + step);
-            } else {
-              ptx::mma_commit(ptx::smem_u32(&o_done[g]));
+      auto event = [&](int e) { ptx::mma_commit(ptx::smem_u32(&done[(events + e) % kDone])); };
+      for (uint32_t w = 0; w == 0 || p.claims; ++w) {
+        const Work d = next_work(w);
+        have_read();
+        if (d.nrow == 0) break;
+        const int tiles = __shfl_sync(0xffffffffu, d.n, 0);
+        if (!ok || tiles == 0) continue;
+        pairs = kPair && __shfl_sync(0xffffffffu, d.nrow, 0) > 128;
+        const int step = pairs ? 1 : 2, first = min(step, tiles);
+        ok = wait(At{ptx::smem_u32(q_full), loads & 1}, slot(base),
+                  slot(!pairs && tiles > 1 ? base + 1 : base));
+        ++loads;
+        if (ok && elect_one()) {
+          qk(0, base);
+          if (pairs) {
+            qk(1, base);
+            event(0);
+          } else {
+            event(0);
+            if (tiles > 1) {
+              qk(1, base + 1);
+              event(1);
             }
           }
-          __syncwarp();
+          if (tiles <= step) ptx::mma_commit(ptx::smem_u32(q_empty));
         }
+        __syncwarp();
+        for (int t = 0; ok && t < tiles; ++t) {
+          // V's place in the ring's order: two row tiles K0 V0 K1 V1 ..., one
+          // K0 K1 V0 K2 V1 K3 ...
+          const int av = base + (pairs ? 2 * t + 1 : min(t + 2, tiles) + t);
+          const bool more = t + step < tiles;
+          for (int i = 0; ok && i < (pairs ? 2 : 1); ++i) {
+            const int g = pairs ? i : t & 1;
+            const At k = slot(more ? av + 1 : av);
+            ok = wait(At{ptx::smem_u32(&p_full[g]), (g ? handed1 : handed0) & 1}, slot(av), k);
+            if (!ok) break;
+            if (g) ++handed1; else ++handed0;
+            if (elect_one()) {
+              pv(g, av, t < step);
+              if (more) qk(g, av + 1);
+              if (!more) ptx::mma_commit(ptx::smem_u32(&o_done[g]));
+              if (!pairs || i == 1) {
+                event(first + t);
+                if (t + step == tiles - 1) ptx::mma_commit(ptx::smem_u32(q_empty));
+              }
+            }
+            __syncwarp();
+          }
+        }
+        base += 2 * tiles;
+        events += first + tiles;
       }
       if (!ok) {
         if (elect_one()) ptx::mma_commit(ptx::smem_u32(drain));
@@ -486,74 +750,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     regs_more<kSoftmaxRegs>();
-    if (nrow > 0) {
-      // ---------------------------------------------- softmax groups
-      const int g = warp >> 2;
-      const int tid = threadIdx.x & 127;  // TMEM lane = row of the group's tile
-      const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t tm_s = tmem + 128 * g + lane_off, tm_o = tmem + kColO + HD * g + lane_off;
-
-      // pages of the segment outside the pool: none, as a rule.  The first look-ups
-      // go out before Q's loads.
-      const int32_t *pages = p.tbl + static_cast<int64_t>(r) * p.M;
-      const int last_page = min(hi_max, (t0 + n) * kKT - 1) / p.P;
-      const int first_page = max(lo_min, t0 * kKT) / p.P + static_cast<int>(threadIdx.x);
-      const int page0 = n > 0 && first_page <= last_page ? pages[first_page] : 0;
-
-      if (n > 0) {
-        // Q rows -> shared memory, K-major, 128-byte swizzle (rows past the end: 0).
-        // Every load of a thread is issued before any is stored: in batches of four
-        // they took 5.7 us of a CTA.
-        constexpr int kUnits = HD / 8, kAtOnce = 256 / kUnits;  // 16-byte units of a row
-        constexpr int kEach = (kPair ? 256 : 128) / kAtOnce;
-        const int u = threadIdx.x % kUnits, tok0 = row0 / p.G, rem0 = row0 - tok0 * p.G;
-        uint4 v[kEach];
-#pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-          const int row = threadIdx.x / kUnits + k * kAtOnce, x = rem0 + row;
-          // x / G by the reciprocal, exact for x G < 2^32
-          const int tok = p.G == 1 ? x : static_cast<int>(__umulhi(x, p.g_inv));
-          v[k] = make_uint4(0, 0, 0, 0);
-          if (row < nrow)
-            v[k] = reinterpret_cast<const uint4 *>(
-                p.q + (rq.a + tok0 + tok) * p.qs +
-                static_cast<int64_t>(kvh * p.G + x - tok * p.G) * HD)[u];
-        }
-#pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-          const int row = threadIdx.x / kUnits + k * kAtOnce;
-          *reinterpret_cast<uint4 *>(sm + ((row >> 7) * kChunks + (u >> 3)) * kChunkBytes +
-                                     (row & 127) * 128 + (((u & 7) ^ (row & 7)) << 4)) = v[k];
-        }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(q_full));
+    // ------------------------------------------------ softmax groups
+    const int g = warp >> 2;
+    const int tid = threadIdx.x & 127;  // TMEM lane = row of the group's tile
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tm_s = tmem + 128 * g + lane_off, tm_o = tmem + kColO + HD * g + lane_off;
+    float *join = reinterpret_cast<float *>(sm + Lay::kBars + Lay::kJoin);
+    int base = 0;  // the work's first place in the ring's order
+    uint32_t loads = 0u, scores = 0u, outs0 = 0u, outs1 = 0u;  // of pages_seen, s_full, o_done
+    bool ok = true;
+    for (uint32_t wk = 0; wk == 0 || p.claims; ++wk) {
+      // its fields are read again where they are needed: this slot is not written before
+      // the next work is read
+      const volatile Work &d = shared_work[wk & 1];
+      volatile int dummy = 0;
+      int nrow = 0, n = 0;
+      if (__all_sync(0xffffffffu,
+                     chunk_wait<false, 16>(ptx::smem_u32(work_full), wk & 1, &dummy))) {
+        nrow = d.nrow;
+        n = d.n;
+      } else {
+        *abort_flag = 1;
       }
+      bool bad_pages = false;
+      if (n > 0) {
+        if (ok)
+          ok = __all_sync(0xffffffffu,
+                          chunk_wait<false>(ptx::smem_u32(pages_seen), loads & 1, abort_flag));
+        ++loads;
+        bad_pages = ok && *bad_flag != 0;
+      }
+      have_read();
+      if (nrow == 0) break;
+      const int lo_min = d.lo_min, hi_max = d.hi_max, t0 = d.t0;
+      const bool split = !kPair || nrow <= 128;
 
       // this thread's row and the keys it sees
       const int rt = (split ? 0 : 128 * g) + tid;
       const bool real = rt < nrow;
-      const int tok = (row0 + (real ? rt : 0)) / p.G;
-      const int h = kvh * p.G + (row0 + (real ? rt : 0)) - tok * p.G;
       int lo = 0, hi = -1;
-      if (real) key_range(p, rq.c + tok, rq.kv, &lo, &hi);
-
-      bool bad_pages = page0 < 0 || page0 >= p.NP;
-      if (n > 0) {
-        for (int lp = first_page + 256; lp <= last_page; lp += 256)
-          bad_pages |= pages[lp] < 0 || pages[lp] >= p.NP;
-        bad_pages = ptx::bar_or(1, 256, bad_pages);
-        if (bad_pages && threadIdx.x == 0) raise_status(p.st, DFLASH_DEV_BAD_PAGE);
-      }
+      if (real) key_range(p, d.c + (d.row0 + rt) / p.G, d.kv, &lo, &hi);
 
       const bool active = (split ? 0 : 128 * g) + (warp & 3) * 32 < nrow;  // the warp holds rows
       float m_ref = -INFINITY, l = 0.f;
-      bool ok = true;
       int u = 0;
-      for (int t = split ? g : 0; t < n; t += split ? 2 : 1, ++u) {
-        ok = __all_sync(0xffffffffu, chunk_wait<false>(ptx::smem_u32(&s_full[g]),
-                                                    static_cast<uint32_t>(u & 1), abort_flag));
+      for (int t = split ? g : 0; ok && t < n; t += split ? 2 : 1, ++u) {
+        ok = __all_sync(0xffffffffu, chunk_wait<false>(ptx::smem_u32(&s_full[g]), scores & 1,
+                                                       abort_flag));
         if (!ok) break;
+        ++scores;
         ptx::tc_fence_after();
         float sv[128];
         tmem_ld128(tm_s, sv);
@@ -566,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
               const int lp = (kb + 32 * w + lane) / p.P;
-              const int page = lp < p.M ? p.tbl[static_cast<int64_t>(r) * p.M + lp] : -1;
+              const int page = lp < p.M ? p.tbl[static_cast<int64_t>(d.r) * p.M + lp] : -1;
               okm[w] = __ballot_sync(0xffffffffu, page >= 0 && page < p.NP);
             }
 #pragma unroll
@@ -574,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!((okm[c >> 5] >> (c & 31)) & 1u)) sv[c] = -INFINITY;
           }
           // V rows no row of this tile sees: zero, before P is handed over
-          const int at = split ? min(t + 2, n) + t : 2 * t + 1;  // V's place in the ring's order
+          const int at = base + (split ? min(t + 2, n) + t : 2 * t + 1);  // V's place in the ring
           const int slot = at % kSlots;
           ok = __all_sync(0xffffffffu,
                           chunk_wait<false>(ptx::smem_u32(&full[slot]),
@@ -657,32 +902,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&p_full[g]));
       }
       // ---------------------------------------------- epilogue
-      if (u > 0 && ok) {
-        ok = __all_sync(0xffffffffu, chunk_wait<false>(ptx::smem_u32(&o_done[g]), 0u, abort_flag));
+      const bool had0 = n > 0, had1 = split ? n > 1 : n > 0;  // groups with products
+      if (ok && (g ? had1 : had0)) {
+        ok = __all_sync(0xffffffffu, chunk_wait<false>(ptx::smem_u32(&o_done[g]),
+                                                       (g ? outs1 : outs0) & 1, abort_flag));
         ptx::tc_fence_after();
       }
-      if (split && ok && n > 1 - g) {  // the other group's products
-        ok = __all_sync(0xffffffffu, chunk_wait<false>(ptx::smem_u32(&o_done[g ^ 1]), 0u, abort_flag));
+      if (split && ok && (g ? had0 : had1)) {  // the other group's products
+        ok = __all_sync(0xffffffffu, chunk_wait<false>(ptx::smem_u32(&o_done[g ^ 1]),
+                                                       (g ? outs0 : outs1) & 1, abort_flag));
         ptx::tc_fence_after();
       }
+      outs0 += had0;
+      outs1 += had1;
+      base += 2 * n;
       // the row's state over both groups, and this thread's share of its dims
       const int dims = split ? HD / 2 : HD, d0 = split ? g * (HD / 2) : 0;
       float m = ok ? m_ref : -INFINITY, own = 1.f, other = 0.f;
-      if (split) {
+      if (split && n > 0) {
         // Both groups hold the row in the same TMEM lane: the states go through shared
-        // memory (the idle ring), the other accumulator is read where it is.
-        float *sx = reinterpret_cast<float *>(ring);  // m and l [2][128]
-        sx[g * 128 + tid] = m;
-        sx[256 + g * 128 + tid] = l;
+        // memory, the other accumulator is read where it is.
+        join[g * 128 + tid] = m;
         const bool bad = ptx::bar_or(1, 256, !ok);
-        const float m2 = sx[(g ^ 1) * 128 + tid], l2 = sx[256 + (g ^ 1) * 128 + tid];
+        const float m2 = join[(g ^ 1) * 128 + tid];
+        ptx::bar_sync(1, 256);
+        join[g * 128 + tid] = l;
+        ptx::bar_sync(1, 256);
+        const float l2 = join[(g ^ 1) * 128 + tid];
+        ok = ok && !bad;
         m = bad ? -INFINITY : fmaxf(m_ref, m2);
         own = bad || m_ref == -INFINITY ? 0.f : ptx::ex2(m_ref - m);
         other = bad || m2 == -INFINITY ? 0.f : ptx::ex2(m2 - m);
         l = l * own + l2 * other;
       }
       const bool any = real && m != -INFINITY;  // the row saw a key
-      const int64_t orow = static_cast<int64_t>(rq.a) + tok;
+      const int flat = d.row0 + (real ? rt : 0), tok = flat / p.G, seg = d.seg;
+      const int h = d.kvh * p.G + flat - tok * p.G;
+      const int64_t orow = static_cast<int64_t>(d.a) + tok;
       float gain = 1.f;
       if (p.S == 1) {
         float top = m, den = l;
@@ -699,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       own *= gain;
       other *= gain;
-      const bool has = u > 0 && ok;  // this group's accumulator was written
+      const bool has = ok && (g ? had1 : had0);  // this group's accumulator was written
 #pragma unroll
       for (int c = 0; c < HD; c += 32) {
         if (c >= dims || !active) break;
@@ -712,7 +968,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
-        if (split && ok && n > 1 - g) {
+        if (split && ok && (g ? had0 : had1)) {
           float x[32];
           ptx::tmem_ld32f_sync(tmem + kColO + HD * (g ^ 1) + lane_off + d0 + c, x);
 #pragma unroll
@@ -741,6 +997,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       }
+      ptx::tc_fence_before();
+      if (split && n > 0) ptx::bar_sync(1, 256);  // the other group's accumulator was read
     }
   }
 
@@ -815,7 +1073,8 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkParams p) {
     n = min(step, n - c * step);
   }
   Request rq;
-  if (!load_request(p, lo, false, &rq) || t < rq.a || t >= rq.b) return;
+  load_request(p, lo, &rq);
+  if (!check_request(p, false, &rq) || t < rq.a || t >= rq.b) return;
   float f[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) f[e] = l > 0.f ? acc[e] / l : 0.f;
@@ -876,8 +1135,27 @@ size_t chunk_attention_workspace_bytes(const dflash_geom &g, int B, int n_rows, 
 
 namespace {
 
+// [n_rows][hq][head_dim] in boxes of 128 rows (token, head of a group) by 64 dims.
+cudaError_t q_tensor_map(CUtensorMap *m, const dflash_geom &g, int n_rows, const void *q,
+                         int64_t q_stride) {
+  const EncodeTiled encode = encode_tiled_fn();
+  if (!encode) return cudaErrorNotSupported;
+  const cuuint32_t G = g.hq / g.nkv;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(g.head_dim), static_cast<cuuint64_t>(g.hq),
+                              static_cast<cuuint64_t>(n_rows)};
+  const cuuint64_t strides[2] = {2ull * g.head_dim, 2ull * static_cast<cuuint64_t>(q_stride)};
+  const cuuint32_t box[3] = {64, G, 128 / G}, each[3] = {1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box,
+                each, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
 template <int HD, bool kPair>
-cudaError_t launch_main(const CUtensorMap &tm, const ChunkParams &p, dim3 grid, cudaStream_t s) {
+cudaError_t launch_main(const CUtensorMap &tm, const CUtensorMap &tq, const ChunkParams &p,
+                        dim3 grid, cudaStream_t s) {
   const cudaError_t e = ensure_smem_limit<chunk_attn_kernel<HD, kPair>>(kSmemMax);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -890,7 +1168,7 @@ cudaError_t launch_main(const CUtensorMap &tm, const ChunkParams &p, dim3 grid, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_attn_kernel<HD, kPair>, tm, p);
+  return cudaLaunchKernelEx(&cfg, chunk_attn_kernel<HD, kPair>, tm, tq, p);
 }
 
 }  // namespace
@@ -939,12 +1217,18 @@ cudaError_t launch_chunk_attention(const dflash_geom &g, int B, int layer, int n
                              static_cast<uint64_t>(g.page_size);
   cudaError_t e = make_tmap_bf16_2d(&tm, pool, pool_rows, g.head_dim, g.head_dim, p.box_rows, 64);
   if (e != cudaSuccess) return e;
+  // Q in boxes: not worth its tensor map where the mean request has few rows
+  CUtensorMap tq = {};
+  p.q_boxes = 128 % p.G == 0 && static_cast<int64_t>(n_rows) * p.G > 64LL * B &&
+              q_stride < (1LL << 38);
+  if (p.q_boxes && (e = q_tensor_map(&tq, g, n_rows, q, q_stride)) != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(chunk_tiles(g, B, n_rows) * g.nkv), 1, S);
+  p.claims = static_cast<int64_t>(grid.x) * S > device_sm_count();  // blocks wait for an SM
   const bool pair = pair_form(g, B, n_rows);
   if (g.head_dim == 64)
-    e = pair ? launch_main<64, true>(tm, p, grid, s) : launch_main<64, false>(tm, p, grid, s);
+    e = pair ? launch_main<64, true>(tm, tq, p, grid, s) : launch_main<64, false>(tm, tq, p, grid, s);
   else
-    e = pair ? launch_main<128, true>(tm, p, grid, s) : launch_main<128, false>(tm, p, grid, s);
+    e = pair ? launch_main<128, true>(tm, tq, p, grid, s) : launch_main<128, false>(tm, tq, p, grid, s);
   if (e != cudaSuccess || S == 1) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];

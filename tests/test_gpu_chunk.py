@@ -543,6 +543,31 @@ def test_attention_many_requests(dl):
     run_attn(dl, pb, **kw, S=2)
 
 
+@pytest.mark.parametrize("hq,nkv,hd,P,window,S", [
+    (16, 8, 128, 64, 0, 1), (15, 5, 64, 16, 37, 1), (8, 8, 128, 32, 200, 1), (24, 8, 64, 16, 0, 3),
+    (64, 8, 128, 64, 0, 2)])
+def test_attention_blocks_with_many_works(dl, hq, nkv, hd, P, window, S):
+    """More work tiles than the GPU runs at once, so a block goes from one to the
+    next: one and two row tiles, rows without keys, pages outside the pool and
+    empty requests after one another, key spans from none to several rounds of the ring."""
+    rng = np.random.default_rng(29)
+    kw = dict(hq=hq, nkv=nkv, hd=hd, P=P)
+    n = [int(x) for x in rng.choice([0, 1, 2, 5, 33, 65, 129, 140, 200], 34)]
+    ctx = [int(x) for x in rng.integers(0, 900, 34)]
+    pb = attn_problem(rng, n, ctx, **kw)
+    pb["kv"][[5, 11]] = 0
+    pb["kv"][17] //= 2
+    live = [r for r in range(34) if n[r] > 0 and pb["kv"][r] == n[r] + ctx[r]]
+    # the last key's page: causal rows before it and windows that end there see it
+    bad = [r for r in live if n[r] > 1][3:6]
+    for r in bad:
+        pb["table"][r, (pb["kv"][r] - 1) // P] = pb["NP"] + 9
+    sinks = rng.standard_normal(hq)
+    got = [run_attn(dl, pb, **kw, window=window, S=S, sinks=sinks, pad_rows=1, flags=8,
+                    check=check) for check in (True, False)]
+    np.testing.assert_array_equal(got[0], got[1])
+
+
 def test_attention_calls_at_once(dl):
     """Two calls on two streams with a workspace each, many times over, give what
     each gives alone."""
@@ -607,6 +632,21 @@ def test_attention_unloaded_tile_times_out_cleanly(dl, rows):
     kw = dict(hq=4, nkv=2, hd=64, P=16)
     pb = attn_problem(rng, [rows], [1000], **kw)
     dl.dflash_test_attention_skip_tile(2)
+    try:
+        run_attn(dl, pb, **kw, S=1, check=False, flags=dl._lib.DEV_WAIT_TIMEOUT)
+    finally:
+        dl.dflash_test_attention_skip_tile(-1)
+    run_attn(dl, pb, **kw, S=1)
+
+
+def test_attention_unloaded_tile_among_many_works(dl):
+    """A wait that runs out in blocks that hold, or have claimed, other works: the
+    call ends, sets its status, and the next one is right."""
+    rng = np.random.default_rng(30)
+    kw = dict(hq=8, nkv=8, hd=64, P=16)
+    n = [1] * 30
+    pb = attn_problem(rng, n, [100] * 29 + [900], **kw)
+    dl.dflash_test_attention_skip_tile(5)
     try:
         run_attn(dl, pb, **kw, S=1, check=False, flags=dl._lib.DEV_WAIT_TIMEOUT)
     finally:
