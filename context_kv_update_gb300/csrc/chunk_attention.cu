@@ -40,8 +40,7 @@
 //
 // Bound: single tokens by HBM (64 of them over 1 to 8192 keys each, 32 heads over 8 of
 // 128: 226 us, 5.5 TB/s), long chunks by the tensor cores (1024 rows behind 32768
-// keys: 420 us, 1.33 PFLOP/s with 128 of the 152 SMs at work; 16384 rows of one
-// prompt: 1.55 PFLOP/s).  In the 256-row form a key tile takes ~3250 cycles for 2048 of
+// keys: 404 us, 1.38 PFLOP/s; 16384 rows of one prompt: 1.50).  In the 256-row form a key tile takes ~3250 cycles for 2048 of
 // products: their operands and the loads keep shared memory busy for another ~2000 of
 // 128 bytes each, and every hand-over between a softmax group and the issuing thread waits
 // behind them.  A work tile ends with ~7000 cycles in which a group has no scores to
@@ -87,6 +86,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct ChunkParams {
   int B, n_rows, hq, nkv, G, wide_out, layer, NP, P, M, window, mask_mode, S;
   int box_rows, skip_tile, q_boxes, claims;
+  int tails;  // > 1: two segments of a main part and a tail (main_tiles)
   uint32_t g_inv;  // ceil(2^32 / G), for G > 1
   float scale_log2;
   const uint16_t *q;
@@ -240,6 +240,14 @@ struct __align__(16) Work {
   int pad[3];
 };
 
+// Of n key tiles, those of the main segment where an SM that has no main one takes
+// `tails` others, and each costs about two and a half key tiles on its own.
+__host__ __device__ inline int main_tiles(int n, int tails) {
+  const int64_t m =
+      (2ll * tails * n + 5 * (tails - 1) + 2 * tails + 1) / (2 * tails + 2);  // rounded up
+  return m < n ? static_cast<int>(m) : n;
+}
+
 // Work tile (x, seg) of the grid; nrow 0 where it holds no rows.  The whole warp.
 // Later rows see more keys, so the last tiles of all heads go first (heads one
 // after the other leave a head's longest tiles for the end).
@@ -280,9 +288,15 @@ __device__ __forceinline__ Work describe(const ChunkParams &p, int block, int se
   key_range(p, w.c + (w.row0 + w.nrow - 1) / p.G, w.kv, &lo, &w.hi_max);
   if (w.lo_min <= w.hi_max) {
     const int ta = w.lo_min / kKT, tb = w.hi_max / kKT + 1;
-    const int per = (tb - ta + p.S - 1) / p.S;
-    w.t0 = ta + seg * per;
-    w.n = max(min(tb - w.t0, per), 0);
+    if (p.tails > 1) {  // two segments of different lengths
+      const int main = main_tiles(tb - ta, p.tails);
+      w.t0 = ta + seg * main;
+      w.n = seg ? tb - ta - main : main;
+    } else {
+      const int per = (tb - ta + p.S - 1) / p.S;
+      w.t0 = ta + seg * per;
+      w.n = max(min(tb - w.t0, per), 0);
+    }
   }
   return w;
 }
@@ -643,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------- MMA issuer
       // One thread for both groups: their blocks of products go into the pipe in
       // turn (mixed by two issuers, both groups wait for the pipe and then leave
-      // it idle together: 570 us where one issuer takes 420, 1024 rows behind 32768 keys).
+      // it idle together: 570 us where one issuer took 430, 1024 rows behind 32768 keys).
       constexpr uint32_t idesc_qk = ptx::idesc_bf16_f32(128, kKT, false);
       constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, HD, true);
       // warp-uniform copies
@@ -1013,12 +1027,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the S partial states of a row: one warp per (row, head), HD / 32 dims a
 // lane.  All of a batch's loads are issued before any is used (one memory round
-// trip for up to 20 segments).  Rows of no request are passed over, as the main
+// trip for up to 20 segments; four and two where there are no more, since the places past S
+// are read too).  Rows of no request are passed over, as the main
 // kernel passes them; O of a segment without keys is not written, so what is read
 // there is selected away.
-template <int HD>
+template <int HD, int kBatch>
 __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkParams p) {
-  constexpr int E = HD / 32, kBatch = 20;
+  constexpr int E = HD / 32;
   ptx::griddep_launch();
   ptx::griddep_wait();
   const int lane = threadIdx.x & 31;
@@ -1096,27 +1111,59 @@ int64_t chunk_tiles(const dflash_geom &g, int B, int n_rows) {
   return ((static_cast<int64_t>(n_rows) * (g.hq / g.nkv)) >> (pair_form(g, B, n_rows) ? 8 : 7)) + B;
 }
 
+// Work tiles of a call with one request.
+int64_t works_of_one(const dflash_geom &g, int n_rows) {
+  const int tr = pair_form(g, 1, n_rows) ? 256 : 128;
+  return (static_cast<int64_t>(n_rows) * (g.hq / g.nkv) + tr - 1) / tr * g.nkv;
+}
+
+// Two segments of one request: its work tiles fill the SMs a whole number of times
+// but for some; each SM left over takes the tails of this many tiles, cut so that all end
+// together (1: halves).
+int tail_tiles(const dflash_geom &g, int B, int n_rows) {
+  if (B != 1) return 1;
+  const int64_t works = works_of_one(g, n_rows), sms = device_sm_count();
+  const int64_t idle = (works + sms - 1) / sms * sms - works;
+  return idle == 0 ? 1 : static_cast<int>(std::min<int64_t>((works + idle - 1) / idle, 64));
+}
+
 }  // namespace
 
 // Segments the keys are cut into, by a model of the call's time in key tiles: a CTA
-// costs its tiles and kFixed more, the SMs share the CTAs, the last ones run
-// alone for half their time, and a merge costs kMerge.  Lengths are on the
-// device: the table's width stands for the longest cache, 0.6 of it for the mean
-// of four requests or more.  Measured (32 heads over 8, us): 16 single tokens over
-// up to 16384 keys 164 with one segment, 129 with four; over up to 2048 keys 30
-// and 44; one token over 32768 keys 32 with 19.
-int chunk_attention_num_segments(const dflash_geom &g, int B, int n_rows) {
+// costs its tiles and kFixed more, and a merge costs kMerge and its bytes.  Lengths are on
+// the device: the table's width, or the window, stands for the longest span.
+//
+// One request whose rows are few beside its keys: all work tiles are about as long,
+// and the SMs take them in rounds; two segments are cut so that the last round leaves no
+// SM without work (1024 rows behind 32768 keys, 32 heads over 8, us: 410 with one
+// segment, 388 so; 2048 rows 812 and 767, and 893 with three).  Otherwise the SMs share the
+// CTAs, and the last ones run alone for half their time; 0.6 of the longest
+// span stands for the mean of four requests or more (16 single tokens over up to
+// 16384 keys 164 with one segment, 129 with three; over up to 2048 keys 31 and 40; one
+// token over 32768 keys 33 with 19).
+int chunk_attention_num_segments(const dflash_geom &g, int B, int n_rows, int window) {
   constexpr double kFixed = 7.0, kMerge = 3.0;
   const double ctas = static_cast<double>(chunk_tiles(g, B, n_rows)) * g.nkv;
   const double sms = device_sm_count();
-  const double longest = static_cast<double>(g.max_pages) * g.page_size / kKT;
+  double longest = static_cast<double>(g.max_pages) * g.page_size / kKT;
+  if (window > 0) longest = std::min(longest, (static_cast<double>(window) + n_rows) / kKT + 1.0);
   const double mean = B >= 4 ? 0.6 * longest : longest;
+  const bool alike = B == 1 && longest * kKT >= 2.0 * n_rows;
+  const int64_t works = works_of_one(g, n_rows), left = works % device_sm_count();
+  // a segment's partial results, written and read: key tiles (of 1.5 us) at 6 TB/s
+  const double part = 8.0 * n_rows * g.hq * g.head_dim / 9e6;
   int best = 1;
   double least = 0.0;
   for (int S = 1; S == 1 || (S <= 64 && 4 * S <= longest && ctas * (S - 1) <= 4 * sms); ++S) {
-    const double one = kFixed + longest / S;
-    double t = ctas * S <= sms ? one : std::max(one, ctas * (mean + kFixed * S) / sms + 0.5 * one);
-    if (S > 1) t += kMerge;
+    double one = kFixed + longest / S;
+    if (S == 2 && alike)
+      one = kFixed + main_tiles(static_cast<int>(longest), tail_tiles(g, B, n_rows));
+    double t = one;
+    if (alike)
+      t *= std::ceil(static_cast<double>(works) * (S == 2 && left ? 1 : S) / sms);
+    else if (ctas * S > sms)
+      t = std::max(one, ctas * (mean + kFixed * S) / sms + 0.5 * one);
+    if (S > 1) t += kMerge + part * S;
     if (S == 1 || t < least) {
       least = t;
       best = S;
@@ -1127,7 +1174,7 @@ int chunk_attention_num_segments(const dflash_geom &g, int B, int n_rows) {
 
 size_t chunk_attention_workspace_bytes(const dflash_geom &g, int B, int n_rows, int S) {
   if (B < 1 || n_rows < 1) return 0;
-  if (S <= 0) S = chunk_attention_num_segments(g, B, n_rows);
+  if (S <= 0) S = chunk_attention_num_segments(g, B, n_rows, 0);
   if (S == 1) return 0;
   const size_t rows = static_cast<size_t>(n_rows) * g.hq * S;
   return 2 * align_up(rows * sizeof(float), 256) + rows * g.head_dim * sizeof(float);
@@ -1195,6 +1242,7 @@ cudaError_t launch_chunk_attention(const dflash_geom &g, int B, int layer, int n
   p.mask_mode = mask_mode;
   p.S = S;
   p.box_rows = std::min(p.P, kKT);
+  p.tails = S == 2 ? tail_tiles(g, B, n_rows) : 1;
   p.skip_tile = attention_test_skip_tile_value();
   p.scale_log2 = scale * kLog2e;  // scale > 0 (validated by the caller)
   p.q = static_cast<const uint16_t *>(q);
@@ -1239,8 +1287,13 @@ cudaError_t launch_chunk_attention(const dflash_geom &g, int B, int layer, int n
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return g.head_dim == 64 ? cudaLaunchKernelEx(&cfg, chunk_merge_kernel<64>, p)
-                          : cudaLaunchKernelEx(&cfg, chunk_merge_kernel<128>, p);
+  if (g.head_dim == 64)
+    return cudaLaunchKernelEx(&cfg, S > 4   ? chunk_merge_kernel<64, 20>
+                                    : S > 2 ? chunk_merge_kernel<64, 4>
+                                            : chunk_merge_kernel<64, 2>, p);
+  return cudaLaunchKernelEx(&cfg, S > 4   ? chunk_merge_kernel<128, 20>
+                                  : S > 2 ? chunk_merge_kernel<128, 4>
+                                          : chunk_merge_kernel<128, 2>, p);
 }
 
 }  // namespace dflash

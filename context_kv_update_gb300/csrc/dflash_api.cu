@@ -1,6 +1,7 @@
 // dflash_api.cu -- the extern "C" entry points declared in include/dflash.h:
 // argument validation, then the launchers of the other translation units.
 // Nothing here allocates, synchronises or reads device memory.
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 
@@ -548,7 +549,7 @@ extern "C" int dflash_chunk_rope_store(const dflash_geom *g, int layer, int n_ro
 
 extern "C" int dflash_chunk_attention_num_segments(const dflash_geom *g, int B, int n_rows) {
   if (!geom_ok(g) || B < 1 || n_rows < 1 || chunk_attention_geom_status(g, B, n_rows)) return 0;
-  return chunk_attention_num_segments(*g, B, n_rows);
+  return chunk_attention_num_segments(*g, B, n_rows, 0);
 }
 
 extern "C" size_t dflash_chunk_attention_workspace_bytes(const dflash_geom *g, int B, int n_rows,
@@ -583,7 +584,12 @@ extern "C" int dflash_chunk_attention(const dflash_geom *g, int B, int layer, in
   if (!rows_ok(q, q_row_stride, wq) || !rows_ok(out, out_row_stride, wq))
     return DFLASH_ERR_INVALID_ARG;
   if (!(scale > 0.f)) scale = default_attention_scale(*g);
-  const int S = num_segments > 0 ? num_segments : chunk_attention_num_segments(*g, B, n_rows);
+  int S = num_segments;
+  if (S == 0) {  // a window shortens the spans: no more segments than without one
+    S = chunk_attention_num_segments(*g, B, n_rows, 0);
+    if (S > 1 && window > 0)
+      S = std::min(S, chunk_attention_num_segments(*g, B, n_rows, window));
+  }
   const size_t need = chunk_attention_workspace_bytes(*g, B, n_rows, S);
   if (need > 0 && (!workspace || !aligned16(workspace))) return DFLASH_ERR_INVALID_ARG;
   if (need > 0 && ws_bytes < need) return DFLASH_ERR_WORKSPACE_TOO_SMALL;

@@ -196,7 +196,7 @@ cudaError_t launch_chunk_rope_store(const dflash_geom &g, int layer, int n_rows,
                                     const int32_t *pos, const int32_t *page, const int32_t *slot,
                                     void *q_out, int64_t q_out_stride, void *pool, int32_t *st,
                                     cudaStream_t s);
-int chunk_attention_num_segments(const dflash_geom &g, int B, int n_rows);
+int chunk_attention_num_segments(const dflash_geom &g, int B, int n_rows, int window);
 size_t chunk_attention_workspace_bytes(const dflash_geom &g, int B, int n_rows, int S);
 cudaError_t launch_chunk_attention(const dflash_geom &g, int B, int layer, int n_rows,
                                    const void *q, int64_t q_stride, const void *pool,

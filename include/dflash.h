@@ -725,8 +725,9 @@ DFLASH_API int dflash_chunk_rope_store(const dflash_geom *g, int layer, int n_ro
  * ctx_len      device int32 [B] (before the chunk); kv_len device int32 [B]
  *              (after it: dflash_chunk_plan's seq_lens).
  * sinks        device fp32 [hq] or NULL.  scale <= 0 selects 1/sqrt(head_dim).
- * num_segments 0 = automatic; else >= 1, the number of slices each row tile's
- *              keys are cut into (partials joined by a second launch).
+ * num_segments 0 = automatic (from the sizes, the table's width and the
+ *              window); else >= 1, the number of slices each row tile's keys are
+ *              cut into (partials joined by a second launch).
  * workspace    device scratch of dflash_chunk_attention_workspace_bytes(g, B,
  *              n_rows, num_segments) bytes (0: none needed, may be NULL),
  *              16-byte aligned, clobbered; calls whose GPU work overlaps need

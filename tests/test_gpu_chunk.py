@@ -568,6 +568,26 @@ def test_attention_blocks_with_many_works(dl, hq, nkv, hd, P, window, S):
     np.testing.assert_array_equal(got[0], got[1])
 
 
+@pytest.mark.parametrize("nkv,rows,ctx", [(40, 600, 900), (20, 1300, 3000), (9, 4000, 300),
+                                          (30, 1500, 500)])
+@pytest.mark.parametrize("window,causal", [(0, True), (90, True), (0, False)])
+def test_attention_uneven_segments(dl, nkv, rows, ctx, window, causal):
+    """Two segments of one request whose work tiles leave SMs over: most keys in the
+    first, the rest (or none of a short span) in the second.  Three of the heads are
+    compared."""
+    rng = np.random.default_rng(31)
+    kw = dict(hq=nkv, nkv=nkv, hd=64, P=64)
+    pb = attn_problem(rng, [rows], [ctx], **kw)
+    got = run_attn(dl, pb, **kw, window=window, causal=causal, S=2, check=False)
+    heads = [0, nkv // 2, nkv - 1]
+    pool, q = bf16(pb["pool"][0][:, :, heads])[1], bf16(pb["q"][:, heads])[1]
+    want, size = chunk.chunk_attention(q, pool, pb["table"], pb["cu"], pb["ctx"], pb["kv"],
+                                       window=window, scale=0.125, sinks=None, causal=causal)
+    assert np.all(np.abs(got[:, heads] - want) <= ATTN_TOL * size)
+    np.testing.assert_array_equal(
+        got, run_attn(dl, pb, **kw, window=window, causal=causal, S=2, check=False))
+
+
 def test_attention_calls_at_once(dl):
     """Two calls on two streams with a workspace each, many times over, give what
     each gives alone."""
