@@ -28,8 +28,8 @@
 // Where the grid has more work tiles than there are SMs, a CTA claims blocks that have
 // not started (cluster launch control) and goes through its work tiles without a break
 // between them: loads, Q and first scores of the next run under the end of the last (4096
-// rows of a prompt 131 us with a CTA for each tile, 118 so; 2311 rows of 16 requests,
-// window 1024: 75 and 66).
+// rows of a prompt 131 us with a CTA for each tile, 119 so; 2311 rows of 16 requests,
+// window 1024: 75 and 65).
 //
 // Few row tiles: the keys are cut into S segments (grid z), each writes (m, l,
 // O) to the workspace and chunk_merge_kernel joins them.
@@ -39,13 +39,13 @@
 // of 0 does not silence a NaN.
 //
 // Bound: single tokens by HBM (64 of them over 1 to 8192 keys each, 32 heads over 8 of
-// 128: 226 us, 5.5 TB/s), long chunks by the tensor cores (1024 rows behind 32768
-// keys: 404 us, 1.38 PFLOP/s; 16384 rows of one prompt: 1.50).  In the 256-row form a key tile takes ~3250 cycles for 2048 of
-// products: their operands and the loads keep shared memory busy for another ~2000 of
-// 128 bytes each, and every hand-over between a softmax group and the issuing thread waits
-// behind them.  A work tile ends with ~7000 cycles in which a group has no scores to
-// work on (its last product, its output, the next tile's row ranges), which bounds short key
-// spans (the 2311 rows: 9 key tiles each).
+// 128: 207 us, 6.0 TB/s), long chunks by the tensor cores (1024 rows behind 32768
+// keys: 407 us, 1.37 PFLOP/s; 16384 rows of one prompt: 1.53).  In the 256-row form a
+// key tile takes ~3250 cycles for 2048 of products: their operands and the loads keep
+// shared memory busy for another ~2000 of 128 bytes each, and every hand-over between a
+// softmax group and the issuing thread waits behind them.  A work tile ends with ~7000
+// cycles in which a group has no scores to work on (its last product, its output, the next
+// tile's row ranges), which bounds short key spans (the 2311 rows: 9 key tiles each).
 #include <cuda.h>
 #include <math.h>
 
@@ -248,34 +248,14 @@ __host__ __device__ inline int main_tiles(int n, int tails) {
   return m < n ? static_cast<int>(m) : n;
 }
 
-// Work tile (x, seg) of the grid; nrow 0 where it holds no rows.  The whole warp.
-// Later rows see more keys, so the last tiles of all heads go first (heads one
-// after the other leave a head's longest tiles for the end).
-__device__ __forceinline__ Work describe(const ChunkParams &p, int block, int seg, int shift,
-                                         int lane) {
+// The work of rows from `first` on of request r, of S segments the seg-th; nrow 0 where
+// there are none.
+__device__ __forceinline__ Work work_of(const ChunkParams &p, int r, const Request &q,
+                                        int64_t first, int kvh, int seg, int shift) {
   Work w = {};
-  w.kvh = block % p.nkv;
+  w.r = r;
+  w.kvh = kvh;
   w.seg = seg;
-  const int64_t x = gridDim.x / p.nkv - 1 - block / p.nkv;
-  Request q;
-  if (p.B <= 32) {  // in one memory round trip: a request a lane
-    const int i = min(lane, p.B - 1);
-    q.a = p.cu[i];
-    q.b = p.cu[i + 1];
-    q.c = p.ctx[i];
-    q.kv = p.kv[i];
-    const int64_t tile = ((static_cast<int64_t>(q.a) * p.G) >> shift) + i;
-    w.r = max(__popc(__ballot_sync(0xffffffffu, lane < p.B && tile <= x)), 1) - 1;
-    q.a = __shfl_sync(0xffffffffu, q.a, w.r);
-    q.b = __shfl_sync(0xffffffffu, q.b, w.r);
-    q.c = __shfl_sync(0xffffffffu, q.c, w.r);
-    q.kv = __shfl_sync(0xffffffffu, q.kv, w.r);
-  } else {
-    w.r = find_request(p, x, shift, lane);
-    load_request(p, w.r, &q);
-  }
-  if (!check_request(p, lane == 0 && w.kvh == 0 && seg == 0, &q)) return w;
-  const int64_t first = (x - (((static_cast<int64_t>(q.a) * p.G) >> shift) + w.r)) << shift;
   w.a = q.a;
   w.c = q.c;
   w.kv = q.kv;
@@ -299,6 +279,119 @@ __device__ __forceinline__ Work describe(const ChunkParams &p, int block, int se
     }
   }
   return w;
+}
+
+// Work tile (x, seg) of the grid, in the requests' order.  The whole warp.  Later rows
+// see more keys, so the last tiles of all heads go first (heads one after the other
+// leave a head's longest tiles for the end).
+__device__ __forceinline__ Work describe(const ChunkParams &p, int block, int seg, int shift,
+                                         int lane) {
+  const int kvh = block % p.nkv;
+  const int64_t x = gridDim.x / p.nkv - 1 - block / p.nkv;
+  Request q;
+  int r;
+  if (p.B <= 32) {  // in one memory round trip: a request a lane
+    const int i = min(lane, p.B - 1);
+    load_request(p, i, &q);
+    const int64_t tile = ((static_cast<int64_t>(q.a) * p.G) >> shift) + i;
+    r = max(__popc(__ballot_sync(0xffffffffu, lane < p.B && tile <= x)), 1) - 1;
+    q.a = __shfl_sync(0xffffffffu, q.a, r);
+    q.b = __shfl_sync(0xffffffffu, q.b, r);
+    q.c = __shfl_sync(0xffffffffu, q.c, r);
+    q.kv = __shfl_sync(0xffffffffu, q.kv, r);
+  } else {
+    r = find_request(p, x, shift, lane);
+    load_request(p, r, &q);
+  }
+  if (!check_request(p, lane == 0 && kvh == 0 && seg == 0, &q)) return Work{};
+  const int64_t first = (x - (((static_cast<int64_t>(q.a) * p.G) >> shift) + r)) << shift;
+  return work_of(p, r, q, first, kvh, seg, shift);
+}
+
+// The requests of a call with 2 to 64 of them, two a lane of the scheduler's warp, in the
+// order of their work tiles' cost, the dearest first: claimed in the requests' own order, a
+// long one that comes late keeps one SM at work when the others have nothing left (64
+// single tokens over up to 8192 keys 226 us, so 208; 32 of them 139 and 105).  Four or eight
+// requests a lane take the warp as long as the order saves (8: ten us more).
+constexpr int kSorted = 64;
+struct Order {
+  Request q[2];      // of requests lane and lane + 32
+  int r[2], end[2];  // the requests at places lane and lane + 32, their tiles' end
+};
+__device__ __forceinline__ int pick(const int (&v)[2], int i) {
+  const int a = __shfl_sync(0xffffffffu, v[0], i & 31);
+  const int b = __shfl_sync(0xffffffffu, v[1], i & 31);
+  return i < 32 ? a : b;
+}
+template <bool kPair>
+__device__ __forceinline__ Order sort_requests(const ChunkParams &p, int shift, int lane,
+                                               uint8_t *places) {
+  Order o = {};
+  const int tiles = gridDim.x / p.nkv;
+  int cost[2], count[2], rank[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = lane + 32 * i;
+    cost[i] = -2;
+    count[i] = 0;
+    if (r < p.B) {
+      load_request(p, r, &o.q[i]);
+      const int from = static_cast<int>((static_cast<int64_t>(o.q[i].a) * p.G) >> shift) + r;
+      const int to = r + 1 < p.B
+                         ? static_cast<int>((static_cast<int64_t>(o.q[i].b) * p.G) >> shift) + r + 1
+                         : tiles;
+      count[i] = min(max(to - from, 0), tiles);
+      cost[i] = -1;
+      if (!check_request(p, blockIdx.x == 0 && blockIdx.z == 0, &o.q[i])) {
+        o.q[i].b = o.q[i].a = 0;  // no rows
+      } else if (o.q[i].b > o.q[i].a) {
+        int lo, hi;
+        key_range(p, o.q[i].c + o.q[i].b - o.q[i].a - 1, o.q[i].kv, &lo, &hi);
+        if (lo <= hi)  // one row tile is done in half the steps of two
+          cost[i] = (hi / kKT - lo / kKT + 1) *
+                    (kPair && (o.q[i].b - o.q[i].a) * p.G > 128 ? 2 : 1);
+      }
+    }
+  }
+#pragma unroll 4
+  for (int j = 0; j < 32; ++j) {
+    const int c0 = __shfl_sync(0xffffffffu, cost[0], j), c1 = __shfl_sync(0xffffffffu, cost[1], j);
+    rank[0] += (c0 > cost[0] || (c0 == cost[0] && j < lane)) + (c1 > cost[0]);
+    rank[1] += (c0 >= cost[1]) + (c1 > cost[1] || (c1 == cost[1] && j < lane));
+  }
+  places[rank[0]] = static_cast<uint8_t>(lane);
+  places[rank[1]] = static_cast<uint8_t>(lane + 32);
+  __syncwarp();
+  int before = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    o.r[i] = places[lane + 32 * i];
+    o.end[i] = pick(count, o.r[i]);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, o.end[i], d);
+      if (lane >= d) o.end[i] += up;
+    }
+    o.end[i] += before;
+    before = __shfl_sync(0xffffffffu, o.end[i], 31);
+  }
+  return o;
+}
+__device__ __forceinline__ Work describe_sorted(const ChunkParams &p, const Order &o, int block,
+                                                int seg, int shift) {
+  const int x = block / p.nkv;
+  const int at = __popc(__ballot_sync(0xffffffffu, o.end[0] <= x)) +
+                 __popc(__ballot_sync(0xffffffffu, o.end[1] <= x));
+  if (at >= p.B) return Work{};
+  const int r = pick(o.r, at), end = pick(o.end, at);
+  Request q;
+  q.a = pick({o.q[0].a, o.q[1].a}, r);
+  q.b = pick({o.q[0].b, o.q[1].b}, r);
+  q.c = pick({o.q[0].c, o.q[1].c}, r);
+  q.kv = pick({o.q[0].kv, o.q[1].kv}, r);
+  // its last tile first; the places past its rows are empty
+  const int64_t first = static_cast<int64_t>(end - 1 - x) << shift;
+  return work_of(p, r, q, first, block - x * p.nkv, seg, shift);
 }
 
 // Ask for a block of the grid that has not started, to do its work here; the
@@ -349,7 +442,8 @@ struct Layout {
   static constexpr uint32_t kWork = (kWords + 12 + 15) / 16 * 16;
   static constexpr uint32_t kAnswer = kWork + 2 * sizeof(Work);
   static constexpr uint32_t kJoin = kAnswer + 16;  // m, then l, of a split tile [256]
-  static constexpr uint32_t kBarBytes = kJoin + 1024;
+  static constexpr uint32_t kPlaces = kJoin + 1024;
+  static constexpr uint32_t kBarBytes = kPlaces + kSorted;
   static constexpr int kFit = (kSmemMax - 1024 - kBarBytes - kRing) / kSlotBytes;
   static constexpr int kSlots = kFit < 12 ? kFit : 12;
   static constexpr uint32_t kBars = kRing + kSlots * kSlotBytes;
@@ -488,11 +582,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       int block = blockIdx.x, seg = blockIdx.z;
       bool have = true, last = !p.claims;
       uint32_t claims = 0, loads = 0;
+      const bool sorted = p.claims && p.B > 1 && p.B <= kSorted;
+      Order order = {};
+      if (sorted)
+        order = sort_requests<kPair>(p, kShift, lane, sm + Lay::kBars + Lay::kPlaces);
       for (uint32_t w = 0;; ++w) {
         Work d = {};
         while (true) {
           if (have) {
-            d = describe(p, block, seg, kShift, lane);
+            d = sorted ? describe_sorted(p, order, block, seg, kShift)
+                       : describe(p, block, seg, kShift, lane);
             have = false;
             if (d.nrow > 0) break;
           }
@@ -1137,10 +1236,10 @@ int tail_tiles(const dflash_geom &g, int B, int n_rows) {
 // and the SMs take them in rounds; two segments are cut so that the last round leaves no
 // SM without work (1024 rows behind 32768 keys, 32 heads over 8, us: 410 with one
 // segment, 388 so; 2048 rows 812 and 767, and 893 with three).  Otherwise the SMs share the
-// CTAs, and the last ones run alone for half their time; 0.6 of the longest
+// CTAs, and the last ones run alone for a part of their time; 0.6 of the longest
 // span stands for the mean of four requests or more (16 single tokens over up to
-// 16384 keys 164 with one segment, 129 with three; over up to 2048 keys 31 and 40; one
-// token over 32768 keys 33 with 19).
+// 16384 keys 162 with one segment, 105 with two, 124 with three; over up to 2048 keys 31
+// and 32 with two; one token over 32768 keys 33 with 19).
 int chunk_attention_num_segments(const dflash_geom &g, int B, int n_rows, int window) {
   constexpr double kFixed = 7.0, kMerge = 3.0;
   const double ctas = static_cast<double>(chunk_tiles(g, B, n_rows)) * g.nkv;
@@ -1161,8 +1260,8 @@ int chunk_attention_num_segments(const dflash_geom &g, int B, int n_rows, int wi
     double t = one;
     if (alike)
       t *= std::ceil(static_cast<double>(works) * (S == 2 && left ? 1 : S) / sms);
-    else if (ctas * S > sms)
-      t = std::max(one, ctas * (mean + kFixed * S) / sms + 0.5 * one);
+    else if (ctas * S > sms)  // in the order of cost the last ones are short
+      t = std::max(one, ctas * (mean + kFixed * S) / sms + (B > kSorted ? 0.5 : 0.25) * one);
     if (S > 1) t += kMerge + part * S;
     if (S == 1 || t < least) {
       least = t;

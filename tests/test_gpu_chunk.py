@@ -588,6 +588,39 @@ def test_attention_uneven_segments(dl, nkv, rows, ctx, window, causal):
         got, run_attn(dl, pb, **kw, window=window, causal=causal, S=2, check=False))
 
 
+@pytest.mark.parametrize("B", [2, 33, 64, 65])
+def test_attention_bad_lengths_among_many_works(dl, B):
+    """Lengths and offsets out of range where blocks take the requests' work tiles in
+    the order of their cost (up to 64) and in their own: flagged, the other requests as ever."""
+    rng = np.random.default_rng(32)
+    kw = dict(hq=48, nkv=24, hd=64, P=16)
+    n = [int(x) for x in rng.integers(1, 4, B)]
+    n[0] = 400 if B == 2 else 70
+    ctx = [int(x) for x in rng.integers(0, 300, B)]
+    ctx[0] = 20
+    pb = attn_problem(rng, n, ctx, **kw)
+    right = run_attn(dl, pb, **kw, S=1, check=B < 64)
+    last = int(pb["cu"][B - 1])
+    bad = dict(pb, ctx=pb["ctx"].copy(), kv=pb["kv"].copy(), cu=pb["cu"].copy())
+    bad["ctx"][B - 1] = -1
+    got = run_attn(dl, bad, **kw, S=1, flags=128, check=False)
+    np.testing.assert_array_equal(got[:last], right[:last])
+    assert np.all(got[last:] == 7.0)
+    bad["ctx"][B - 1], bad["cu"][B] = ctx[B - 1], bad["cu"][B] + 5   # past the last row
+    got = run_attn(dl, bad, **kw, S=1, flags=128, check=False)
+    np.testing.assert_array_equal(got[:last], right[:last])
+    assert np.all(got[last:] == 7.0)
+    bad["cu"][B] -= 5
+    bad["kv"][0] = -7
+    got = run_attn(dl, bad, **kw, S=1, flags=16, check=False)
+    np.testing.assert_array_equal(got[n[0]:], right[n[0]:])
+    assert np.all(got[:n[0]] == 0.0)
+    # offsets that go back: flagged, nothing outside the rows is written
+    bad = dict(pb, cu=pb["cu"].copy())
+    bad["cu"][1:B] = bad["cu"][1:B][::-1] if B > 2 else pb["cu"][B] + 3
+    run_attn(dl, bad, **kw, S=1, flags=128, check=False)
+
+
 def test_attention_calls_at_once(dl):
     """Two calls on two streams with a workspace each, many times over, give what
     each gives alone."""
