@@ -219,7 +219,7 @@ cudaError_t launch_chunk_plan(const dflash_geom &g, int B, int n_rows, const int
   // a thread per request and per row, 1024 at most; rows over as many CTAs as
   // there are SMs
   const int most = B > n_rows ? B : n_rows;
-  const int threads = most >= 1024 ? 1024 : (most + 31) / 32 * 32;
+  const int threads = most >= 1024 ? 1024 : most < 1 ? 32 : (most + 31) / 32 * 32;
   const int ctas = (n_rows + threads - 1) / threads;
   const int sms = device_sm_count();
   cudaLaunchConfig_t cfg = {};

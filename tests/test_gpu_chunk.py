@@ -127,6 +127,8 @@ def test_plan_without_requests_or_rows(dl):
                 table=np.zeros((0, 4), np.int32), free=np.zeros(0, np.int32),
                 range=np.array([0, 0], np.int32), valid=None)
     run_plan(dl, case, 7, 16, 4)
+    got = run_plan(dl, case, 0, 16, 4)   # neither
+    assert got["cu_rows"][0] == 0 and got["free_head"][0] == 0
 
 
 def test_plan_lengths_out_of_range(dl):
@@ -646,6 +648,44 @@ def test_attention_calls_at_once(dl):
     for o, w in zip(outs, want):
         for x in o:
             np.testing.assert_array_equal(bf16_f64(bits(x)).reshape(w.shape), w)
+
+
+@pytest.mark.parametrize("B,S", [(40, 1), (40, 2), (100, 1)])
+def test_attention_many_works_captured_and_at_once(dl, B, S):
+    """Calls with more work tiles than the GPU runs at once, in two graphs replayed on
+    two streams at the same time, give what each gives alone."""
+    import torch
+    rng = np.random.default_rng(33)
+    kw = dict(hq=16, nkv=8, hd=128, P=32)
+    pbs = [attn_problem(rng, [int(x) for x in rng.choice([1, 2, 90, 150], B)],
+                        [int(x) for x in rng.integers(0, 500, B)], **kw) for _ in range(2)]
+    want = [run_attn(dl, pb, **kw, S=S, check=False) for pb in pbs]
+    graphs, outs, streams, keep = [], [], [torch.cuda.Stream() for _ in pbs], []
+    for pb, s in zip(pbs, streams):
+        g = geom(dl, M=pb["M"], NP=pb["NP"], **kw)
+        a = [bf16(pb["q"])[0], bf16(pb["pool"])[0],
+             *(dev(pb[k]) for k in ("table", "cu", "ctx", "kv"))]
+        need = dl.dflash_chunk_attention_workspace_bytes(g, B, pb["q"].shape[0], S)
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+        o = torch.empty_like(a[0])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            for _ in range(3):
+                dl.dflash_chunk_attention(g, 0, *a, o, ws, num_segments=S, stream=s)
+        graphs.append(graph)
+        outs.append(o)
+        keep.append((a, ws))
+    for _ in range(5):
+        for o in outs:
+            o.fill_(7.0)
+        torch.cuda.synchronize()
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            np.testing.assert_array_equal(bf16_f64(bits(o)).reshape(w.shape), w)
 
 
 def test_a_workspace_serves_captured_graphs_in_turn(dl):
