@@ -39,8 +39,8 @@
 // of 0 does not silence a NaN.
 //
 // Bound: single tokens by HBM (64 of them over 1 to 8192 keys each, 32 heads over 8 of
-// 128: 207 us, 6.0 TB/s), long chunks by the tensor cores (1024 rows behind 32768
-// keys: 407 us, 1.37 PFLOP/s; 16384 rows of one prompt: 1.53).  In the 256-row form a
+// 128: 209 us, 5.9 TB/s), long chunks by the tensor cores (1024 rows behind 32768
+// keys: 409 us, 1.36 PFLOP/s; 16384 rows of one prompt: 1.53).  In the 256-row form a
 // key tile takes ~3250 cycles for 2048 of products: their operands and the loads keep
 // shared memory busy for another ~2000 of 128 bytes each, and every hand-over between a
 // softmax group and the issuing thread waits behind them.  A work tile ends with ~7000
@@ -70,9 +70,10 @@ namespace {
 constexpr int kKT = kAttnTileKeys;  // 128 keys per tile
 constexpr int kThreads = 384;
 // Registers: 384 threads launch with 168 each, 64512 in all; the softmax groups
-// take 216 (a row's 128 scores and 64 packed weights), the third group gives up
-// the difference: 2 x 128 x 216 + 128 x 72 = 64512.
-constexpr int kSoftmaxRegs = 216, kIssueRegs = 72;
+// take 200 (a row's 128 scores and 64 packed weights), the third group gives up the
+// difference: 2 x 128 x 200 + 128 x 104 = 64512.  (224 and 56 spill the scheduler's: 4%
+// slower; 216 and 72: 1%.)
+constexpr int kSoftmaxRegs = 200, kIssueRegs = 104;
 static_assert(256 * kSoftmaxRegs + 128 * kIssueRegs <= kThreads * 168, "register split");
 constexpr int kSmemMax = 227 * 1024;
 // Barriers of the events that free ring slots, more than can be between a slot's use
@@ -85,7 +86,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 struct ChunkParams {
   int B, n_rows, hq, nkv, G, wide_out, layer, NP, P, M, window, mask_mode, S;
-  int box_rows, skip_tile, q_boxes, claims;
+  int box_rows, skip_tile, q_boxes;
   int tails;  // > 1: two segments of a main part and a tail (main_tiles)
   uint32_t g_inv;  // ceil(2^32 / G), for G > 1
   float scale_log2;
@@ -308,87 +309,94 @@ __device__ __forceinline__ Work describe(const ChunkParams &p, int block, int se
   return work_of(p, r, q, first, kvh, seg, shift);
 }
 
-// The requests of a call with 2 to 64 of them, two a lane of the scheduler's warp, in the
-// order of their work tiles' cost, the dearest first: claimed in the requests' own order, a
-// long one that comes late keeps one SM at work when the others have nothing left (64
-// single tokens over up to 8192 keys 226 us, so 208; 32 of them 139 and 105).  Four or eight
-// requests a lane take the warp as long as the order saves (8: ten us more).
-constexpr int kSorted = 64;
-struct Order {
-  Request q[2];      // of requests lane and lane + 32
-  int r[2], end[2];  // the requests at places lane and lane + 32, their tiles' end
+// The requests of a call with 2 to 256 of them in the order of their work tiles' cost,
+// the dearest first: claimed in the requests' own order, a long one that comes late keeps one
+// SM at work when the others have nothing left (64 single tokens over up to 8192 keys
+// 226 us, so 210; 32 of them 139 and 107, 256 over up to 2048 keys 274 and 248).  Every
+// block sorts for itself, all its threads together (one warp alone took 10 us for 256).
+constexpr int kSortLanes = 8, kSorted = 32 * kSortLanes;
+struct Order {  // lane l holds places l, l + 32, ...
+  int r[kSortLanes], end[kSortLanes];  // the request at a place, where its work tiles end
 };
-__device__ __forceinline__ int pick(const int (&v)[2], int i) {
-  const int a = __shfl_sync(0xffffffffu, v[0], i & 31);
-  const int b = __shfl_sync(0xffffffffu, v[1], i & 31);
-  return i < 32 ? a : b;
-}
+// By the whole block: into places[k] the request at place k, into tiles[k] its work tiles.
 template <bool kPair>
-__device__ __forceinline__ Order sort_requests(const ChunkParams &p, int shift, int lane,
-                                               uint8_t *places) {
-  Order o = {};
-  const int tiles = gridDim.x / p.nkv;
-  int cost[2], count[2], rank[2] = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = lane + 32 * i;
-    cost[i] = -2;
-    count[i] = 0;
-    if (r < p.B) {
-      load_request(p, r, &o.q[i]);
-      const int from = static_cast<int>((static_cast<int64_t>(o.q[i].a) * p.G) >> shift) + r;
-      const int to = r + 1 < p.B
-                         ? static_cast<int>((static_cast<int64_t>(o.q[i].b) * p.G) >> shift) + r + 1
-                         : tiles;
-      count[i] = min(max(to - from, 0), tiles);
-      cost[i] = -1;
-      if (!check_request(p, blockIdx.x == 0 && blockIdx.z == 0, &o.q[i])) {
-        o.q[i].b = o.q[i].a = 0;  // no rows
-      } else if (o.q[i].b > o.q[i].a) {
-        int lo, hi;
-        key_range(p, o.q[i].c + o.q[i].b - o.q[i].a - 1, o.q[i].kv, &lo, &hi);
-        if (lo <= hi)  // one row tile is done in half the steps of two
-          cost[i] = (hi / kKT - lo / kKT + 1) *
-                    (kPair && (o.q[i].b - o.q[i].a) * p.G > 128 ? 2 : 1);
-      }
+__device__ __forceinline__ void sort_requests(const ChunkParams &p, int shift, int *tiles,
+                                              uint8_t *places) {
+  const int i = threadIdx.x, all = gridDim.x / p.nkv;
+  int cost = -1, count = 0, rank = 0;
+  if (i < p.B) {
+    Request q;
+    load_request(p, i, &q);
+    const int from = static_cast<int>((static_cast<int64_t>(q.a) * p.G) >> shift) + i;
+    const int to = i + 1 < p.B
+                       ? static_cast<int>((static_cast<int64_t>(q.b) * p.G) >> shift) + i + 1
+                       : all;
+    count = min(max(to - from, 0), all);
+    if (check_request(p, blockIdx.x == 0 && blockIdx.z == 0, &q) && q.b > q.a) {
+      int lo, hi;
+      key_range(p, q.c + q.b - q.a - 1, q.kv, &lo, &hi);
+      if (lo <= hi)  // one row tile is done in half the steps of two
+        cost = (hi / kKT - lo / kKT + 1) * (kPair && (q.b - q.a) * p.G > 128 ? 2 : 1);
     }
   }
+  if (i < kSorted) tiles[i] = i < p.B ? cost : -2;  // behind them all
+  __syncthreads();
+  if (i < p.B) {
+    const int4 *costs = reinterpret_cast<const int4 *>(tiles);
 #pragma unroll 4
-  for (int j = 0; j < 32; ++j) {
-    const int c0 = __shfl_sync(0xffffffffu, cost[0], j), c1 = __shfl_sync(0xffffffffu, cost[1], j);
-    rank[0] += (c0 > cost[0] || (c0 == cost[0] && j < lane)) + (c1 > cost[0]);
-    rank[1] += (c0 >= cost[1]) + (c1 > cost[1] || (c1 == cost[1] && j < lane));
+    for (int j = 0; j < (p.B + 3) / 4; ++j) {
+      const int4 c = costs[j];
+      rank += (c.x > cost || (c.x == cost && 4 * j < i)) +
+              (c.y > cost || (c.y == cost && 4 * j + 1 < i)) +
+              (c.z > cost || (c.z == cost && 4 * j + 2 < i)) +
+              (c.w > cost || (c.w == cost && 4 * j + 3 < i));
+    }
+    places[rank] = static_cast<uint8_t>(i);
   }
-  places[rank[0]] = static_cast<uint8_t>(lane);
-  places[rank[1]] = static_cast<uint8_t>(lane + 32);
-  __syncwarp();
+  __syncthreads();
+  if (i < p.B) tiles[rank] = count;
+  __syncthreads();
+}
+__device__ __forceinline__ Order read_order(const ChunkParams &p, int lane, const int *tiles,
+                                            const uint8_t *places) {
+  Order o;
   int before = 0;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    o.r[i] = places[lane + 32 * i];
-    o.end[i] = pick(count, o.r[i]);
+  for (int k = 0; k < kSortLanes; ++k) {
+    o.r[k] = 0;
+    o.end[k] = INT32_MAX;
+    if (32 * k < p.B) {
+      const int at = lane + 32 * k;
+      o.r[k] = at < p.B ? places[at] : 0;
+      int end = at < p.B ? tiles[at] : 0;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, o.end[i], d);
-      if (lane >= d) o.end[i] += up;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, end, d);
+        if (lane >= d) end += up;
+      }
+      o.end[k] = end + before;
+      before = __shfl_sync(0xffffffffu, o.end[k], 31);
     }
-    o.end[i] += before;
-    before = __shfl_sync(0xffffffffu, o.end[i], 31);
   }
   return o;
 }
 __device__ __forceinline__ Work describe_sorted(const ChunkParams &p, const Order &o, int block,
                                                 int seg, int shift) {
   const int x = block / p.nkv;
-  const int at = __popc(__ballot_sync(0xffffffffu, o.end[0] <= x)) +
-                 __popc(__ballot_sync(0xffffffffu, o.end[1] <= x));
+  int at = 0, r = 0, end = 0;
+#pragma unroll
+  for (int k = 0; k < kSortLanes; ++k)
+    if (32 * k < p.B) at += __popc(__ballot_sync(0xffffffffu, o.end[k] <= x));
   if (at >= p.B) return Work{};
-  const int r = pick(o.r, at), end = pick(o.end, at);
+#pragma unroll
+  for (int k = 0; k < kSortLanes; ++k)
+    if (at >> 5 == k) {
+      r = __shfl_sync(0xffffffffu, o.r[k], at & 31);
+      end = __shfl_sync(0xffffffffu, o.end[k], at & 31);
+    }
   Request q;
-  q.a = pick({o.q[0].a, o.q[1].a}, r);
-  q.b = pick({o.q[0].b, o.q[1].b}, r);
-  q.c = pick({o.q[0].c, o.q[1].c}, r);
-  q.kv = pick({o.q[0].kv, o.q[1].kv}, r);
+  load_request(p, r, &q);
+  if (!check_request(p, false, &q)) return Work{};
   // its last tile first; the places past its rows are empty
   const int64_t first = static_cast<int64_t>(end - 1 - x) << shift;
   return work_of(p, r, q, first, block - x * p.nkv, seg, shift);
@@ -451,7 +459,9 @@ struct Layout {
   static_assert(kSlots >= 5, "");
 };
 
-template <int HD, bool kPair>
+// kMany: more blocks than SMs.  A grid that fits them has one work a block, and the form
+// without the rest is shorter: cold instructions cost the shortest calls 0.5 us.
+template <int HD, bool kPair, bool kMany>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tq,
                       const __grid_constant__ ChunkParams p) {
@@ -504,6 +514,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tslot;
   ptx::griddep_launch();
   ptx::griddep_wait();
+
+  const bool sorted = kMany && p.B > 1 && p.B <= kSorted;
+  if (sorted)  // in memory that the works' joins use later
+    sort_requests<kPair>(p, kShift, reinterpret_cast<int *>(sm + Lay::kBars + Lay::kJoin),
+                         sm + Lay::kBars + Lay::kPlaces);
 
   // The CTA's works, one after the other: its own block of the grid, then blocks that
   // have not started (there are none where the grid fits the SMs).  The next one is
@@ -580,12 +595,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) {
       // ---------------------------------------------- scheduler, half of Q
       int block = blockIdx.x, seg = blockIdx.z;
-      bool have = true, last = !p.claims;
+      bool have = true, last = !kMany;
       uint32_t claims = 0, loads = 0;
-      const bool sorted = p.claims && p.B > 1 && p.B <= kSorted;
       Order order = {};
-      if (sorted)
-        order = sort_requests<kPair>(p, kShift, lane, sm + Lay::kBars + Lay::kPlaces);
+      if (sorted) order = read_order(p, lane, reinterpret_cast<const int *>(sm + Lay::kBars + Lay::kJoin),
+                                       sm + Lay::kBars + Lay::kPlaces);
       for (uint32_t w = 0;; ++w) {
         Work d = {};
         while (true) {
@@ -618,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (d.nrow == 0) break;
         if (d.n > 0 && load_q(d, 0, loads++) && !q_in_boxes(d)) q_copied();
-        if (!p.claims) break;
+        if (!kMany) break;
         volatile int dummy = 0;
         if (!__all_sync(0xffffffffu,
                         chunk_wait<false, 4>(ptx::smem_u32(work_read), w & 1, &dummy)) ||
@@ -632,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 9) {
       // ---------------------------------------------- half of Q, the pages' check
       uint32_t loads = 0;
-      for (uint32_t w = 0; w == 0 || p.claims; ++w) {
+      for (uint32_t w = 0; w == 0 || kMany; ++w) {
         const Work d = next_work(w);
         have_read();
         if (d.nrow == 0) break;
@@ -667,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // t's values and tile t + 2's scores.  Lane s keeps the one that frees slot s.
       int events = 0, freed_by = 0;
       bool ok = true;
-      for (uint32_t w = 0; w == 0 || p.claims; ++w) {
+      for (uint32_t w = 0; w == 0 || kMany; ++w) {
         const Work d = next_work(w);
         if (d.nrow == 0 || d.n == 0 || !ok) {
           have_read();
@@ -802,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                            idesc_pv, (!first || ks > 0) ? 1u : 0u);
       };
       auto event = [&](int e) { ptx::mma_commit(ptx::smem_u32(&done[(events + e) % kDone])); };
-      for (uint32_t w = 0; w == 0 || p.claims; ++w) {
+      for (uint32_t w = 0; w == 0 || kMany; ++w) {
         const Work d = next_work(w);
         have_read();
         if (d.nrow == 0) break;
@@ -872,7 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int base = 0;  // the work's first place in the ring's order
     uint32_t loads = 0u, scores = 0u, outs0 = 0u, outs1 = 0u;  // of pages_seen, s_full, o_done
     bool ok = true;
-    for (uint32_t wk = 0; wk == 0 || p.claims; ++wk) {
+    for (uint32_t wk = 0; wk == 0 || kMany; ++wk) {
       // its fields are read again where they are needed: this slot is not written before
       // the next work is read
       const volatile Work &d = shared_work[wk & 1];
@@ -1299,10 +1313,10 @@ cudaError_t q_tensor_map(CUtensorMap *m, const dflash_geom &g, int n_rows, const
              : cudaErrorInvalidValue;
 }
 
-template <int HD, bool kPair>
-cudaError_t launch_main(const CUtensorMap &tm, const CUtensorMap &tq, const ChunkParams &p,
+template <int HD, bool kPair, bool kMany>
+cudaError_t launch_form(const CUtensorMap &tm, const CUtensorMap &tq, const ChunkParams &p,
                         dim3 grid, cudaStream_t s) {
-  const cudaError_t e = ensure_smem_limit<chunk_attn_kernel<HD, kPair>>(kSmemMax);
+  const cudaError_t e = ensure_smem_limit<chunk_attn_kernel<HD, kPair, kMany>>(kSmemMax);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -1314,7 +1328,18 @@ cudaError_t launch_main(const CUtensorMap &tm, const CUtensorMap &tq, const Chun
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_attn_kernel<HD, kPair>, tm, tq, p);
+  return cudaLaunchKernelEx(&cfg, chunk_attn_kernel<HD, kPair, kMany>, tm, tq, p);
+}
+
+template <int HD>
+cudaError_t launch_main(bool pair, const CUtensorMap &tm, const CUtensorMap &tq,
+                        const ChunkParams &p, dim3 grid, cudaStream_t s) {
+  const bool many = static_cast<int64_t>(grid.x) * grid.z > device_sm_count();
+  if (pair)
+    return many ? launch_form<HD, true, true>(tm, tq, p, grid, s)
+                : launch_form<HD, true, false>(tm, tq, p, grid, s);
+  return many ? launch_form<HD, false, true>(tm, tq, p, grid, s)
+              : launch_form<HD, false, false>(tm, tq, p, grid, s);
 }
 
 }  // namespace
@@ -1370,12 +1395,9 @@ cudaError_t launch_chunk_attention(const dflash_geom &g, int B, int layer, int n
               q_stride < (1LL << 38);
   if (p.q_boxes && (e = q_tensor_map(&tq, g, n_rows, q, q_stride)) != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(chunk_tiles(g, B, n_rows) * g.nkv), 1, S);
-  p.claims = static_cast<int64_t>(grid.x) * S > device_sm_count();  // blocks wait for an SM
   const bool pair = pair_form(g, B, n_rows);
-  if (g.head_dim == 64)
-    e = pair ? launch_main<64, true>(tm, tq, p, grid, s) : launch_main<64, false>(tm, tq, p, grid, s);
-  else
-    e = pair ? launch_main<128, true>(tm, tq, p, grid, s) : launch_main<128, false>(tm, tq, p, grid, s);
+  e = g.head_dim == 64 ? launch_main<64>(pair, tm, tq, p, grid, s)
+                       : launch_main<128>(pair, tm, tq, p, grid, s);
   if (e != cudaSuccess || S == 1) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];

@@ -590,10 +590,10 @@ def test_attention_uneven_segments(dl, nkv, rows, ctx, window, causal):
         got, run_attn(dl, pb, **kw, window=window, causal=causal, S=2, check=False))
 
 
-@pytest.mark.parametrize("B", [2, 33, 64, 65])
+@pytest.mark.parametrize("B", [2, 33, 65, 256, 257])
 def test_attention_bad_lengths_among_many_works(dl, B):
     """Lengths and offsets out of range where blocks take the requests' work tiles in
-    the order of their cost (up to 64) and in their own: flagged, the other requests as ever."""
+    the order of their cost (up to 256) and in their own: flagged, the other requests as ever."""
     rng = np.random.default_rng(32)
     kw = dict(hq=48, nkv=24, hd=64, P=16)
     n = [int(x) for x in rng.integers(1, 4, B)]
@@ -601,7 +601,7 @@ def test_attention_bad_lengths_among_many_works(dl, B):
     ctx = [int(x) for x in rng.integers(0, 300, B)]
     ctx[0] = 20
     pb = attn_problem(rng, n, ctx, **kw)
-    right = run_attn(dl, pb, **kw, S=1, check=B < 64)
+    right = run_attn(dl, pb, **kw, S=1, check=B < 256)
     last = int(pb["cu"][B - 1])
     bad = dict(pb, ctx=pb["ctx"].copy(), kv=pb["kv"].copy(), cu=pb["cu"].copy())
     bad["ctx"][B - 1] = -1
@@ -650,7 +650,7 @@ def test_attention_calls_at_once(dl):
             np.testing.assert_array_equal(bf16_f64(bits(x)).reshape(w.shape), w)
 
 
-@pytest.mark.parametrize("B,S", [(40, 1), (40, 2), (100, 1)])
+@pytest.mark.parametrize("B,S", [(40, 1), (40, 2), (100, 1), (300, 1)])
 def test_attention_many_works_captured_and_at_once(dl, B, S):
     """Calls with more work tiles than the GPU runs at once, in two graphs replayed on
     two streams at the same time, give what each gives alone."""
