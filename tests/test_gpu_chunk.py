@@ -509,6 +509,17 @@ def test_attention_wide_tiles(dl, shape, window, sinks, causal):
              sinks=rng.standard_normal(4) if sinks else None)
 
 
+@pytest.mark.parametrize("hq,nkv,rows", [(4, 1, 20), (16, 2, 9), (16, 1, 5), (128, 1, 1),
+                                         (3, 3, 70), (64, 1, 3), (256, 1, 1)])
+def test_attention_fewer_rows_than_a_box(dl, hq, nkv, rows):
+    """More than 64 rows of a KV head's group, of fewer tokens than 128 rows hold."""
+    rng = np.random.default_rng(34)
+    kw = dict(hq=hq, nkv=nkv, hd=128, P=32)
+    pb = attn_problem(rng, [rows], [150], **kw)
+    run_attn(dl, pb, **kw, S=1)
+    run_attn(dl, pb, **kw, S=2, stride_pad=64, window=70)
+
+
 @pytest.mark.parametrize("S", [2, 5])
 @pytest.mark.parametrize("hd", [64, 128])
 def test_attention_wide_tiles_in_segments(dl, S, hd):
