@@ -1,8 +1,9 @@
 """GB300 (sm_103a) library for the data-parallel hot path of a DFlash / DSpark
 block drafter's decode step: bookkeeping, context-KV update, block-KV scatter
-and split-KV block attention, behind the C ABI of include/dflash.h.
+and split-KV block attention, and for a layer over a ragged chunk of new tokens
+(plan, RoPE + paged store, attention), behind the C ABI of include/dflash.h.
 
-The Python names below are the C entry points of the same names (ctypes
+The Python names below are the C entry points of the same names (argument
 marshalling only).  ``inputs`` holds the seeded synthetic workloads.
 """
 from ._lib import (ChunkOutputs, DflashError, Geom, LayerWeights, RopeSpec,  # noqa: F401

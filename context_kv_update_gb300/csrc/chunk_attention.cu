@@ -463,7 +463,8 @@ struct Layout {
 // without the rest is shorter: cold instructions cost the shortest calls 0.5 us.
 template <int HD, bool kPair, bool kMany>
 __global__ void __launch_bounds__(kThreads, 1)
-    chunk_attn_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tq,
+    chunk_attn_kernel(const __grid_constant__ CUtensorMap tm,
+                      const __grid_constant__ CUtensorMap tq,
                       const __grid_constant__ ChunkParams p) {
   constexpr int kChunks = HD / 64;
   constexpr int kShift = kPair ? 8 : 7;
@@ -598,8 +599,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool have = true, last = !kMany;
       uint32_t claims = 0, loads = 0;
       Order order = {};
-      if (sorted) order = read_order(p, lane, reinterpret_cast<const int *>(sm + Lay::kBars + Lay::kJoin),
-                                       sm + Lay::kBars + Lay::kPlaces);
+      if (sorted)
+        order = read_order(p, lane, reinterpret_cast<const int *>(sm + Lay::kBars + Lay::kJoin),
+                           sm + Lay::kBars + Lay::kPlaces);
       for (uint32_t w = 0;; ++w) {
         Work d = {};
         while (true) {
