@@ -14,6 +14,7 @@ import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdflash.so")
+CALLS_PATH = os.path.join(HERE, "_calls.so")
 
 DFLASH_OK = 0
 DFLASH_ERR_INVALID_ARG = 1
@@ -110,13 +111,12 @@ class RopeSpec(ctypes.Structure):
                 ("beta_slow", ctypes.c_double), ("magnitude", ctypes.c_double)]
 
 _lib = None
-_calls = None  # the module that marshals the ragged-chunk calls (csrc/calls.c)
-_raw_stream = _current_device = None  # of torch, set with the library
+_calls = None  # the module that marshals the ragged-chunk calls, once one is made
 
 
 def load():
     """Load libdflash.so (raises when it has not been built)."""
-    global _lib, _calls, _raw_stream, _current_device
+    global _lib
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -193,16 +193,27 @@ def load():
                  "dflash_chunk_rope_store", "dflash_chunk_attention",
                  "dflash_chunk_attention_num_segments"):
         getattr(lib, name).restype = ctypes.c_int
-    import torch
-    _raw_stream = torch._C._cuda_getCurrentRawStream
-    _current_device = torch._C._cuda_getDevice
-    from . import _calls as calls
-    calls.bind(*[ctypes.cast(f, vp).value for f in (
-        lib.dflash_chunk_plan, lib.dflash_chunk_rope_store, lib.dflash_chunk_attention)],
-        _current_device, _raw_stream)
-    _calls = calls
     _lib = lib
     return lib
+
+
+def _load_calls():
+    """The module of csrc/calls.c, bound to the library's entry points.  Only the
+    ragged-chunk calls need it; load() and every other call do without."""
+    global _calls
+    if _calls is None:
+        lib = load()
+        import torch
+        try:
+            from . import _calls as calls
+        except ImportError as e:
+            raise ImportError(f"the ragged-chunk calls need {CALLS_PATH}: build it with "
+                              "`python -m context_kv_update_gb300.build`") from e
+        calls.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.dflash_chunk_plan, lib.dflash_chunk_rope_store, lib.dflash_chunk_attention)],
+            torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+        _calls = calls
+    return _calls
 
 
 # ---------------------------------------------------------------- helpers
@@ -228,7 +239,9 @@ def _stream(stream):
     if stream is None:
         # the current device's current stream, without building a Stream object
         # (3.3 us a call against 0.3)
-        return _raw_stream(_current_device())
+        import torch
+        c = torch._C
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -454,10 +467,9 @@ def dflash_chunk_plan(geom, n_new, ctx_len, n_pages, block_table, free_pages, fr
     are written), free_pages int32, free_range int32 [2] CUDA tensors, valid
     uint8 [B] or None; out: dict of the dflash_chunk_outputs fields ->
     preallocated int32 CUDA tensors (n_rows = length of row_req)."""
-    if _calls is None:
-        load()
-    rc = _calls.chunk_plan(geom, n_new, ctx_len, n_pages, block_table, free_pages, free_range,
-                           valid, max_ctx, out, dev_status, stream)
+    rc = (_calls or _load_calls()).chunk_plan(geom, n_new, ctx_len, n_pages, block_table,
+                                              free_pages, free_range, valid, max_ctx, out,
+                                              dev_status, stream)
     if rc:
         _check("dflash_chunk_plan", rc)
 
@@ -468,10 +480,9 @@ def dflash_chunk_rope_store(geom, layer, rope, q, k, v, row_pos, row_page, row_s
     head_dim] bf16 CUDA tensors (row-strided views of a packed projection output
     allowed, also as [n_rows, heads, head_dim]); q_out like q.  q and q_out, or
     k and v, may be None."""
-    if _calls is None:
-        load()
-    rc = _calls.chunk_rope_store(geom, layer, rope, q, k, v, row_pos, row_page, row_slot, q_out,
-                                 kv_pool, gamma_q, gamma_k, dev_status, stream)
+    rc = (_calls or _load_calls()).chunk_rope_store(geom, layer, rope, q, k, v, row_pos, row_page,
+                                                    row_slot, q_out, kv_pool, gamma_q, gamma_k,
+                                                    dev_status, stream)
     if rc:
         _check("dflash_chunk_rope_store", rc)
 
@@ -493,11 +504,10 @@ def dflash_chunk_attention(geom, layer, q, kv_pool, block_table, cu_rows, ctx_le
     allowed); block_table int32 [B, M], cu_rows int32 [B + 1], ctx_len and kv_len
     int32 [B]; workspace: uint8 tensor of dflash_chunk_attention_workspace_bytes
     bytes (None where that is 0)."""
-    if _calls is None:
-        load()
-    rc = _calls.chunk_attention(geom, layer, q, kv_pool, block_table, cu_rows, ctx_len, kv_len,
-                                out, workspace, window, sinks, scale, mask_mode, num_segments,
-                                dev_status, stream)
+    rc = (_calls or _load_calls()).chunk_attention(geom, layer, q, kv_pool, block_table, cu_rows,
+                                                   ctx_len, kv_len, out, workspace, window, sinks,
+                                                   scale, mask_mode, num_segments, dev_status,
+                                                   stream)
     if rc:
         _check("dflash_chunk_attention", rc)
 

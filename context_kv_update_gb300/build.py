@@ -46,15 +46,21 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "dflash.h"),
-                                                                  CALLS_SRC,
                                                                   os.path.abspath(__file__)]
 
 
+def _older(path: str, deps) -> bool:
+    return not os.path.exists(path) or any(os.path.getmtime(p) > os.path.getmtime(path)
+                                           for p in deps)
+
+
+def _calls_stale() -> bool:
+    return _older(CALLS_PATH, [CALLS_SRC, os.path.join(INCLUDE, "dflash.h"),
+                               os.path.abspath(__file__)])
+
+
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
-        return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
-    return any(os.path.getmtime(p) > t for p in _deps())
+    return _older(LIB_PATH, _deps()) or _calls_stale()
 
 
 def _compile(src: str, extra=()) -> str:
@@ -79,8 +85,16 @@ def _build_calls() -> None:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    if not force and not is_stale():
-        return LIB_PATH
+    if force or _older(LIB_PATH, _deps()):
+        _build_lib(verbose_ptxas)
+    # last: the library is there for the calls that need nothing else, even where
+    # the module does not compile
+    if force or _calls_stale():
+        _build_calls()
+    return LIB_PATH
+
+
+def _build_lib(verbose_ptxas: bool) -> None:
     os.makedirs(BUILD_DIR, exist_ok=True)
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
     srcs = _sources()
@@ -92,8 +106,6 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    _build_calls()
-    return LIB_PATH
 
 
 if __name__ == "__main__":
