@@ -1,7 +1,7 @@
 """ctypes binding of ``libdflash.so`` (include/dflash.h).
 
-Argument marshalling only (that of the ragged-chunk calls is in csrc/calls.c):
-every function here validates nothing beyond what ctypes needs, converts torch
+Argument marshalling only (that of the ragged-chunk calls, with checks of their
+tensors' types, layouts, lengths and devices, is in csrc/calls.cpp): every function here validates nothing beyond what ctypes needs, converts torch
 tensors to device pointers and the current torch stream to a ``cudaStream_t``,
 calls the C entry point of the same name and raises ``DflashError`` on a non-zero
 status.  All arithmetic runs in the CUDA kernels of the library; there is no CPU
@@ -198,7 +198,7 @@ def load():
 
 
 def _load_calls():
-    """The module of csrc/calls.c, bound to the library's entry points.  Only the
+    """The module of csrc/calls.cpppp, bound to the library's entry points.  Only the
     ragged-chunk calls need it; load() and every other call do without."""
     global _calls
     if _calls is None:
@@ -209,9 +209,12 @@ def _load_calls():
         except ImportError as e:
             raise ImportError(f"the ragged-chunk calls need {CALLS_PATH}: build it with "
                               "`python -m context_kv_update_gb300.build`") from e
+        if torch.__version__.partition("+")[0] != calls.torch_version.partition("+")[0]:
+            raise ImportError(f"{CALLS_PATH} was built with torch {calls.torch_version}, this is "
+                              f"{torch.__version__}: build it again with "
+                              "`python -m context_kv_update_gb300.build --force`")
         calls.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
-            lib.dflash_chunk_plan, lib.dflash_chunk_rope_store, lib.dflash_chunk_attention)],
-            torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+            lib.dflash_chunk_plan, lib.dflash_chunk_rope_store, lib.dflash_chunk_attention)])
         _calls = calls
     return _calls
 
@@ -465,8 +468,9 @@ def dflash_chunk_plan(geom, n_new, ctx_len, n_pages, block_table, free_pages, fr
                       max_ctx, out: dict, dev_status=None, stream=None):
     """n_new / ctx_len / n_pages int32 [B], block_table int32 [B, M] (new entries
     are written), free_pages int32, free_range int32 [2] CUDA tensors, valid
-    uint8 [B] or None; out: dict of the dflash_chunk_outputs fields ->
-    preallocated int32 CUDA tensors (n_rows = length of row_req)."""
+    uint8 or bool [B] or None; out: dict of the dflash_chunk_outputs fields ->
+    preallocated int32 CUDA tensors (n_rows = length of row_req).  Contiguous, on
+    the current device, and no shorter than that; longer ones are allowed."""
     rc = (_calls or _load_calls()).chunk_plan(geom, n_new, ctx_len, n_pages, block_table,
                                               free_pages, free_range, valid, max_ctx, out,
                                               dev_status, stream)
@@ -479,7 +483,8 @@ def dflash_chunk_rope_store(geom, layer, rope, q, k, v, row_pos, row_page, row_s
     """rope: a RopeSpec; q [n_rows, hq * head_dim], k and v [n_rows, nkv *
     head_dim] bf16 CUDA tensors (row-strided views of a packed projection output
     allowed, also as [n_rows, heads, head_dim]); q_out like q.  q and q_out, or
-    k and v, may be None."""
+    k and v, may be None.  row_pos / row_page / row_slot int32 [n_rows] (n_rows =
+    length of row_pos; the others may be longer), gamma_q / gamma_k bf16 [head_dim]."""
     rc = (_calls or _load_calls()).chunk_rope_store(geom, layer, rope, q, k, v, row_pos, row_page,
                                                     row_slot, q_out, kv_pool, gamma_q, gamma_k,
                                                     dev_status, stream)
@@ -502,7 +507,8 @@ def dflash_chunk_attention(geom, layer, q, kv_pool, block_table, cu_rows, ctx_le
                            stream=None):
     """q, out bf16 CUDA tensors [n_rows, hq, head_dim] (row-strided views
     allowed); block_table int32 [B, M], cu_rows int32 [B + 1], ctx_len and kv_len
-    int32 [B]; workspace: uint8 tensor of dflash_chunk_attention_workspace_bytes
+    int32 [B] (n_rows = q's rows, B = kv_len's length; the others may be longer);
+    sinks fp32 [hq]; workspace: uint8 tensor of dflash_chunk_attention_workspace_bytes
     bytes (None where that is 0)."""
     rc = (_calls or _load_calls()).chunk_attention(geom, layer, q, kv_pool, block_table, cu_rows,
                                                    ctx_len, kv_len, out, workspace, window, sinks,

@@ -2,9 +2,9 @@
 
 Each translation unit under ``csrc/`` compiles in parallel with nvcc; the
 objects link into one shared library next to this file.  The CUDA runtime is
-linked statically, so the library depends only on the driver.  ``csrc/calls.c``,
+linked statically, so the library depends only on the driver.  ``csrc/calls.cpp``,
 the CPython module that marshals the ragged-chunk calls, compiles beside it with
-gcc.
+g++ against the headers of the installed torch.
 
     python -m context_kv_update_gb300.build            # build if stale
     python -m context_kv_update_gb300.build --force
@@ -24,7 +24,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libdflash.so")
-CALLS_SRC = os.path.join(CSRC, "calls.c")
+CALLS_SRC = os.path.join(CSRC, "calls.cpp")
 CALLS_PATH = os.path.join(HERE, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -75,22 +75,32 @@ def _compile(src: str, extra=()) -> str:
 
 
 def _build_calls() -> None:
+    import torch
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
     tmp = CALLS_PATH + ".tmp"
-    cmd = [shutil.which("gcc") or "cc", "-O2", "-Wall", "-Werror", "-fPIC", "-shared",
-           "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"], CALLS_SRC, "-o", tmp]
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-Wall", "-Werror", "-fPIC",
+           "-shared", "-fvisibility=hidden",
+           f'-DDFLASH_TORCH_VERSION="{torch.__version__}"',
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(at, "include"),
+           "-isystem", os.path.join(cuda, "include"), CALLS_SRC, "-o", tmp,
+           "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"gcc failed on calls.c:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"g++ failed on calls.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALLS_PATH)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    if force or _older(LIB_PATH, _deps()):
-        _build_lib(verbose_ptxas)
-    # last: the library is there for the calls that need nothing else, even where
-    # the module does not compile
-    if force or _calls_stale():
-        _build_calls()
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        calls = ex.submit(_build_calls) if force or _calls_stale() else None
+        if force or _older(LIB_PATH, _deps()):
+            _build_lib(verbose_ptxas)
+        # the library is there for the calls that need nothing else, even where the
+        # module does not compile
+        if calls:
+            calls.result()
     return LIB_PATH
 
 
