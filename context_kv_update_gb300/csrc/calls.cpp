@@ -175,6 +175,16 @@ int64_t row_width(const dflash_geom *g, int heads) {
   return g->kind == DFLASH_KIND_GQA ? static_cast<int64_t>(heads) * g->head_dim : 0;
 }
 
+// The entry point called without the interpreter's lock: a launch waits where the GPU's
+// queue is full, and what it waits for may need another Python thread.
+template <class F>
+PyObject *unlocked(F f) {
+  PyThreadState *saved = PyEval_SaveThread();
+  const int rc = f();  // a C entry point: no exceptions
+  PyEval_RestoreThread(saved);
+  return PyLong_FromLong(rc);
+}
+
 // A call with `want` arguments; C++ exceptions become Python's.
 template <class F>
 PyObject *call(Py_ssize_t n, Py_ssize_t want, F f) {
@@ -212,8 +222,10 @@ PyObject *chunk_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
       o[i] = t.ints(fields.o[i], kOutKeys[i], i == 0 ? B + 1.0 : i < 4 ? B : i == 4 ? 1 : n_rows);
     const dflash_stream_t stream = t.stream(a[11]);
     const dflash_chunk_outputs out = {o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7], o[8]};
-    return PyLong_FromLong(plan_fn(g, B, n_rows, n_new, ctx, have, tbl, free_pages, n_free, range,
-                                   valid, max_ctx, &out, st, stream));
+    return unlocked([&] {
+      return plan_fn(g, B, n_rows, n_new, ctx, have, tbl, free_pages, n_free, range, valid, max_ctx,
+                     &out, st, stream);
+    });
   });
 }
 
@@ -238,8 +250,10 @@ PyObject *chunk_rope_store(PyObject *, PyObject *const *a, Py_ssize_t n) {
                *gk = t.dense(a[12], "gamma_k", at::kBFloat16, g->head_dim);
     int32_t *st = t.ints(a[13], "dev_status", 1);
     const dflash_stream_t stream = t.stream(a[14]);
-    return PyLong_FromLong(rope_fn(g, layer, n_rows, spec.get(), q, qs, k, ks, v, vs, gq, gk, pos,
-                                   page, slot, q_out, os, pool, st, stream));
+    return unlocked([&] {
+      return rope_fn(g, layer, n_rows, spec.get(), q, qs, k, ks, v, vs, gq, gk, pos, page, slot,
+                     q_out, os, pool, st, stream);
+    });
   });
 }
 
@@ -268,9 +282,10 @@ PyObject *chunk_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int mode = integer(a[13]), segments = integer(a[14]);
     int32_t *st = t.ints(a[15], "dev_status", 1);
     const dflash_stream_t stream = t.stream(a[16]);
-    return PyLong_FromLong(attn_fn(g, B, layer, n_rows, q, qs, pool, tbl, cu, ctx, kv, window,
-                                   sinks, static_cast<float>(scale), mode, segments, ws, ws_bytes,
-                                   out, os, st, stream));
+    return unlocked([&] {
+      return attn_fn(g, B, layer, n_rows, q, qs, pool, tbl, cu, ctx, kv, window, sinks,
+                     static_cast<float>(scale), mode, segments, ws, ws_bytes, out, os, st, stream);
+    });
   });
 }
 
