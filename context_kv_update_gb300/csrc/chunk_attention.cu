@@ -313,7 +313,9 @@ __device__ __forceinline__ Work describe(const ChunkParams &p, int block, int se
 // the dearest first: claimed in the requests' own order, a long one that comes late keeps one
 // SM at work when the others have nothing left (64 single tokens over up to 8192 keys
 // 226 us, so 210; 32 of them 139 and 107, 256 over up to 2048 keys 274 and 248).  Every
-// block sorts for itself, all its threads together (one warp alone took 10 us for 256).
+// block sorts for itself, all its threads together (one warp alone took 10 us for 256),
+// and reports what makes no sense: which of them run is not known (a claimed one does
+// not come here), and their order is not either.
 constexpr int kSortLanes = 8, kSorted = 32 * kSortLanes;
 struct Order {  // lane l holds places l, l + 32, ...
   int r[kSortLanes], end[kSortLanes];  // the request at a place, where its work tiles end
@@ -332,7 +334,7 @@ __device__ __forceinline__ void sort_requests(const ChunkParams &p, int shift, i
                        ? static_cast<int>((static_cast<int64_t>(q.b) * p.G) >> shift) + i + 1
                        : all;
     count = min(max(to - from, 0), all);
-    if (check_request(p, blockIdx.x == 0 && blockIdx.z == 0, &q) && q.b > q.a) {
+    if (check_request(p, true, &q) && q.b > q.a) {
       int lo, hi;
       key_range(p, q.c + q.b - q.a - 1, q.kv, &lo, &hi);
       if (lo <= hi)  // one row tile is done in half the steps of two
