@@ -718,6 +718,9 @@ DFLASH_API int dflash_chunk_rope_store(const dflash_geom *g, int layer, int n_ro
  * DFLASH_DEV_KV_LEN_RANGE; a visible key on a page outside the pool is masked
  * and flags DFLASH_DEV_BAD_PAGE; ctx_len < 0 or cu_rows that do not ascend
  * within [0, n_rows] give the request no rows and flag DFLASH_DEV_BAD_ROWS.
+ * The offsets also place the work: where they do not ascend, rows of other
+ * requests may be left as they are too, and a row that two requests claim holds
+ * either's result.  No other memory is touched.
  *
  * q            device bf16, row t at + t * q_row_stride elements, [hq,
  *              head_dim] contiguous.  out likewise with out_row_stride.
