@@ -971,6 +971,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!active) {  // its rows of P may hold anything: they reach no other row
           ptx::tc_fence_before();
+          __syncwarp();  // all lanes' zeros are written
           if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&p_full[g]));
           continue;
         }
