@@ -622,9 +622,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           volatile int dummy = 0;
-          have = __all_sync(0xffffffffu,
-                            chunk_wait<false, 4>(ptx::smem_u32(claim), claims & 1, &dummy)) &&
-                 claimed_block(answer, &block, &seg);
+          const bool told = __all_sync(
+              0xffffffffu, chunk_wait<false, 4>(ptx::smem_u32(claim), claims & 1, &dummy));
+          if (!told) *abort_flag = 1;  // a block may be lost: reported
+          have = told && claimed_block(answer, &block, &seg);
           __syncwarp();
           ++claims;
           last = !have;  // none left: not to be asked again
