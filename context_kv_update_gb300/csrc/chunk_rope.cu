@@ -29,7 +29,8 @@ struct TurnFreqs {
 
 struct RopeStoreParams {
   int n_rows, hq, nkv, hd, rot, layout, P, NP, layer;
-  int rows, lph;  // rows of a CTA, lanes of a head
+  int rows, lph;   // rows of a CTA, lanes of a head
+  int skip_group;  // tests only: of each CTA's groups the one that is not loaded (-1: off)
   float eps, inv_hd, mag;
   const uint16_t *q, *k, *v;
   int64_t qs, ks, vs, qos;
@@ -134,7 +135,8 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 2)
   // this warp's row of a group, its share of the row's heads
   const int wpr = kRopeWarps / p.rows, rr = warp / wpr, part = warp - rr * wpr;
   ptx::griddep_launch();
-  auto load = [&](int group, int stage) {  // by thread 0
+  auto load = [&](int group, int stage, int nth) {  // by thread 0
+    if (nth == p.skip_group) return;
     const int r0 = group * p.rows, rows = min(p.rows, p.n_rows - r0);
     const uint32_t bar = ptx::smem_u32(&s_bar[stage]);
     ptx::mbar_arrive_expect_tx(bar, rows * row_bytes);
@@ -154,8 +156,8 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 2)
     ptx::mbar_init(ptx::smem_u32(&s_bar[1]), 1);
     ptx::fence_mbar_init();
     ptx::griddep_wait();
-    load(blockIdx.x, 0);
-    if (blockIdx.x + gridDim.x < groups) load(blockIdx.x + gridDim.x, 1);
+    load(blockIdx.x, 0, 0);
+    if (blockIdx.x + gridDim.x < groups) load(blockIdx.x + gridDim.x, 1, 1);
   }
   ptx::griddep_wait();
   struct Place {
@@ -278,8 +280,8 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 2)
   };
 
   uint32_t phase = 0u;  // bit s: of stage s
-  int stage = 0;
-  for (int group = blockIdx.x; group < groups; group += gridDim.x) {
+  int stage = 0, nth = 0;
+  for (int group = blockIdx.x; group < groups; group += gridDim.x, ++nth) {
     const int t = group * p.rows + rr;
     const Place now = here;
     here = place(group + gridDim.x);
@@ -309,8 +311,17 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 2)
         }
       }
     }
-    __syncthreads();  // the stage and the angles are free
-    if (threadIdx.x == 0 && group + 2 * gridDim.x < groups) load(group + 2 * gridDim.x, stage);
+    if (__syncthreads_or(!got)) {  // wind down: the copies in flight land before the CTA ends
+      for (int i = 0; i < 2 && threadIdx.x == 0; ++i, stage ^= 1) {
+        volatile int dummy = 0;
+        if (group + i * gridDim.x < groups)
+          ptx::mbar_wait(ptx::smem_u32(&s_bar[stage]), (phase >> stage) & 1u, &dummy);
+      }
+      return;
+    }
+    // the stage and the angles are free
+    if (threadIdx.x == 0 && group + 2 * gridDim.x < groups)
+      load(group + 2 * gridDim.x, stage, nth + 2);
     phase ^= 1u << stage;
     stage ^= 1;
   }
@@ -428,6 +439,7 @@ cudaError_t launch_chunk_rope_store(const dflash_geom &g, int layer, int n_rows,
   p.q_out = static_cast<uint16_t *>(q_out);
   p.pool = static_cast<uint16_t *>(pool);
   p.st = st;
+  p.skip_group = attention_test_skip_tile_value();
   struct Table {
     dflash_rope_spec spec;
     double theta;

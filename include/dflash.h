@@ -759,7 +759,8 @@ DFLASH_API int dflash_chunk_attention(const dflash_geom *g, int B, int layer, in
  * While set (tile >= 0), every dflash_block_attention and
  * dflash_chunk_attention launched from the calling host thread leaves key tile
  * `tile` of each CTA's segment unloaded (MLA: the first 64-key half of it;
- * chunks: its keys, not its values): the wait for it runs out (about 2 s),
+ * chunks: its keys, not its values), every dflash_chunk_rope_store group
+ * `tile` of each CTA's groups of rows: the wait for it runs out (about 2 s),
  * the kernel winds down, ORs
  * DFLASH_DEV_WAIT_TIMEOUT into *dev_status and the context stays usable.
  * tile < 0 turns it off (the default).  Never set it in production.

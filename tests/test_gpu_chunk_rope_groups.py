@@ -118,3 +118,29 @@ def test_rope_rows_wider_than_shared_memory(dl):  # noqa: F811
     for layout in ("half", "pairs"):
         check(dl, rows=21, hq=420, nkv=2, hd=128, rot=128, layout=layout, gamma=True,
               in_place=True, packed=True, seed=4)
+
+
+@pytest.mark.parametrize("group", [0, 1, 3])
+def test_unloaded_group_times_out_cleanly(dl, group):  # noqa: F811
+    """The bounded waits: one group of rows is not loaded, the CTAs wind down with
+    their copies landed, the status is set, and the next call is right."""
+    import torch
+    rows = 8 * 2 * sm_count() * 5 + 3
+    g = geom(dl, hq=2, nkv=1, hd=64, P=16, NP=4)
+    q, _ = bf16(np.ones((rows, 128), np.float32))
+    pos, out = dev(np.zeros(rows, np.int32)), torch.empty_like(q)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    call = lambda: dl.dflash_chunk_rope_store(  # noqa: E731
+        g, 0, rope_spec(dl, "half", 64), q, None, None, pos, None, None, out, None, dev_status=st)
+    dl.dflash_test_attention_skip_tile(group)
+    try:
+        call()
+        torch.cuda.synchronize()
+    finally:
+        dl.dflash_test_attention_skip_tile(-1)
+    assert int(st.item()) == dl._lib.DEV_WAIT_TIMEOUT
+    st.zero_()
+    out.zero_()
+    call()
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and torch.equal(out, q)
