@@ -681,7 +681,7 @@ DFLASH_API int dflash_chunk_plan(const dflash_geom *g, int B, int n_rows, const 
  * gamma_q, gamma_k  device bf16 [head_dim] or NULL.
  * row_pos, row_page, row_slot  device int32 [n_rows] (dflash_chunk_plan).
  * Errors: DFLASH_ERR_INVALID_ARG (null pointers, n_rows < 0, strides below the
- * row widths, q / k / v / q_out / kv_pool not 16-byte aligned or strides not a
+ * row widths, q / k / v / q_out / kv_pool or a gain not 16-byte aligned, strides not a
  * multiple of 8, a bad spec: unknown layout or scaling, factor < 1, trained_ctx
  * < 1, betas not positive and in order, values not finite),
  * DFLASH_ERR_UNSUPPORTED_GEOM (MLA, head_dim not a multiple of 8 up to 256,
@@ -720,7 +720,7 @@ DFLASH_API int dflash_chunk_rope_store(const dflash_geom *g, int layer, int n_ro
  * within [0, n_rows] give the request no rows and flag DFLASH_DEV_BAD_ROWS.
  * The offsets also place the work: where they do not ascend, rows of other
  * requests may be left as they are too, and a row that two requests claim holds
- * either's result.  No other memory is touched.
+ * no result in particular.  No other memory is touched.
  *
  * q            device bf16, row t at + t * q_row_stride elements, [hq,
  *              head_dim] contiguous.  out likewise with out_row_stride.
@@ -728,19 +728,27 @@ DFLASH_API int dflash_chunk_rope_store(const dflash_geom *g, int layer, int n_ro
  * ctx_len      device int32 [B] (before the chunk); kv_len device int32 [B]
  *              (after it: dflash_chunk_plan's seq_lens).
  * sinks        device fp32 [hq] or NULL.  scale <= 0 selects 1/sqrt(head_dim).
- * num_segments 0 = automatic (from the sizes, the table's width and the
- *              window); else >= 1, the number of slices each row tile's keys are
- *              cut into (partials joined by a second launch).
+ * num_segments 0 = automatic, from the sizes: the lengths are on the device, so
+ *              the table's width (or the window, if shorter) stands for the longest
+ *              key span.  A table much wider than that is cut into more segments
+ *              than pay: a prompt of 4096 rows takes 117 us behind a table of its own
+ *              length and 181 (two segments, 136 MB of workspace) behind one of 32768 keys.
+ *              A caller that knows its lengths gives the number itself.
+ *              >= 1: the number of slices each row tile's keys are cut into
+ *              (partials joined by a second launch; 1: none, no workspace).
  * workspace    device scratch of dflash_chunk_attention_workspace_bytes(g, B,
  *              n_rows, num_segments) bytes (0: none needed, may be NULL),
  *              16-byte aligned, clobbered; calls whose GPU work overlaps need
- *              one each.
+ *              one each.  With num_segments 0 the size does not fall with B and
+ *              n_rows (fewer rows, more segments): a buffer for calls of several
+ *              sizes is the largest of theirs.  With a given number it only grows.
  * Errors: DFLASH_ERR_INVALID_ARG (null or misaligned pointers, strides below
- * hq * head_dim or not a multiple of 8, bad indices, scale not finite, window
- * < 0, unknown mask_mode, num_segments > 65535), DFLASH_ERR_UNSUPPORTED_GEOM (MLA, head_dim not 64
- * or 128, hq not a multiple of nkv, page_size not a multiple of 8 that divides
- * 128 or is a multiple of 128, pool rows >= 2^31, max_pages * page_size >
- * 2^31 - 256, n_rows * hq >= 2^31, B * nkv >= 2^30), DFLASH_ERR_WORKSPACE_TOO_SMALL, DFLASH_ERR_CUDA.
+ * hq * head_dim or not a multiple of 8, bad indices, hq not a multiple of nkv, scale not
+ * finite, window < 0, unknown mask_mode, num_segments > 65535),
+ * DFLASH_ERR_UNSUPPORTED_GEOM (MLA, head_dim not 64 or 128, page_size not a multiple
+ * of 8 that divides 128 or is a multiple of 128, pool rows >= 2^31, max_pages *
+ * page_size > 2^31 - 256, n_rows * hq >= 2^31, B * nkv >= 2^30),
+ * DFLASH_ERR_WORKSPACE_TOO_SMALL, DFLASH_ERR_CUDA.
  * ------------------------------------------------------------------- */
 DFLASH_API int dflash_chunk_attention_num_segments(const dflash_geom *g, int B, int n_rows);
 DFLASH_API size_t dflash_chunk_attention_workspace_bytes(const dflash_geom *g, int B, int n_rows,
