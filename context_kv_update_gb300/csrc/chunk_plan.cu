@@ -11,9 +11,9 @@
 // lengths; a row's table or free-list entry; the stores).  So every CTA repeats
 // the sums over all requests in shared memory instead of waiting for another
 // CTA's, which would take a second launch or a grid barrier, and its rows find
-// their request by binary search there.  Calls back to back: 5.2 us for 64
-// requests of one row, 4.9 for 1024 requests and 8192 rows, 4.5 for 16384 rows of 4
-// requests (the first is the host's rate of launches, 4.8 on the device).
+// their request by binary search there.  Calls back to back: 5.4 us for 64
+// requests of one row, 4.9 for 1024 requests and 8192 rows, 4.1 for 16384 rows of 4
+// requests.
 // Entries of the page table below the owned count are
 // only read and those from it on only written, and rows on new pages take the
 // id from the free list, so CTAs never read what another one writes.
