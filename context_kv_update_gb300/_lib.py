@@ -55,7 +55,10 @@ EXPORTS = ("dflash_step_bookkeeping", "dflash_ctx_workspace_bytes", "dflash_ctx_
            "dflash_ctx_kv_prefill", "dflash_test_attention_skip_tile",
            "dflash_block_scatter_attention", "dflash_chunk_plan", "dflash_chunk_rope_store",
            "dflash_chunk_attention", "dflash_chunk_attention_num_segments",
-           "dflash_chunk_attention_workspace_bytes")
+           "dflash_chunk_attention_workspace_bytes", "dflash_cache8_code_bytes",
+           "dflash_cache8_scale_bytes", "dflash_chunk_rope_store8", "dflash_chunk_read8",
+           "dflash_chunk_attention8", "dflash_chunk_attention8_num_segments",
+           "dflash_chunk_attention8_workspace_bytes")
 
 
 class DflashError(RuntimeError):
@@ -109,6 +112,12 @@ class RopeSpec(ctypes.Structure):
                 ("scaling", ctypes.c_int32), ("trained_ctx", ctypes.c_int32),
                 ("factor", ctypes.c_double), ("beta_fast", ctypes.c_double),
                 ("beta_slow", ctypes.c_double), ("magnitude", ctypes.c_double)]
+
+
+class Cache8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("block", ctypes.c_int32), ("reserved0", ctypes.c_int32)]
+
 
 _lib = None
 _calls = None  # the module that marshals the ragged-chunk calls, once one is made
@@ -185,20 +194,39 @@ def load():
     lib.dflash_chunk_attention.argtypes = [G, ctypes.c_int, ctypes.c_int, ctypes.c_int, vp, i64,
                                            vp, vp, vp, vp, vp, i32, vp, ctypes.c_float,
                                            ctypes.c_int, ctypes.c_int, vp, sz, vp, i64, vp, vp]
+    C8 = ctypes.POINTER(Cache8)
+    lib.dflash_cache8_code_bytes.argtypes = [G]
+    lib.dflash_cache8_code_bytes.restype = sz
+    lib.dflash_cache8_scale_bytes.argtypes = [G, ctypes.c_int]
+    lib.dflash_cache8_scale_bytes.restype = sz
+    lib.dflash_chunk_rope_store8.argtypes = [G, ctypes.c_int, ctypes.c_int,
+                                             ctypes.POINTER(RopeSpec), vp, i64, vp, i64, vp, i64,
+                                             vp, vp, vp, vp, vp, vp, i64, C8, vp, vp]
+    lib.dflash_chunk_read8.argtypes = [G, ctypes.c_int, ctypes.c_int, C8, vp, vp, vp, i64, vp, i64,
+                                       vp, vp]
+    lib.dflash_chunk_attention8_num_segments.argtypes = [G, ctypes.c_int, ctypes.c_int]
+    lib.dflash_chunk_attention8_workspace_bytes.argtypes = [G, ctypes.c_int, ctypes.c_int,
+                                                            ctypes.c_int]
+    lib.dflash_chunk_attention8_workspace_bytes.restype = sz
+    lib.dflash_chunk_attention8.argtypes = [G, ctypes.c_int, ctypes.c_int, ctypes.c_int, vp, i64,
+                                            C8, vp, vp, vp, vp, i32, vp, ctypes.c_float,
+                                            ctypes.c_int, ctypes.c_int, vp, sz, vp, i64, vp, vp]
     for name in ("dflash_step_bookkeeping", "dflash_ctx_kv_update", "dflash_block_kv_scatter",
                  "dflash_block_attention", "dflash_attention_num_segments", "dflash_abi_version",
                  "dflash_ctx_kv_project", "dflash_ctx_kv_commit", "dflash_q_norm_rope",
                  "dflash_pack_weights", "dflash_strict_accept", "dflash_embedding_gather",
                  "dflash_ctx_kv_prefill", "dflash_block_scatter_attention", "dflash_chunk_plan",
                  "dflash_chunk_rope_store", "dflash_chunk_attention",
-                 "dflash_chunk_attention_num_segments"):
+                 "dflash_chunk_attention_num_segments", "dflash_chunk_rope_store8",
+                 "dflash_chunk_read8", "dflash_chunk_attention8",
+                 "dflash_chunk_attention8_num_segments"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
 
 
 def _load_calls():
-    """The module of csrc/calls.cpppp, bound to the library's entry points.  Only the
+    """The module of csrc/calls.cpp, bound to the library's entry points.  Only the
     ragged-chunk calls need it; load() and every other call do without."""
     global _calls
     if _calls is None:
@@ -214,7 +242,8 @@ def _load_calls():
                               f"{torch.__version__}: build it again with "
                               "`python -m context_kv_update_gb300.build --force`")
         calls.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
-            lib.dflash_chunk_plan, lib.dflash_chunk_rope_store, lib.dflash_chunk_attention)])
+            lib.dflash_chunk_plan, lib.dflash_chunk_rope_store, lib.dflash_chunk_attention,
+            lib.dflash_chunk_rope_store8, lib.dflash_chunk_read8, lib.dflash_chunk_attention8)])
         _calls = calls
     return _calls
 
@@ -516,6 +545,62 @@ def dflash_chunk_attention(geom, layer, q, kv_pool, block_table, cu_rows, ctx_le
                                                    stream)
     if rc:
         _check("dflash_chunk_attention", rc)
+
+
+def dflash_cache8_code_bytes(geom) -> int:
+    return int(load().dflash_cache8_code_bytes(ctypes.byref(geom)))
+
+
+def dflash_cache8_scale_bytes(geom, block) -> int:
+    return int(load().dflash_cache8_scale_bytes(ctypes.byref(geom), int(block)))
+
+
+def dflash_chunk_rope_store8(geom, layer, rope, q, k, v, row_pos, row_page, row_slot, q_out, codes,
+                             scales, block, *, gamma_q=None, gamma_k=None, dev_status=None,
+                             stream=None):
+    """dflash_chunk_rope_store into a cache held in 8 bits; rope may be None (nothing is
+    turned).  codes: uint8 or float8_e4m3fn CUDA tensor [L, num_pool_pages, 2, nkv, page_size,
+    head_dim]; scales: uint8 or float8_e8m0fnu [L, num_pool_pages, 2, nkv, page_size / block];
+    block: 16, 32 or 64 tokens that share a scale."""
+    rc = (_calls or _load_calls()).chunk_rope_store8(geom, layer, rope, q, k, v, row_pos, row_page,
+                                                     row_slot, q_out, codes, scales, block,
+                                                     gamma_q, gamma_k, dev_status, stream)
+    if rc:
+        _check("dflash_chunk_rope_store8", rc)
+
+
+def dflash_chunk_read8(geom, layer, codes, scales, block, row_page, row_slot, k_out, v_out, *,
+                       dev_status=None, stream=None):
+    """Rows (row_page, row_slot: int32 [n_rows], n_rows = length of row_page) of a cache held in
+    8 bits into k_out and v_out, bf16 [n_rows, nkv, head_dim] (row-strided views allowed); one of
+    them may be None."""
+    rc = (_calls or _load_calls()).chunk_read8(geom, layer, codes, scales, block, row_page,
+                                               row_slot, k_out, v_out, dev_status, stream)
+    if rc:
+        _check("dflash_chunk_read8", rc)
+
+
+def dflash_chunk_attention8_num_segments(geom, B, n_rows) -> int:
+    return int(load().dflash_chunk_attention8_num_segments(ctypes.byref(geom), B, n_rows))
+
+
+def dflash_chunk_attention8_workspace_bytes(geom, B, n_rows, num_segments=0) -> int:
+    return int(load().dflash_chunk_attention8_workspace_bytes(ctypes.byref(geom), B, n_rows,
+                                                              num_segments))
+
+
+def dflash_chunk_attention8(geom, layer, q, codes, scales, block, block_table, cu_rows, ctx_len,
+                            kv_len, out, workspace=None, *, window=0, sinks=None, scale=None,
+                            mask_mode=MASK_CAUSAL_TAIL, num_segments=0, dev_status=None,
+                            stream=None):
+    """dflash_chunk_attention over a cache held in 8 bits (codes, scales, block as in
+    dflash_chunk_rope_store8); workspace: dflash_chunk_attention8_workspace_bytes bytes."""
+    rc = (_calls or _load_calls()).chunk_attention8(geom, layer, q, codes, scales, block,
+                                                    block_table, cu_rows, ctx_len, kv_len, out,
+                                                    workspace, window, sinks, scale, mask_mode,
+                                                    num_segments, dev_status, stream)
+    if rc:
+        _check("dflash_chunk_attention8", rc)
 
 
 def dflash_test_attention_skip_tile(tile: int) -> None:

@@ -18,6 +18,7 @@
 
 #include <cstdint>
 #include <cstring>
+#include <optional>
 
 #include "../../include/dflash.h"
 
@@ -26,6 +27,9 @@ namespace {
 decltype(&dflash_chunk_plan) plan_fn;
 decltype(&dflash_chunk_rope_store) rope_fn;
 decltype(&dflash_chunk_attention) attn_fn;
+decltype(&dflash_chunk_rope_store8) rope8_fn;
+decltype(&dflash_chunk_read8) read8_fn;
+decltype(&dflash_chunk_attention8) attn8_fn;
 PyObject *s_cuda_stream, *out_keys[9];
 const char *const kOutKeys[9] = {"cu_rows", "n_pages", "alloc_limit", "seq_lens", "free_head",
                                  "row_req", "row_pos", "row_page",    "row_slot"};
@@ -171,6 +175,23 @@ double pool_values(const dflash_geom *g) {
   if (g->kind != DFLASH_KIND_GQA) return 0;
   return 2.0 * product(g->num_layers, g->num_pool_pages, g->nkv, g->page_size, g->head_dim);
 }
+// A cache in 8 bits: codes as bytes or e4m3, scales as bytes or e8m0.
+at::ScalarType byte_type(PyObject *o, at::ScalarType other) {
+  return o != Py_None && THPVariable_Check(o) && THPVariable_Unpack(o).scalar_type() == other
+             ? other
+             : at::kByte;
+}
+dflash_cache8 cache8(Tensors &t, const dflash_geom *g, PyObject *codes, PyObject *scales,
+                     PyObject *block) {
+  dflash_cache8 c = {};
+  c.block = integer(block);
+  const double cells = pool_values(g);
+  c.codes = t.dense(codes, "codes", byte_type(codes, at::kFloat8_e4m3fn), cells);
+  // a block that makes no sense is refused by the entry point
+  c.scales = t.dense(scales, "scales", byte_type(scales, at::kFloat8_e8m0fnu),
+                     c.block > 0 && g->head_dim > 0 ? cells / g->head_dim / c.block : 0);
+  return c;
+}
 int64_t row_width(const dflash_geom *g, int heads) {
   return g->kind == DFLASH_KIND_GQA ? static_cast<int64_t>(heads) * g->head_dim : 0;
 }
@@ -289,11 +310,92 @@ PyObject *chunk_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
-// plan, rope and attention addresses
+// geom, layer, rope, q, k, v, row_pos, row_page, row_slot, q_out, codes, scales, block, gamma_q,
+// gamma_k, dev_status, stream
+PyObject *chunk_rope_store8(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return call(n, 17, [&] {
+    const Structure<dflash_geom> geom(a[0]);
+    const dflash_geom *g = geom.get();
+    std::optional<Structure<dflash_rope_spec>> spec;
+    if (a[2] != Py_None) spec.emplace(a[2]);
+    const int layer = integer(a[1]), n_rows = count(a[6], "row_pos");
+    const int64_t wq = row_width(g, g->hq), wk = row_width(g, g->nkv);
+    int64_t qs, ks, vs, os;
+    Tensors t;
+    const void *q = t.rows(a[3], "q", n_rows, wq, &qs), *k = t.rows(a[4], "k", n_rows, wk, &ks),
+               *v = t.rows(a[5], "v", n_rows, wk, &vs);
+    const int32_t *pos = t.ints(a[6], "row_pos", n_rows), *page = t.ints(a[7], "row_page", n_rows),
+                  *slot = t.ints(a[8], "row_slot", n_rows);
+    void *q_out = t.rows(a[9], "q_out", n_rows, wq, &os);
+    const dflash_cache8 cache = cache8(t, g, a[10], a[11], a[12]);
+    const void *gq = t.dense(a[13], "gamma_q", at::kBFloat16, g->head_dim),
+               *gk = t.dense(a[14], "gamma_k", at::kBFloat16, g->head_dim);
+    int32_t *st = t.ints(a[15], "dev_status", 1);
+    const dflash_stream_t stream = t.stream(a[16]);
+    return unlocked([&] {
+      return rope8_fn(g, layer, n_rows, spec ? spec->get() : nullptr, q, qs, k, ks, v, vs, gq, gk,
+                      pos, page, slot, q_out, os, &cache, st, stream);
+    });
+  });
+}
+
+// geom, layer, codes, scales, block, row_page, row_slot, k_out, v_out, dev_status, stream
+PyObject *chunk_read8(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return call(n, 11, [&] {
+    const Structure<dflash_geom> geom(a[0]);
+    const dflash_geom *g = geom.get();
+    const int layer = integer(a[1]), n_rows = count(a[5], "row_page");
+    const int64_t wk = row_width(g, g->nkv);
+    int64_t ks, vs;
+    Tensors t;
+    const dflash_cache8 cache = cache8(t, g, a[2], a[3], a[4]);
+    const int32_t *page = t.ints(a[5], "row_page", n_rows), *slot = t.ints(a[6], "row_slot", n_rows);
+    void *k = t.rows(a[7], "k_out", n_rows, wk, &ks), *v = t.rows(a[8], "v_out", n_rows, wk, &vs);
+    int32_t *st = t.ints(a[9], "dev_status", 1);
+    const dflash_stream_t stream = t.stream(a[10]);
+    return unlocked([&] {
+      return read8_fn(g, layer, n_rows, &cache, page, slot, k, ks, v, vs, st, stream);
+    });
+  });
+}
+
+// geom, layer, q, codes, scales, block, block_table, cu_rows, ctx_len, kv_len, out, workspace,
+// window, sinks, scale, mask_mode, num_segments, dev_status, stream
+PyObject *chunk_attention8(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return call(n, 19, [&] {
+    const Structure<dflash_geom> geom(a[0]);
+    const dflash_geom *g = geom.get();
+    const int layer = integer(a[1]), n_rows = count(a[2], "q"), B = count(a[9], "kv_len");
+    const int64_t wq = row_width(g, g->hq);
+    int64_t qs, os;
+    size_t ws_bytes;
+    Tensors t;
+    const void *q = t.rows(a[2], "q", n_rows, wq, &qs);
+    const dflash_cache8 cache = cache8(t, g, a[3], a[4], a[5]);
+    const int32_t *tbl = t.ints(a[6], "block_table", product(B, g->max_pages)),
+                  *cu = t.ints(a[7], "cu_rows", B + 1.0), *ctx = t.ints(a[8], "ctx_len", B),
+                  *kv = t.ints(a[9], "kv_len", B);
+    void *out = t.rows(a[10], "out", n_rows, wq, &os);
+    void *ws = t.scratch(a[11], "workspace", &ws_bytes);
+    const int window = integer(a[12]);
+    const float *sinks = t.dense<float>(a[13], "sinks", at::kFloat, g->hq);
+    const double scale = a[14] == Py_None ? 0.0 : PyFloat_AsDouble(a[14]);
+    if (scale == -1.0 && PyErr_Occurred()) throw PythonError{};
+    const int mode = integer(a[15]), segments = integer(a[16]);
+    int32_t *st = t.ints(a[17], "dev_status", 1);
+    const dflash_stream_t stream = t.stream(a[18]);
+    return unlocked([&] {
+      return attn8_fn(g, B, layer, n_rows, q, qs, &cache, tbl, cu, ctx, kv, window, sinks,
+                      static_cast<float>(scale), mode, segments, ws, ws_bytes, out, os, st, stream);
+    });
+  });
+}
+
+// the entry points' addresses: plan, rope, attention, and the three over a cache in 8 bits
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  return call(n, 3, [&] {
-    void *f[3];
-    for (int i = 0; i < 3; ++i) {
+  return call(n, 6, [&] {
+    void *f[6];
+    for (int i = 0; i < 6; ++i) {
       f[i] = PyLong_AsVoidPtr(a[i]);
       if (!f[i] && PyErr_Occurred()) throw PythonError{};
       if (!f[i]) refuse(PyExc_ValueError, "null entry point");
@@ -301,6 +403,9 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     std::memcpy(&plan_fn, &f[0], sizeof f[0]);
     std::memcpy(&rope_fn, &f[1], sizeof f[1]);
     std::memcpy(&attn_fn, &f[2], sizeof f[2]);
+    std::memcpy(&rope8_fn, &f[3], sizeof f[3]);
+    std::memcpy(&read8_fn, &f[4], sizeof f[4]);
+    std::memcpy(&attn8_fn, &f[5], sizeof f[5]);
     return Py_NewRef(Py_None);
   });
 }
@@ -314,6 +419,9 @@ PyMethodDef methods[] = {
     {"chunk_plan", method(chunk_plan), METH_FASTCALL, nullptr},
     {"chunk_rope_store", method(chunk_rope_store), METH_FASTCALL, nullptr},
     {"chunk_attention", method(chunk_attention), METH_FASTCALL, nullptr},
+    {"chunk_rope_store8", method(chunk_rope_store8), METH_FASTCALL, nullptr},
+    {"chunk_read8", method(chunk_read8), METH_FASTCALL, nullptr},
+    {"chunk_attention8", method(chunk_attention8), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

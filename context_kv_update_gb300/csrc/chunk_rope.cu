@@ -12,20 +12,15 @@
 // take 53, 6.2 TB/s (65 with groups of at most four rows); a few rows are bound
 // by latency (16 rows: 4 us on the device).
 #include <algorithm>
-#include <cmath>
-#include <cstring>
 #include <type_traits>
 
+#include "chunk_turn.cuh"
 #include "dflash_internal.cuh"
 #include "f32x2.cuh"
 #include "sm100_ptx.cuh"
 
 namespace dflash {
 namespace {
-
-struct TurnFreqs {
-  uint64_t f[kMaxHeadDim / 2];  // turns per position, 2^64 to a turn
-};
 
 struct RopeStoreParams {
   int n_rows, hq, nkv, hd, rot, layout, P, NP, layer;
@@ -39,14 +34,6 @@ struct RopeStoreParams {
   uint16_t *q_out, *pool;
   int32_t *st;
 };
-
-// cos and sin (times the magnitude) of position p at f turns per position.
-__device__ __forceinline__ float2 turn_cos_sin(int p, uint64_t f, float mag) {
-  const uint64_t t = static_cast<uint64_t>(static_cast<uint32_t>(p)) * f;
-  float s, c;  // top 32 bits: a signed fraction of half a turn in units of 2^-31
-  sincospif(static_cast<float>(static_cast<int32_t>(t >> 32)) * 0x1p-31f, &s, &c);
-  return make_float2(c * mag, s * mag);
-}
 
 // Where the K (kv = 0) or V row of head h goes, or nullptr.
 __device__ __forceinline__ uint16_t *pool_row(const RopeStoreParams &p, int pg, int sl, int kv,
@@ -376,33 +363,6 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Turns per position of every pair, and the factor on cos and sin.
-// (The powers of a 128-wide head take the host ~5 us: the launcher keeps the
-// thread's last table with the specification it was made from.)
-void fill_turn_freqs(TurnFreqs *tf, float *mag, const dflash_rope_spec &r, int rot, double theta) {
-  const double two_pi = 6.283185307179586476925286766559;
-  double j0 = 0.0, j1 = 0.0;
-  *mag = 1.f;
-  if (r.scaling == DFLASH_ROPE_YARN) {
-    const double per = rot / (2.0 * std::log(theta));
-    j0 = std::fmax(std::floor(per * std::log(r.trained_ctx / (two_pi * r.beta_fast))), 0.0);
-    j1 = std::fmin(std::ceil(per * std::log(r.trained_ctx / (two_pi * r.beta_slow))), rot - 1.0);
-    *mag = static_cast<float>(r.magnitude > 0.0 ? r.magnitude : 0.1 * std::log(r.factor) + 1.0);
-  }
-  for (int j = 0; j < rot / 2; ++j) {
-    double f = std::pow(theta, -2.0 * j / rot);
-    if (r.scaling == DFLASH_ROPE_LINEAR) f /= r.factor;
-    if (r.scaling == DFLASH_ROPE_YARN) {
-      const double u = std::fmin(std::fmax((j - j0) / std::fmax(j1 - j0, 1e-3), 0.0), 1.0);
-      f = f / r.factor * u + f * (1.0 - u);
-    }
-    const double turns = f / two_pi;
-    // the fraction of a turn; 2^64 times it is an integer below 2^64 (a
-    // double's 53 bits)
-    tf->f[j] = static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 64));
-  }
-}
-
 }  // namespace
 
 cudaError_t launch_chunk_rope_store(const dflash_geom &g, int layer, int n_rows,
@@ -440,20 +400,9 @@ cudaError_t launch_chunk_rope_store(const dflash_geom &g, int layer, int n_rows,
   p.pool = static_cast<uint16_t *>(pool);
   p.st = st;
   p.skip_group = attention_test_skip_tile_value();
-  struct Table {
-    dflash_rope_spec spec;
-    double theta;
-    float mag;
-    TurnFreqs tf;
-  };
-  static thread_local Table last = {};  // rot_dim 0: made from nothing yet
-  if (std::memcmp(&last.spec, &rope, sizeof(rope)) != 0 || last.theta != g.rope_theta) {
-    last.spec = rope;
-    last.theta = g.rope_theta;
-    fill_turn_freqs(&last.tf, &last.mag, rope, p.rot, g.rope_theta);
-  }
-  const TurnFreqs &tf = last.tf;
-  p.mag = last.mag;
+  const TurnTable &table = turn_table(rope, g.rope_theta);
+  const TurnFreqs &tf = table.tf;
+  p.mag = table.mag;
   // the widest chunk (16 or 8 bytes) that no turning pair of chunks is cut by
   const bool halves = p.layout == DFLASH_ROPE_HALF;
   const int unit = halves ? p.rot / 2 : p.rot;  // a whole number of chunks

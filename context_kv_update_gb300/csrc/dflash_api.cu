@@ -443,6 +443,62 @@ bool rows_ok(const void *p, int64_t stride, int64_t width) {
 // Row strides apply between rows: a single row may have any.
 int64_t row_stride(int n_rows, int64_t stride, int64_t width) { return n_rows > 1 ? stride : width; }
 
+// The rotation that a store is asked for.
+int rope_spec_status(const dflash_geom *g, const dflash_rope_spec &r) {
+  if (r.layout != DFLASH_ROPE_HALF && r.layout != DFLASH_ROPE_PAIRS) return DFLASH_ERR_INVALID_ARG;
+  if (r.scaling != DFLASH_ROPE_PLAIN && r.scaling != DFLASH_ROPE_LINEAR &&
+      r.scaling != DFLASH_ROPE_YARN)
+    return DFLASH_ERR_INVALID_ARG;
+  if (r.rot_dim < 2 || r.rot_dim % 2 != 0 || r.rot_dim > g->head_dim)
+    return DFLASH_ERR_UNSUPPORTED_GEOM;
+  if (r.scaling != DFLASH_ROPE_PLAIN && !(std::isfinite(r.factor) && r.factor >= 1.0))
+    return DFLASH_ERR_INVALID_ARG;
+  if (r.scaling == DFLASH_ROPE_YARN) {
+    if (r.trained_ctx < 1 || !std::isfinite(r.beta_fast) || !std::isfinite(r.magnitude) ||
+        !(r.beta_slow > 0.0 && r.beta_fast >= r.beta_slow))
+      return DFLASH_ERR_INVALID_ARG;
+    if (!(g->rope_theta > 1.0)) return DFLASH_ERR_UNSUPPORTED_GEOM;
+  }
+  return DFLASH_OK;
+}
+
+// The rows of a store: q with q_out, k with v, or all four; strides that apply.
+struct StoreRows {
+  const void *q, *k, *v, *gamma_q, *gamma_k;
+  const int32_t *pos, *page, *slot;
+  const void *q_out;
+  int64_t qs, ks, vs, qos;
+};
+int store_rows_status(const dflash_geom *g, int n_rows, StoreRows &a) {
+  const int64_t wq = static_cast<int64_t>(g->hq) * g->head_dim;
+  const int64_t wk = static_cast<int64_t>(g->nkv) * g->head_dim;
+  if ((a.q == nullptr) != (a.q_out == nullptr) || (a.k == nullptr) != (a.v == nullptr) ||
+      (!a.q && !a.k) || !a.pos)
+    return DFLASH_ERR_INVALID_ARG;
+  a.qs = row_stride(n_rows, a.qs, wq);
+  a.qos = row_stride(n_rows, a.qos, wq);
+  a.ks = row_stride(n_rows, a.ks, wk);
+  a.vs = row_stride(n_rows, a.vs, wk);
+  if (a.q && (!rows_ok(a.q, a.qs, wq) || !rows_ok(a.q_out, a.qos, wq) ||
+              (a.q == a.q_out && a.qs != a.qos)))
+    return DFLASH_ERR_INVALID_ARG;
+  if (a.k && (!rows_ok(a.k, a.ks, wk) || !rows_ok(a.v, a.vs, wk) || !a.page || !a.slot))
+    return DFLASH_ERR_INVALID_ARG;
+  if (!aligned16(a.gamma_q) || !aligned16(a.gamma_k)) return DFLASH_ERR_INVALID_ARG;
+  return DFLASH_OK;
+}
+
+// The geometry of a cache in 8 bits.
+int cache8_geom_status(const dflash_geom *g, int block) {
+  if (g->kind != DFLASH_KIND_GQA || g->head_dim % 16 != 0 || g->head_dim > kMaxHeadDim ||
+      (block != 16 && block != 32 && block != 64) || g->page_size % block != 0)
+    return DFLASH_ERR_UNSUPPORTED_GEOM;
+  return DFLASH_OK;
+}
+int cache8_ptrs_status(const dflash_cache8 &c) {
+  return c.codes && aligned16(c.codes) && c.scales ? DFLASH_OK : DFLASH_ERR_INVALID_ARG;
+}
+
 int chunk_attention_geom_status(const dflash_geom *g, int B, int n_rows) {
   if (g->kind != DFLASH_KIND_GQA || (g->head_dim != 64 && g->head_dim != 128))
     return DFLASH_ERR_UNSUPPORTED_GEOM;
@@ -458,6 +514,29 @@ int chunk_attention_geom_status(const dflash_geom *g, int B, int n_rows) {
       static_cast<long long>(B) * g->nkv >= (1LL << 30))
     return DFLASH_ERR_UNSUPPORTED_GEOM;
   return DFLASH_OK;
+}
+
+// The two attentions of a chunk: arguments by value, then their buffers.
+int chunk_attention_args_status(const dflash_geom *g, int B, int layer, int n_rows, int32_t window,
+                                float scale, int mask_mode, int num_segments) {
+  if (!geom_ok(g) || B < 0 || n_rows < 0 || layer < 0 || layer >= g->num_layers || window < 0 ||
+      num_segments < 0 || num_segments > kMaxChunkSegments || !std::isfinite(scale))
+    return DFLASH_ERR_INVALID_ARG;
+  if (mask_mode != DFLASH_MASK_CAUSAL_TAIL && mask_mode != DFLASH_MASK_BLOCK_BIDIR)
+    return DFLASH_ERR_INVALID_ARG;
+  return chunk_attention_geom_status(g, B, n_rows);
+}
+int chunk_attention_ptrs_status(const dflash_geom &g, int B, int n_rows, const void *q,
+                                int64_t *q_stride, const void *pool, const int32_t *tbl,
+                                const int32_t *cu, const int32_t *ctx, const int32_t *kv,
+                                const void *out, int64_t *out_stride) {
+  if (!tbl || !cu || !ctx) return DFLASH_ERR_INVALID_ARG;
+  if (const int st = attention_ptrs_status(B, q, nullptr, pool, tbl, kv, out)) return st;
+  const int64_t wq = static_cast<int64_t>(g.hq) * g.head_dim;
+  *q_stride = row_stride(n_rows, *q_stride, wq);
+  *out_stride = row_stride(n_rows, *out_stride, wq);
+  return rows_ok(q, *q_stride, wq) && rows_ok(out, *out_stride, wq) ? DFLASH_OK
+                                                                   : DFLASH_ERR_INVALID_ARG;
 }
 
 }  // namespace
@@ -509,42 +588,15 @@ extern "C" int dflash_chunk_rope_store(const dflash_geom *g, int layer, int n_ro
   if (g->kind != DFLASH_KIND_GQA || g->head_dim % 8 != 0 || g->head_dim > kMaxHeadDim ||
       n_rows >= (1 << 30))
     return DFLASH_ERR_UNSUPPORTED_GEOM;
-  const dflash_rope_spec &r = *rope;
-  if (r.layout != DFLASH_ROPE_HALF && r.layout != DFLASH_ROPE_PAIRS) return DFLASH_ERR_INVALID_ARG;
-  if (r.scaling != DFLASH_ROPE_PLAIN && r.scaling != DFLASH_ROPE_LINEAR &&
-      r.scaling != DFLASH_ROPE_YARN)
-    return DFLASH_ERR_INVALID_ARG;
-  if (r.rot_dim < 2 || r.rot_dim % 2 != 0 || r.rot_dim > g->head_dim)
-    return DFLASH_ERR_UNSUPPORTED_GEOM;
-  if (r.scaling != DFLASH_ROPE_PLAIN && !(std::isfinite(r.factor) && r.factor >= 1.0))
-    return DFLASH_ERR_INVALID_ARG;
-  if (r.scaling == DFLASH_ROPE_YARN) {
-    if (r.trained_ctx < 1 || !std::isfinite(r.beta_fast) || !std::isfinite(r.magnitude) ||
-        !(r.beta_slow > 0.0 && r.beta_fast >= r.beta_slow))
-      return DFLASH_ERR_INVALID_ARG;
-    if (!(g->rope_theta > 1.0)) return DFLASH_ERR_UNSUPPORTED_GEOM;
-  }
+  if (const int st = rope_spec_status(g, *rope)) return st;
   if (n_rows == 0) return DFLASH_OK;
-  const int64_t wq = static_cast<int64_t>(g->hq) * g->head_dim;
-  const int64_t wk = static_cast<int64_t>(g->nkv) * g->head_dim;
-  if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (v == nullptr) || (!q && !k) ||
-      !row_pos)
-    return DFLASH_ERR_INVALID_ARG;
-  q_row_stride = row_stride(n_rows, q_row_stride, wq);
-  q_out_row_stride = row_stride(n_rows, q_out_row_stride, wq);
-  k_row_stride = row_stride(n_rows, k_row_stride, wk);
-  v_row_stride = row_stride(n_rows, v_row_stride, wk);
-  if (q && (!rows_ok(q, q_row_stride, wq) || !rows_ok(q_out, q_out_row_stride, wq) ||
-            (q == q_out && q_row_stride != q_out_row_stride)))
-    return DFLASH_ERR_INVALID_ARG;
-  if (k && (!rows_ok(k, k_row_stride, wk) || !rows_ok(v, v_row_stride, wk) || !kv_pool ||
-            !aligned16(kv_pool) || !row_page || !row_slot))
-    return DFLASH_ERR_INVALID_ARG;
-  if (!aligned16(gamma_q) || !aligned16(gamma_k)) return DFLASH_ERR_INVALID_ARG;
+  StoreRows a = {q, k, v, gamma_q, gamma_k, row_pos, row_page, row_slot, q_out,
+                 q_row_stride, k_row_stride, v_row_stride, q_out_row_stride};
+  if (const int st = store_rows_status(g, n_rows, a)) return st;
+  if (k && (!kv_pool || !aligned16(kv_pool))) return DFLASH_ERR_INVALID_ARG;
   return cuda_status(launch_chunk_rope_store(
-      *g, layer, n_rows, r, q, q_row_stride, k, k_row_stride, v, v_row_stride, gamma_q, gamma_k,
-      row_pos, row_page, row_slot, q_out, q_out_row_stride, kv_pool, dev_status,
-      reinterpret_cast<cudaStream_t>(stream)));
+      *g, layer, n_rows, *rope, q, a.qs, k, a.ks, v, a.vs, gamma_q, gamma_k, row_pos, row_page,
+      row_slot, q_out, a.qos, kv_pool, dev_status, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 extern "C" int dflash_chunk_attention_num_segments(const dflash_geom *g, int B, int n_rows) {
@@ -568,21 +620,14 @@ extern "C" int dflash_chunk_attention(const dflash_geom *g, int B, int layer, in
                                       int mask_mode, int num_segments, void *workspace,
                                       size_t ws_bytes, void *out, int64_t out_row_stride,
                                       int32_t *dev_status, dflash_stream_t stream) {
-  if (!geom_ok(g) || B < 0 || n_rows < 0 || layer < 0 || layer >= g->num_layers || window < 0 ||
-      num_segments < 0 || num_segments > kMaxChunkSegments || !std::isfinite(scale))
-    return DFLASH_ERR_INVALID_ARG;
-  if (mask_mode != DFLASH_MASK_CAUSAL_TAIL && mask_mode != DFLASH_MASK_BLOCK_BIDIR)
-    return DFLASH_ERR_INVALID_ARG;
-  if (const int st = chunk_attention_geom_status(g, B, n_rows)) return st;
-  if (B == 0 || n_rows == 0) return DFLASH_OK;
-  if (!block_table || !cu_rows || !ctx_len) return DFLASH_ERR_INVALID_ARG;
-  if (const int st = attention_ptrs_status(B, q, nullptr, kv_pool, block_table, kv_len, out))
+  if (const int st = chunk_attention_args_status(g, B, layer, n_rows, window, scale, mask_mode,
+                                                 num_segments))
     return st;
-  const int64_t wq = static_cast<int64_t>(g->hq) * g->head_dim;
-  q_row_stride = row_stride(n_rows, q_row_stride, wq);
-  out_row_stride = row_stride(n_rows, out_row_stride, wq);
-  if (!rows_ok(q, q_row_stride, wq) || !rows_ok(out, out_row_stride, wq))
-    return DFLASH_ERR_INVALID_ARG;
+  if (B == 0 || n_rows == 0) return DFLASH_OK;
+  if (const int st = chunk_attention_ptrs_status(*g, B, n_rows, q, &q_row_stride, kv_pool,
+                                                 block_table, cu_rows, ctx_len, kv_len, out,
+                                                 &out_row_stride))
+    return st;
   if (!(scale > 0.f)) scale = default_attention_scale(*g);
   int S = num_segments;
   if (S == 0) {  // a window shortens the spans: no more segments than without one
@@ -597,4 +642,115 @@ extern "C" int dflash_chunk_attention(const dflash_geom *g, int B, int layer, in
                                             block_table, cu_rows, ctx_len, kv_len, window, sinks,
                                             scale, mask_mode, S, workspace, out, out_row_stride,
                                             dev_status, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------ ragged chunk, cache in 8 bits
+
+extern "C" size_t dflash_cache8_code_bytes(const dflash_geom *g) {
+  if (!geom_ok(g) || g->kind != DFLASH_KIND_GQA) return 0;
+  return 2ull * g->num_layers * g->num_pool_pages * g->nkv * g->page_size * g->head_dim;
+}
+
+extern "C" size_t dflash_cache8_scale_bytes(const dflash_geom *g, int block) {
+  if (!geom_ok(g) || cache8_geom_status(g, block)) return 0;
+  return 2ull * g->num_layers * g->num_pool_pages * g->nkv * (g->page_size / block);
+}
+
+extern "C" int dflash_chunk_rope_store8(const dflash_geom *g, int layer, int n_rows,
+                                        const dflash_rope_spec *rope, const void *q,
+                                        int64_t q_row_stride, const void *k, int64_t k_row_stride,
+                                        const void *v, int64_t v_row_stride, const void *gamma_q,
+                                        const void *gamma_k, const int32_t *row_pos,
+                                        const int32_t *row_page, const int32_t *row_slot,
+                                        void *q_out, int64_t q_out_row_stride,
+                                        const dflash_cache8 *cache, int32_t *dev_status,
+                                        dflash_stream_t stream) {
+  if (!geom_ok(g) || !cache || layer < 0 || layer >= g->num_layers || n_rows < 0)
+    return DFLASH_ERR_INVALID_ARG;
+  if (n_rows >= (1 << 30)) return DFLASH_ERR_UNSUPPORTED_GEOM;
+  if (const int st = cache8_geom_status(g, cache->block)) return st;
+  if (rope)
+    if (const int st = rope_spec_status(g, *rope)) return st;
+  if (n_rows == 0) return DFLASH_OK;
+  StoreRows a = {q, k, v, gamma_q, gamma_k, row_pos, row_page, row_slot, q_out,
+                 q_row_stride, k_row_stride, v_row_stride, q_out_row_stride};
+  if (const int st = store_rows_status(g, n_rows, a)) return st;
+  if (k)
+    if (const int st = cache8_ptrs_status(*cache)) return st;
+  const dflash_rope_spec still = {};  // no dims turn
+  return cuda_status(launch_chunk_rope_store8(
+      *g, layer, n_rows, rope ? *rope : still, q, a.qs, k, a.ks, v, a.vs, gamma_q, gamma_k,
+      row_pos, row_page, row_slot, q_out, a.qos, *cache, dev_status,
+      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int dflash_chunk_read8(const dflash_geom *g, int layer, int n_rows,
+                                  const dflash_cache8 *cache, const int32_t *row_page,
+                                  const int32_t *row_slot, void *k_out, int64_t k_row_stride,
+                                  void *v_out, int64_t v_row_stride, int32_t *dev_status,
+                                  dflash_stream_t stream) {
+  if (!geom_ok(g) || !cache || layer < 0 || layer >= g->num_layers || n_rows < 0)
+    return DFLASH_ERR_INVALID_ARG;
+  if (n_rows >= (1 << 30)) return DFLASH_ERR_UNSUPPORTED_GEOM;
+  if (const int st = cache8_geom_status(g, cache->block)) return st;
+  if (n_rows == 0) return DFLASH_OK;
+  const int64_t wk = static_cast<int64_t>(g->nkv) * g->head_dim;
+  k_row_stride = row_stride(n_rows, k_row_stride, wk);
+  v_row_stride = row_stride(n_rows, v_row_stride, wk);
+  if ((!k_out && !v_out) || !row_page || !row_slot ||
+      (k_out && !rows_ok(k_out, k_row_stride, wk)) || (v_out && !rows_ok(v_out, v_row_stride, wk)))
+    return DFLASH_ERR_INVALID_ARG;
+  if (const int st = cache8_ptrs_status(*cache)) return st;
+  return cuda_status(launch_chunk_read8(*g, layer, n_rows, *cache, row_page, row_slot, k_out,
+                                        k_row_stride, v_out, v_row_stride, dev_status,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int dflash_chunk_attention8_num_segments(const dflash_geom *g, int B, int n_rows) {
+  if (!geom_ok(g) || B < 1 || n_rows < 1 || chunk_attention_geom_status(g, B, n_rows)) return 0;
+  return chunk_attention8_num_segments(*g, B, n_rows, 0);
+}
+
+extern "C" size_t dflash_chunk_attention8_workspace_bytes(const dflash_geom *g, int B, int n_rows,
+                                                          int num_segments) {
+  if (!geom_ok(g) || B < 0 || n_rows < 0 || num_segments < 0 ||
+      num_segments > kMaxChunkSegments || chunk_attention_geom_status(g, B, n_rows))
+    return 0;
+  return chunk_attention8_workspace_bytes(*g, B, n_rows, num_segments);
+}
+
+extern "C" int dflash_chunk_attention8(const dflash_geom *g, int B, int layer, int n_rows,
+                                       const void *q, int64_t q_row_stride,
+                                       const dflash_cache8 *cache, const int32_t *block_table,
+                                       const int32_t *cu_rows, const int32_t *ctx_len,
+                                       const int32_t *kv_len, int32_t window, const float *sinks,
+                                       float scale, int mask_mode, int num_segments,
+                                       void *workspace, size_t ws_bytes, void *out,
+                                       int64_t out_row_stride, int32_t *dev_status,
+                                       dflash_stream_t stream) {
+  if (!cache) return DFLASH_ERR_INVALID_ARG;
+  if (const int st = chunk_attention_args_status(g, B, layer, n_rows, window, scale, mask_mode,
+                                                 num_segments))
+    return st;
+  if (const int st = cache8_geom_status(g, cache->block)) return st;
+  if (B == 0 || n_rows == 0) return DFLASH_OK;
+  if (const int st = chunk_attention_ptrs_status(*g, B, n_rows, q, &q_row_stride, cache->codes,
+                                                 block_table, cu_rows, ctx_len, kv_len, out,
+                                                 &out_row_stride))
+    return st;
+  if (const int st = cache8_ptrs_status(*cache)) return st;
+  if (!(scale > 0.f)) scale = default_attention_scale(*g);
+  int S = num_segments;
+  if (S == 0) {  // a window shortens the spans: no more segments than without one
+    S = chunk_attention8_num_segments(*g, B, n_rows, 0);
+    if (S > 1 && window > 0)
+      S = std::min(S, chunk_attention8_num_segments(*g, B, n_rows, window));
+  }
+  const size_t need = chunk_attention8_workspace_bytes(*g, B, n_rows, S);
+  if (need > 0 && (!workspace || !aligned16(workspace))) return DFLASH_ERR_INVALID_ARG;
+  if (need > 0 && ws_bytes < need) return DFLASH_ERR_WORKSPACE_TOO_SMALL;
+  return cuda_status(launch_chunk_attention8(*g, B, layer, n_rows, q, q_row_stride, *cache,
+                                             block_table, cu_rows, ctx_len, kv_len, window, sinks,
+                                             scale, mask_mode, S, workspace, out, out_row_stride,
+                                             dev_status, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -205,4 +205,25 @@ cudaError_t launch_chunk_attention(const dflash_geom &g, int B, int layer, int n
                                    float scale, int mask_mode, int S, void *ws, void *out,
                                    int64_t out_stride, int32_t *st, cudaStream_t s);
 
+// the same over a cache held in 8 bits
+cudaError_t launch_chunk_rope_store8(const dflash_geom &g, int layer, int n_rows,
+                                     const dflash_rope_spec &rope, const void *q, int64_t q_stride,
+                                     const void *k, int64_t k_stride, const void *v,
+                                     int64_t v_stride, const void *gamma_q, const void *gamma_k,
+                                     const int32_t *pos, const int32_t *page, const int32_t *slot,
+                                     void *q_out, int64_t q_out_stride, const dflash_cache8 &cache,
+                                     int32_t *st, cudaStream_t s);
+cudaError_t launch_chunk_read8(const dflash_geom &g, int layer, int n_rows,
+                               const dflash_cache8 &cache, const int32_t *page,
+                               const int32_t *slot, void *k_out, int64_t k_stride, void *v_out,
+                               int64_t v_stride, int32_t *st, cudaStream_t s);
+int chunk_attention8_num_segments(const dflash_geom &g, int B, int n_rows, int window);
+size_t chunk_attention8_workspace_bytes(const dflash_geom &g, int B, int n_rows, int S);
+cudaError_t launch_chunk_attention8(const dflash_geom &g, int B, int layer, int n_rows,
+                                    const void *q, int64_t q_stride, const dflash_cache8 &cache,
+                                    const int32_t *tbl, const int32_t *cu, const int32_t *ctx,
+                                    const int32_t *kv, int32_t window, const float *sinks,
+                                    float scale, int mask_mode, int S, void *ws, void *out,
+                                    int64_t out_stride, int32_t *st, cudaStream_t s);
+
 }  // namespace dflash

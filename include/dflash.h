@@ -11,7 +11,7 @@
  *   3. the block-KV scatter and the decode-shaped split-KV block attention.
  * Beside them, a layer over a ragged chunk of new tokens (any number of rows per
  * request): its page and slot plan, its rotary positions and paged store, and its
- * attention.
+ * attention; and the last two over a cache held in 8 bits, with a call that reads it back.
  *
  * Conventions shared by every call
  *  - All pointers named as device buffers are device pointers the caller owns
@@ -44,6 +44,8 @@
  *    page_size * head_dim contiguous values.
  *  - MLA: bf16 [L][num_pool_pages][page_size][latent_dim + rope_dim]; one
  *    latent row per token: RMS-normed latent then the rotated rope part.
+ *  - GQA in 8 bits (dflash_cache8): e4m3 codes in the GQA layout, and a scale for
+ *    every block of tokens, head by head, K and V apart.
  *
  * Sources (page title and part):
  *  [TRT-20548] TensorRT-LLM issue #20548, Proposal.
@@ -196,6 +198,23 @@ typedef struct dflash_rope_spec {
   double beta_slow;    /* YARN: pairs turning less often than this are divided by factor */
   double magnitude;    /* YARN: factor on cos and sin; <= 0 selects 0.1 ln(factor) + 1 */
 } dflash_rope_spec;
+
+/* A GQA cache held in 8 bits, of the chunk calls that end in 8.
+ *  codes   device e4m3 [L][num_pool_pages][2][nkv][page_size][head_dim], 16-byte aligned
+ *          (dflash_cache8_code_bytes).
+ *  scales  device bytes [L][num_pool_pages][2][nkv][page_size / block]
+ *          (dflash_cache8_scale_bytes): the `block` tokens of a page from block * i on share
+ *          scale i, head by head, K and V apart.
+ *  block   16, 32 or 64 tokens; divides page_size.
+ * A cell's value is code * 2^(scale - 127); scale 255 makes it NaN.  Powers of two: a block's
+ * scale can be raised by a shift of what it holds, exact but for its smallest values,
+ * and every value of a written scale is a bf16 number. */
+typedef struct dflash_cache8 {
+  void *codes;
+  void *scales;
+  int32_t block;
+  int32_t reserved0;
+} dflash_cache8;
 
 /* ---------------------------------------------------------------------
  * dflash_pack_weights -- stack every drafter layer's K/V (GQA) or latent (MLA)
@@ -761,6 +780,91 @@ DFLASH_API int dflash_chunk_attention(const dflash_geom *g, int B, int layer, in
                                       int mask_mode, int num_segments, void *workspace,
                                       size_t ws_bytes, void *out, int64_t out_row_stride,
                                       int32_t *dev_status, dflash_stream_t stream);
+
+/* ---------------------------------------------------------------------
+ * A ragged chunk over a cache held in 8 bits: dflash_chunk_rope_store8,
+ * dflash_chunk_read8, dflash_chunk_attention8 (with dflash_chunk_plan as it is).
+ * Half the cache's memory, and half the bytes that attention streams.
+ *
+ * dflash_chunk_rope_store8 -- dflash_chunk_rope_store into the 8-bit cache: q, k and v
+ * rows as that call takes them (norm, rotation, q_out, strides), k' and v quantised.
+ *
+ * For every block that rows of the call are placed in, head by head, K and V apart:
+ *   e = max(ceil(log2(a / 448)), -124), a = the largest finite magnitude of the rows' values;
+ *   where no row of the call is at the block's first slot, the block goes on: with f the
+ *   exponent that it has, e = max(e, f), and the codes of the slots that get no row become
+ *   rn(code * 2^(f - e)); where one is, it is begun anew: those codes stay as they are
+ *   (what they stand for is given up);
+ *   code = rn(x * 2^-e) of the fp32 value x (nearest e4m3, ties to even), scale = e + 127.
+ * A value that is not finite becomes NaN and counts for no scale.  Values lie within half an
+ * e4m3 step of x: 2^-4 |x|, or 2^(e - 10) for the smallest ones.
+ * The call's rows of one block follow one another, in any order of slots, as dflash_chunk_plan
+ * places a request's: no row of another block, or without a place, between them.  A block that
+ * comes twice holds no values in particular, nor do two rows that share a slot; rows past
+ * `block` of one block are left out and flag DFLASH_DEV_BAD_ROWS.
+ *
+ * rope         as dflash_chunk_rope_store, or NULL: nothing is turned (keys rotated elsewhere, a
+ *              bf16 cache taken over).
+ * cache        the cache (HOST structure).
+ * Other arguments, flags and errors as dflash_chunk_rope_store (cache in place of kv_pool);
+ * DFLASH_ERR_INVALID_ARG also for a null or misaligned buffer of the cache,
+ * DFLASH_ERR_UNSUPPORTED_GEOM also for head_dim not a multiple of 16, or a block other than
+ * 16, 32 or 64 or that does not divide page_size.
+ * ------------------------------------------------------------------- */
+DFLASH_API size_t dflash_cache8_code_bytes(const dflash_geom *g);
+DFLASH_API size_t dflash_cache8_scale_bytes(const dflash_geom *g, int block);
+DFLASH_API int dflash_chunk_rope_store8(const dflash_geom *g, int layer, int n_rows,
+                                        const dflash_rope_spec *rope, const void *q,
+                                        int64_t q_row_stride, const void *k, int64_t k_row_stride,
+                                        const void *v, int64_t v_row_stride, const void *gamma_q,
+                                        const void *gamma_k, const int32_t *row_pos,
+                                        const int32_t *row_page, const int32_t *row_slot,
+                                        void *q_out, int64_t q_out_row_stride,
+                                        const dflash_cache8 *cache, int32_t *dev_status,
+                                        dflash_stream_t stream);
+
+/* ---------------------------------------------------------------------
+ * dflash_chunk_read8 -- rows of the 8-bit cache as bf16: a prefix handed to another worker,
+ * or to a layer that keeps its cache in 16 bits.
+ *
+ * k_out[t], v_out[t] = the nkv heads of (row_page[t], row_slot[t]) of `layer`, each value
+ * rounded to bf16 once (exact for the scales that dflash_chunk_rope_store8 writes).  A row with
+ * row_page < 0 is left as it is; so is one with a page or slot outside the pool, which flags
+ * DFLASH_DEV_BAD_PAGE.  Rows may come in any order, and more than once.
+ *
+ * k_out, v_out  device bf16, row t at + t * stride elements, heads contiguous; one of them may
+ *               be NULL.  They must not overlap each other or the cache.
+ * Errors: DFLASH_ERR_INVALID_ARG (null or misaligned pointers, n_rows < 0, bad layer, strides
+ * below nkv * head_dim or not a multiple of 8), DFLASH_ERR_UNSUPPORTED_GEOM (as
+ * dflash_chunk_rope_store8), DFLASH_ERR_CUDA.
+ * ------------------------------------------------------------------- */
+DFLASH_API int dflash_chunk_read8(const dflash_geom *g, int layer, int n_rows,
+                                  const dflash_cache8 *cache, const int32_t *row_page,
+                                  const int32_t *row_slot, void *k_out, int64_t k_row_stride,
+                                  void *v_out, int64_t v_row_stride, int32_t *dev_status,
+                                  dflash_stream_t stream);
+
+/* ---------------------------------------------------------------------
+ * dflash_chunk_attention8 -- dflash_chunk_attention over the 8-bit cache: the same rows, masks,
+ * sinks, flags and promises, k_j and v_j being the values of the cells.
+ *
+ * cache        the cache (HOST structure) in place of kv_pool.
+ * num_segments, workspace  as there, of this call's own dflash_chunk_attention8_num_segments
+ *              and dflash_chunk_attention8_workspace_bytes.
+ * Errors: those of dflash_chunk_attention and, for the cache, of dflash_chunk_rope_store8.
+ * ------------------------------------------------------------------- */
+DFLASH_API int dflash_chunk_attention8_num_segments(const dflash_geom *g, int B, int n_rows);
+DFLASH_API size_t dflash_chunk_attention8_workspace_bytes(const dflash_geom *g, int B, int n_rows,
+                                                          int num_segments);
+DFLASH_API int dflash_chunk_attention8(const dflash_geom *g, int B, int layer, int n_rows,
+                                       const void *q, int64_t q_row_stride,
+                                       const dflash_cache8 *cache, const int32_t *block_table,
+                                       const int32_t *cu_rows, const int32_t *ctx_len,
+                                       const int32_t *kv_len, int32_t window, const float *sinks,
+                                       float scale, int mask_mode, int num_segments,
+                                       void *workspace, size_t ws_bytes, void *out,
+                                       int64_t out_row_stride, int32_t *dev_status,
+                                       dflash_stream_t stream);
 
 /* ---------------------------------------------------------------------
  * dflash_test_attention_skip_tile -- for tests of the bounded-wait path only.
