@@ -7,6 +7,7 @@
 #include "cache8.cuh"
 #include "chunk_turn.cuh"
 #include "dflash_internal.cuh"
+#include "sm100_ptx.cuh"
 
 namespace dflash {
 namespace {
@@ -115,32 +116,373 @@ __global__ void __launch_bounds__(128)
   if (threadIdx.x == 0) *scale = static_cast<uint8_t>(e + 127);
 }
 
+// The heads of 64 or 128 that no turning pair of 8-value chunks is cut by: one launch for q, k
+// and v.  A row's HD values are held by HD / 16 lanes, two chunks of 8 each: in the half layout
+// the two that turn together, in the pairs layout neighbouring ones (as the 16-bit store).
+//
+// K and V.  A CTA takes the blocks that its window of rows is the first in, for one head of K
+// or V; a warp holds kRows rows in registers, so that memory is read once: blocks of that many
+// rows are a warp's, each, larger ones all four warps' (they join their largest values).  Every
+// (row, pair) of a head is turned once, so its angle is taken where it is needed.
+//
+// Q.  A CTA takes 16 pieces, each as many heads of a row as a warp holds.
+//
+// Bound by HBM: 8192 rows of 32 + 8 + 8 heads of 128 are 184 MB with their codes.
+constexpr int kQPieces = 16;
+
+struct Store8Fast {
+  Store8Params s;
+  const uint16_t *q, *gq;
+  uint16_t *q_out;
+  int64_t qs, qos;
+  int hq, window, q_pieces, kv_blocks;  // q_pieces: of a row
+};
+
+template <int HD, bool kHalf>
+struct Lanes {
+  static constexpr int kLanes = HD / 16, kAtOnce = 32 / kLanes;  // of a row; rows of a warp's access
+  int d0, d1, pair0;
+  bool turn0, turn1;
+  __device__ __forceinline__ explicit Lanes(int lane, int rot) {
+    const int u = lane % kLanes;
+    pair0 = 8 * u;
+    if (kHalf) {
+      const int nrot = rot / 16;
+      turn0 = turn1 = u < nrot;
+      d0 = turn0 ? 8 * u : rot + 16 * (u - nrot);
+      d1 = turn0 ? d0 + rot / 2 : d0 + 8;
+    } else {
+      d0 = 16 * u;
+      d1 = d0 + 8;
+      turn0 = d0 < rot;
+      turn1 = d1 < rot;
+    }
+  }
+};
+
+__device__ __forceinline__ void unpack8(const uint4 &v, float *x) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x[2 * e] = __uint_as_float(w[e] << 16);
+    x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float *x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = ptx::pack_bf16x2(x[2 * e], x[2 * e + 1]);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// cos and sin of a lane's pairs at a position.
+__device__ __forceinline__ void angles(const TurnFreqs &tf, int pos, int pair0, float mag,
+                                       float (&c)[8], float (&s)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float2 cs = turn_cos_sin(pos, tf.f[pair0 + e], mag);
+    c[e] = cs.x;
+    s[e] = cs.y;
+  }
+}
+// The norm's factor of a row that kLanes lanes hold.
+template <int kLanes>
+__device__ __forceinline__ float norm_of(const float (&x)[16], float eps, int hd) {
+  float a = 0.f, b = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    a = fmaf(x[e], x[e], a);
+    b = fmaf(x[8 + e], x[8 + e], b);
+  }
+  a += b;
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  return rsqrtf(a / static_cast<float>(hd) + eps);
+}
+template <bool kHalf>
+__device__ __forceinline__ void turn16(float (&x)[16], const float (&c)[8], const float (&s)[8],
+                                       bool turn0, bool turn1) {
+  if (kHalf) {
+    if (!turn0) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float a = x[e], b = x[8 + e];
+      x[e] = a * c[e] - b * s[e];
+      x[8 + e] = b * c[e] + a * s[e];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (!(e < 4 ? turn0 : turn1)) continue;
+      const float a = x[2 * e], b = x[2 * e + 1];
+      x[2 * e] = a * c[e] - b * s[e];
+      x[2 * e + 1] = b * c[e] + a * s[e];
+    }
+  }
+}
+
+template <int HD, bool kHalf>
+__device__ __forceinline__ void store_q(const Store8Fast &p, const TurnFreqs &tf, int block) {
+  using L = Lanes<HD, kHalf>;
+  constexpr int kEach = kQPieces / 4;  // of a warp
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const L at(lane, p.s.rot);
+  const int64_t first = static_cast<int64_t>(block) * kQPieces + warp * kEach;
+  uint4 v[kEach][2] = {};
+  int pos[kEach], row[kEach], head[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int64_t r = (first + i) / p.q_pieces;
+    row[i] = static_cast<int>(r < p.s.n_rows ? r : 0);
+    head[i] = static_cast<int>(first + i - r * p.q_pieces) * L::kAtOnce + lane / L::kLanes;
+    pos[i] = r < p.s.n_rows ? p.s.pos[row[i]] : -1;
+    if (head[i] < p.hq && r < p.s.n_rows) {
+      const uint16_t *src = p.q + row[i] * p.qs + static_cast<int64_t>(head[i]) * HD;
+      v[i][0] = *reinterpret_cast<const uint4 *>(src + at.d0);
+      v[i][1] = *reinterpret_cast<const uint4 *>(src + at.d1);
+    }
+  }
+  float g[16];
+  if (p.gq) {
+    unpack8(*reinterpret_cast<const uint4 *>(p.gq + at.d0), g);
+    unpack8(*reinterpret_cast<const uint4 *>(p.gq + at.d1), g + 8);
+  }
+  float c[8], s[8];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    if (pos[i] < 0) continue;  // the whole warp's row
+    if (at.turn0 && (i == 0 || pos[i] != pos[i ? i - 1 : 0])) angles(tf, pos[i], at.pair0, p.s.mag, c, s);
+    float x[16];
+    unpack8(v[i][0], x);
+    unpack8(v[i][1], x + 8);
+    if (p.gq) {
+      const float inv = norm_of<L::kLanes>(x, p.s.eps, HD);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = x[e] * inv * g[e];
+    }
+    turn16<kHalf>(x, c, s, at.turn0, at.turn1);
+    if (head[i] < p.hq) {
+      uint16_t *dst = p.q_out + row[i] * p.qos + static_cast<int64_t>(head[i]) * HD;
+      *reinterpret_cast<uint4 *>(dst + at.d0) = pack8(x);
+      *reinterpret_cast<uint4 *>(dst + at.d1) = pack8(x + 8);
+    }
+  }
+}
+
+constexpr int kMostWindow = 16;
+
+template <int HD, bool kHalf>
+__global__ void __launch_bounds__(128)
+    chunk_store8_fast_kernel(const __grid_constant__ Store8Fast p,
+                             const __grid_constant__ TurnFreqs tf) {
+  using L = Lanes<HD, kHalf>;
+  constexpr int kIters = 4, kRows = kIters * L::kAtOnce;  // rows that a warp holds
+  ptx::griddep_launch();
+  ptx::griddep_wait();
+  if (blockIdx.x >= p.kv_blocks) {
+    store_q<HD, kHalf>(p, tf, blockIdx.x - p.kv_blocks);
+    return;
+  }
+  __shared__ int64_t s_block[kMostWindow + 65];  // of rows first - 1 on
+  __shared__ float s_most[4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Cache8 &cache = p.s.cache;
+  const int hk = blockIdx.x % (2 * cache.nkv), kv = hk & 1, h = hk >> 1;
+  const int first = blockIdx.x / (2 * cache.nkv) * p.window, block = cache.block;
+  if (static_cast<int>(threadIdx.x) <= p.window + block) {
+    const int t = first - 1 + static_cast<int>(threadIdx.x);
+    const bool mine = hk == 0 && t >= first && t < first + p.window;  // reports it
+    s_block[threadIdx.x] = t >= 0 && t < p.s.n_rows ? block_of(p.s, t, mine) : -1;
+  }
+  __syncthreads();
+  const L at(lane, kv ? 0 : p.s.rot);
+  const int sub = lane / L::kLanes;  // the lane's row of kAtOnce
+  const uint16_t *src = (kv ? p.s.v : p.s.k) + static_cast<int64_t>(h) * HD;
+  const int64_t step = kv ? p.s.vs : p.s.ks;
+  const uint16_t *gamma = kv ? nullptr : p.s.gk;
+
+  int small = 0;  // runs that are one warp's, so far
+  for (int i = 0; i < p.window; ++i) {
+    const int64_t id = s_block[1 + i];
+    if (id < 0 || s_block[i] == id) continue;
+    int n = 1;  // rows of the block
+    while (n <= block && s_block[1 + i + n] == id) ++n;
+    if (n > block) {  // more rows than slots
+      if (threadIdx.x == 0 && hk == 0) raise_status(p.s.st, DFLASH_DEV_BAD_ROWS);
+      n = block;
+    }
+    const bool together = n > kRows;
+    if (!together && (small++ & 3) != warp) continue;
+    const int t0 = first + i, page = p.s.page[t0], slot0 = p.s.slot[t0] / block * block;
+    uint8_t *scale = cache.scale(page, kv, h, slot0);
+    const int before = static_cast<int>(*scale) - 127;
+    // this warp's rows: a whole number of kAtOnce
+    const int each = together ? ((n + 3) / 4 + L::kAtOnce - 1) / L::kAtOnce * L::kAtOnce : kRows;
+    const int r0 = t0 + (together ? warp * each : 0);
+    const int rows = max(min(each, t0 + n - r0), 0);
+    uint4 v[kIters][2] = {};
+    int slot[kIters];
+#pragma unroll
+    for (int j = 0; j < kIters; ++j) {
+      const int r = j * L::kAtOnce + sub;
+      slot[j] = -1;
+      if (r < rows) {
+        const uint16_t *x = src + (r0 + r) * step;
+        v[j][0] = *reinterpret_cast<const uint4 *>(x + at.d0);
+        v[j][1] = *reinterpret_cast<const uint4 *>(x + at.d1);
+        slot[j] = p.s.slot[r0 + r];
+      }
+    }
+    // the slots that the block's rows write: bit s of slot s
+    uint64_t written = 0;
+    for (int r = lane; r < n; r += 32) written |= 1ull << (p.s.slot[t0 + r] - slot0);
+    written = static_cast<uint64_t>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(written))) |
+              static_cast<uint64_t>(
+                  __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(written >> 32)))
+                  << 32;
+    float g[16];
+    if (gamma) {
+      unpack8(*reinterpret_cast<const uint4 *>(gamma + at.d0), g);
+      unpack8(*reinterpret_cast<const uint4 *>(gamma + at.d1), g + 8);
+    }
+    float y[kIters][16], most = 0.f;
+#pragma unroll
+    for (int j = 0; j < kIters; ++j) {
+      if (j * L::kAtOnce >= rows) {  // the whole warp
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[j][e] = 0.f;
+        continue;
+      }
+      unpack8(v[j][0], y[j]);
+      unpack8(v[j][1], y[j] + 8);
+      if (gamma) {
+        const float inv = norm_of<L::kLanes>(y[j], p.s.eps, HD);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[j][e] = y[j][e] * inv * g[e];
+      }
+      if (at.turn0 && slot[j] >= 0) {
+        float c[8], s[8];
+        angles(tf, p.s.pos[r0 + j * L::kAtOnce + sub], at.pair0, p.s.mag, c, s);
+        turn16<kHalf>(y[j], c, s, at.turn0, at.turn1);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float a = fabsf(y[j][e]);
+        if (a < INFINITY) most = fmaxf(most, a);
+        else y[j][e] = NAN;
+      }
+    }
+    most = warp_max(most);
+    if (together) {
+      if (lane == 0) s_most[warp] = most;
+      __syncthreads();
+      most = fmaxf(fmaxf(s_most[0], s_most[1]), fmaxf(s_most[2], s_most[3]));
+      __syncthreads();
+    }
+    int e = scale8_exponent(most);
+    if (!(written & 1)) {  // the block goes on
+      e = max(e, before);
+      if (e != before) {
+        const float shift = before - e < -149 ? 0.f : exp2_int(before - e);
+        const int vecs = block * HD / 16, c16 = HD / 16;
+        uint4 *cells = reinterpret_cast<uint4 *>(cache.code(page, kv, h, slot0));
+        for (int x = (together ? threadIdx.x : lane); x < vecs; x += together ? 128 : 32) {
+          if ((written >> (x / c16)) & 1) continue;
+          const uint4 old = cells[x];
+          uint32_t w[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const float2 lo = e4m3_values(w[b]), hi = e4m3_values(w[b] >> 16);
+            w[b] = e4m3_pair(lo.x * shift, lo.y * shift) |
+                   e4m3_pair(hi.x * shift, hi.y * shift) << 16;
+          }
+          cells[x] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+    const float down = exp2_int(-e);
+#pragma unroll
+    for (int j = 0; j < kIters; ++j) {
+      if (slot[j] < 0) continue;
+      uint32_t w[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        w[b] = e4m3_pair(y[j][4 * b] * down, y[j][4 * b + 1] * down) |
+               e4m3_pair(y[j][4 * b + 2] * down, y[j][4 * b + 3] * down) << 16;
+      uint8_t *cell = cache.code(page, kv, h, slot[j]);
+      *reinterpret_cast<uint2 *>(cell + at.d0) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2 *>(cell + at.d1) = make_uint2(w[2], w[3]);
+    }
+    // (every warp has read the scale before the barriers, where there is more than one)
+    if (lane == 0 && (!together || warp == 0)) *scale = static_cast<uint8_t>(e + 127);
+  }
+}
+
 struct Read8Params {
   Cache8 cache;
-  int n_rows;
+  int n_rows, rows, vecs, sides;  // rows of a CTA, 16 codes each of a row's K (or V), K and V
   const int32_t *page, *slot;
   uint16_t *out[2];
   int64_t stride[2];
   int32_t *st;
 };
 
-// One CTA for a row; a thread a value.
-__global__ void __launch_bounds__(256) chunk_read8_kernel(const Read8Params p) {
-  const int t = blockIdx.x, pg = p.page[t], sl = p.slot[t];
-  if (pg < 0) return;
-  if (pg >= p.cache.NP || sl < 0 || sl >= p.cache.P) {
-    if (threadIdx.x == 0) raise_status(p.st, DFLASH_DEV_BAD_PAGE);
-    return;
-  }
-  for (int kv = 0; kv < 2; ++kv) {
-    if (!p.out[kv]) continue;
-    for (int i = threadIdx.x; i < p.cache.nkv * p.cache.hd; i += blockDim.x) {
-      const int h = i / p.cache.hd;
-      const float f = e4m3_values(p.cache.code(pg, kv, h, sl)[i - h * p.cache.hd]).x *
-                      scale8_value(*p.cache.scale(pg, kv, h, sl));
-      p.out[kv][t * p.stride[kv] + i] = f32_to_bf16_rn(f);
+// 16 codes a lane, kEach times: all loads before the first is used.  Bound by HBM.
+__global__ void __launch_bounds__(256) chunk_read8_kernel(const __grid_constant__ Read8Params p) {
+  constexpr int kEach = 4;
+  ptx::griddep_launch();
+  ptx::griddep_wait();
+  const int r0 = blockIdx.x * p.rows, rows = min(p.rows, p.n_rows - r0);
+  const int per_row = p.vecs * p.sides, all = rows * per_row, head = p.cache.hd / 16;
+  for (int base = threadIdx.x; base < all; base += kEach * 256) {
+    uint4 codes[kEach];
+    uint32_t scale[kEach];
+    uint16_t *to[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int x = base + 256 * i, r = x / per_row, y = x - r * per_row;
+      to[i] = nullptr;
+      if (x >= all) continue;
+      const int t = r0 + r, pg = p.page[t], sl = p.slot[t];
+      if (pg < 0) continue;
+      if (pg >= p.cache.NP || sl < 0 || sl >= p.cache.P) {
+        if (y == 0) raise_status(p.st, DFLASH_DEV_BAD_PAGE);
+        continue;
+      }
+      const int kv = p.sides == 1 ? (p.out[0] ? 0 : 1) : y >= p.vecs, c = y - (p.sides == 2 && kv ? p.vecs : 0);
+      const int h = c / head;
+      to[i] = p.out[kv] + t * p.stride[kv] + 16 * c;
+      codes[i] = __ldcs(reinterpret_cast<const uint4 *>(p.cache.code(pg, kv, h, sl)) + (c - h * head));
+      scale[i] = *p.cache.scale(pg, kv, h, sl);
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      if (!to[i]) continue;
+      const float f = scale8_value(scale[i]);
+      const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+      uint32_t o[8];
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        const float2 v = e4m3_values(w[b >> 1] >> (16 * (b & 1)));
+        o[b] = ptx::pack_bf16x2(v.x * f, v.y * f);
+      }
+      reinterpret_cast<uint4 *>(to[i])[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      reinterpret_cast<uint4 *>(to[i])[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
   }
+}
+
+// A launch that may begin under the end of the one before it.
+cudaLaunchConfig_t config(cudaLaunchAttribute *attr, int64_t blocks, int threads, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
 }
 
 }  // namespace
@@ -152,12 +494,6 @@ cudaError_t launch_chunk_rope_store8(const dflash_geom &g, int layer, int n_rows
                                      const int32_t *pos, const int32_t *page, const int32_t *slot,
                                      void *q_out, int64_t q_out_stride, const dflash_cache8 &cache,
                                      int32_t *st, cudaStream_t s) {
-  if (q) {
-    const cudaError_t e = launch_chunk_rope_store(
-        g, layer, n_rows, rope, q, q_stride, nullptr, 0, nullptr, 0, gamma_q, nullptr, pos, nullptr,
-        nullptr, q_out, q_out_stride, nullptr, st, s);
-    if (e != cudaSuccess || !k) return e;
-  }
   const TurnTable &table = turn_table(rope, g.rope_theta);
   Store8Params p = {};
   p.cache = cache8_of(g, cache, layer);
@@ -175,6 +511,41 @@ cudaError_t launch_chunk_rope_store8(const dflash_geom &g, int layer, int n_rows
   p.page = page;
   p.slot = slot;
   p.st = st;
+  const bool halves = rope.layout == DFLASH_ROPE_HALF;
+  if ((g.head_dim == 64 || g.head_dim == 128) && rope.rot_dim % (halves ? 16 : 8) == 0) {
+    Store8Fast f = {};
+    f.s = p;
+    f.q = static_cast<const uint16_t *>(q);
+    f.gq = static_cast<const uint16_t *>(gamma_q);
+    f.q_out = static_cast<uint16_t *>(q_out);
+    f.qs = q_stride;
+    f.qos = q_out_stride;
+    f.hq = g.hq;
+    // Rows of a CTA's window: single tokens are a block each, a prompt's rows share one.
+    f.window = 1;
+    while (f.window < kMostWindow && n_rows > 512 * f.window) f.window *= 2;
+    const int at_once = 512 / g.head_dim;
+    f.q_pieces = (g.hq + at_once - 1) / at_once;
+    const int64_t kv_blocks =
+        k ? static_cast<int64_t>((n_rows + f.window - 1) / f.window) * 2 * g.nkv : 0;
+    const int64_t q_blocks =
+        q ? (static_cast<int64_t>(n_rows) * f.q_pieces + kQPieces - 1) / kQPieces : 0;
+    if (kv_blocks + q_blocks >= (1LL << 31)) return cudaErrorInvalidValue;
+    f.kv_blocks = static_cast<int>(kv_blocks);
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = config(attr, kv_blocks + q_blocks, 128, s);
+    if (g.head_dim == 64)
+      return cudaLaunchKernelEx(&cfg, halves ? chunk_store8_fast_kernel<64, true>
+                                             : chunk_store8_fast_kernel<64, false>, f, table.tf);
+    return cudaLaunchKernelEx(&cfg, halves ? chunk_store8_fast_kernel<128, true>
+                                           : chunk_store8_fast_kernel<128, false>, f, table.tf);
+  }
+  if (q) {
+    const cudaError_t e = launch_chunk_rope_store(
+        g, layer, n_rows, rope, q, q_stride, nullptr, 0, nullptr, 0, gamma_q, nullptr, pos, nullptr,
+        nullptr, q_out, q_out_stride, nullptr, st, s);
+    if (e != cudaSuccess || !k) return e;
+  }
   chunk_store8_kernel<<<dim3(n_rows, g.nkv, 2), 128, 0, s>>>(p, table.tf);
   return cudaGetLastError();
 }
@@ -183,11 +554,22 @@ cudaError_t launch_chunk_read8(const dflash_geom &g, int layer, int n_rows,
                                const dflash_cache8 &cache, const int32_t *page,
                                const int32_t *slot, void *k_out, int64_t k_stride, void *v_out,
                                int64_t v_stride, int32_t *st, cudaStream_t s) {
-  Read8Params p = {cache8_of(g, cache, layer), n_rows, page, slot,
-                   {static_cast<uint16_t *>(k_out), static_cast<uint16_t *>(v_out)},
-                   {k_stride, v_stride}, st};
-  chunk_read8_kernel<<<n_rows, 256, 0, s>>>(p);
-  return cudaGetLastError();
+  Read8Params p = {};
+  p.cache = cache8_of(g, cache, layer);
+  p.n_rows = n_rows;
+  p.vecs = g.nkv * g.head_dim / 16;
+  p.sides = (k_out != nullptr) + (v_out != nullptr);
+  p.rows = 1024 / (p.vecs * p.sides) > 0 ? 1024 / (p.vecs * p.sides) : 1;
+  p.page = page;
+  p.slot = slot;
+  p.out[0] = static_cast<uint16_t *>(k_out);
+  p.out[1] = static_cast<uint16_t *>(v_out);
+  p.stride[0] = k_stride;
+  p.stride[1] = v_stride;
+  p.st = st;
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = config(attr, (n_rows + p.rows - 1) / p.rows, 256, s);
+  return cudaLaunchKernelEx(&cfg, chunk_read8_kernel, p);
 }
 
 }  // namespace dflash
