@@ -175,14 +175,55 @@ __device__ __forceinline__ uint4 pack8(const float *x) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// cos and sin of a lane's pairs at a position.
-__device__ __forceinline__ void angles(const TurnFreqs &tf, int pos, int pair0, float mag,
-                                       float (&c)[8], float (&s)[8]) {
+// A lane's gains.
+struct Gains {
+  uint4 g[2] = {};
+  bool norm;
+  template <class L>
+  __device__ __forceinline__ Gains(const uint16_t *gamma, const L &at) : norm(gamma != nullptr) {
+    if (norm) {
+      g[0] = *reinterpret_cast<const uint4 *>(gamma + at.d0);
+      g[1] = *reinterpret_cast<const uint4 *>(gamma + at.d1);
+    }
+  }
+};
+// The turns of pairs `first` on.  (Through a generic address: as constants, the lanes' different
+// places are read one after another.)
+template <int N>
+__device__ __forceinline__ void turns_of(const TurnFreqs &tf, int first, bool any, uint64_t (&f)[N]) {
+  const uint64_t *from = tf.f + first;
+  asm("" : "+l"(from));
+#pragma unroll
+  for (int e = 0; e < N; ++e) f[e] = any ? from[e] : 0;
+}
+// cos and sin of a key's pairs: the hardware's functions on the reduced angle, off by at most
+// 2^-21, where the codes are off by 2^-4 (8192 rows take 89 us with the exact ones for q and k).
+__device__ __forceinline__ void key_angles(const uint64_t (&f)[8], int pos, float mag, float (&c)[8],
+                                           float (&s)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float2 cs = turn_cos_sin(pos, tf.f[pair0 + e], mag);
-    c[e] = cs.x;
-    s[e] = cs.y;
+    const uint64_t t = static_cast<uint64_t>(static_cast<uint32_t>(pos)) * f[e];
+    float sn, cs;  // top 32 bits: a signed fraction of half a turn in units of 2^-31
+    __sincosf(static_cast<float>(static_cast<int32_t>(t >> 32)) * (3.14159265358979f * 0x1p-31f),
+              &sn, &cs);
+    c[e] = cs * mag;
+    s[e] = sn * mag;
+  }
+}
+// cos and sin of a query row's pairs, as in the 16-bit store: the lanes that hold the same
+// dims of different heads take some of them each.
+template <class L>
+__device__ __forceinline__ void query_angles(const uint64_t (&f)[8 / L::kAtOnce], int lane, int pos,
+                                             float mag, float (&c)[8], float (&s)[8]) {
+  constexpr int kEach = 8 / L::kAtOnce;
+  float2 mine[kEach];
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) mine[e] = turn_cos_sin(pos, f[e], mag);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int from = e / kEach * L::kLanes + lane % L::kLanes;
+    c[e] = __shfl_sync(0xffffffffu, mine[e % kEach].x, from);
+    s[e] = __shfl_sync(0xffffffffu, mine[e % kEach].y, from);
   }
 }
 // The norm's factor of a row that kLanes lanes hold.
@@ -198,6 +239,16 @@ __device__ __forceinline__ float norm_of(const float (&x)[16], float eps, int hd
 #pragma unroll
   for (int o = 1; o < kLanes; o <<= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
   return rsqrtf(a / static_cast<float>(hd) + eps);
+}
+template <int kLanes>
+__device__ __forceinline__ void norm16(const Gains &k, float eps, int hd, float (&x)[16]) {
+  if (!k.norm) return;
+  const float inv = norm_of<kLanes>(x, eps, hd);
+  float g[16];
+  unpack8(k.g[0], g);
+  unpack8(k.g[1], g + 8);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) x[e] = x[e] * inv * g[e];
 }
 template <bool kHalf>
 __device__ __forceinline__ void turn16(float (&x)[16], const float (&c)[8], const float (&s)[8],
@@ -227,6 +278,9 @@ __device__ __forceinline__ void store_q(const Store8Fast &p, const TurnFreqs &tf
   constexpr int kEach = kQPieces / 4;  // of a warp
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const L at(lane, p.s.rot);
+  const Gains gains(p.gq, at);
+  uint64_t f[8 / L::kAtOnce];
+  turns_of(tf, at.pair0 + lane / L::kLanes * (8 / L::kAtOnce), at.turn0, f);
   const int64_t first = static_cast<int64_t>(block) * kQPieces + warp * kEach;
   uint4 v[kEach][2] = {};
   int pos[kEach], row[kEach], head[kEach];
@@ -242,24 +296,16 @@ __device__ __forceinline__ void store_q(const Store8Fast &p, const TurnFreqs &tf
       v[i][1] = *reinterpret_cast<const uint4 *>(src + at.d1);
     }
   }
-  float g[16];
-  if (p.gq) {
-    unpack8(*reinterpret_cast<const uint4 *>(p.gq + at.d0), g);
-    unpack8(*reinterpret_cast<const uint4 *>(p.gq + at.d1), g + 8);
-  }
   float c[8], s[8];
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     if (pos[i] < 0) continue;  // the whole warp's row
-    if (at.turn0 && (i == 0 || pos[i] != pos[i ? i - 1 : 0])) angles(tf, pos[i], at.pair0, p.s.mag, c, s);
+    if (p.s.rot && (i == 0 || pos[i] != pos[i ? i - 1 : 0]))  // uniform
+      query_angles<L>(f, lane, pos[i], p.s.mag, c, s);
     float x[16];
     unpack8(v[i][0], x);
     unpack8(v[i][1], x + 8);
-    if (p.gq) {
-      const float inv = norm_of<L::kLanes>(x, p.s.eps, HD);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = x[e] * inv * g[e];
-    }
+    norm16<L::kLanes>(gains, p.s.eps, HD, x);
     turn16<kHalf>(x, c, s, at.turn0, at.turn1);
     if (head[i] < p.hq) {
       uint16_t *dst = p.q_out + row[i] * p.qos + static_cast<int64_t>(head[i]) * HD;
@@ -269,10 +315,10 @@ __device__ __forceinline__ void store_q(const Store8Fast &p, const TurnFreqs &tf
   }
 }
 
-constexpr int kMostWindow = 16;
+constexpr int kMostWindow = 64;
 
 template <int HD, bool kHalf>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(128, 4)
     chunk_store8_fast_kernel(const __grid_constant__ Store8Fast p,
                              const __grid_constant__ TurnFreqs tf) {
   using L = Lanes<HD, kHalf>;
@@ -289,17 +335,19 @@ __global__ void __launch_bounds__(128)
   const Cache8 &cache = p.s.cache;
   const int hk = blockIdx.x % (2 * cache.nkv), kv = hk & 1, h = hk >> 1;
   const int first = blockIdx.x / (2 * cache.nkv) * p.window, block = cache.block;
-  if (static_cast<int>(threadIdx.x) <= p.window + block) {
-    const int t = first - 1 + static_cast<int>(threadIdx.x);
+  const L at(lane, kv ? 0 : p.s.rot);
+  const Gains gains(kv ? nullptr : p.s.gk, at);
+  uint64_t f[8];
+  turns_of(tf, at.pair0, at.turn0, f);
+  for (int x = threadIdx.x; x <= p.window + block; x += 128) {
+    const int t = first - 1 + x;
     const bool mine = hk == 0 && t >= first && t < first + p.window;  // reports it
-    s_block[threadIdx.x] = t >= 0 && t < p.s.n_rows ? block_of(p.s, t, mine) : -1;
+    s_block[x] = t >= 0 && t < p.s.n_rows ? block_of(p.s, t, mine) : -1;
   }
   __syncthreads();
-  const L at(lane, kv ? 0 : p.s.rot);
   const int sub = lane / L::kLanes;  // the lane's row of kAtOnce
   const uint16_t *src = (kv ? p.s.v : p.s.k) + static_cast<int64_t>(h) * HD;
   const int64_t step = kv ? p.s.vs : p.s.ks;
-  const uint16_t *gamma = kv ? nullptr : p.s.gk;
 
   int small = 0;  // runs that are one warp's, so far
   for (int i = 0; i < p.window; ++i) {
@@ -321,16 +369,18 @@ __global__ void __launch_bounds__(128)
     const int r0 = t0 + (together ? warp * each : 0);
     const int rows = max(min(each, t0 + n - r0), 0);
     uint4 v[kIters][2] = {};
-    int slot[kIters];
+    int slot[kIters], pos[kIters];
 #pragma unroll
     for (int j = 0; j < kIters; ++j) {
       const int r = j * L::kAtOnce + sub;
       slot[j] = -1;
+      pos[j] = 0;
       if (r < rows) {
         const uint16_t *x = src + (r0 + r) * step;
         v[j][0] = *reinterpret_cast<const uint4 *>(x + at.d0);
         v[j][1] = *reinterpret_cast<const uint4 *>(x + at.d1);
         slot[j] = p.s.slot[r0 + r];
+        pos[j] = p.s.pos[r0 + r];
       }
     }
     // the slots that the block's rows write: bit s of slot s
@@ -340,11 +390,6 @@ __global__ void __launch_bounds__(128)
               static_cast<uint64_t>(
                   __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(written >> 32)))
                   << 32;
-    float g[16];
-    if (gamma) {
-      unpack8(*reinterpret_cast<const uint4 *>(gamma + at.d0), g);
-      unpack8(*reinterpret_cast<const uint4 *>(gamma + at.d1), g + 8);
-    }
     float y[kIters][16], most = 0.f;
 #pragma unroll
     for (int j = 0; j < kIters; ++j) {
@@ -355,22 +400,24 @@ __global__ void __launch_bounds__(128)
       }
       unpack8(v[j][0], y[j]);
       unpack8(v[j][1], y[j] + 8);
-      if (gamma) {
-        const float inv = norm_of<L::kLanes>(y[j], p.s.eps, HD);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) y[j][e] = y[j][e] * inv * g[e];
-      }
+      norm16<L::kLanes>(gains, p.s.eps, HD, y[j]);
       if (at.turn0 && slot[j] >= 0) {
         float c[8], s[8];
-        angles(tf, p.s.pos[r0 + j * L::kAtOnce + sub], at.pair0, p.s.mag, c, s);
+        key_angles(f, pos[j], p.s.mag, c, s);
         turn16<kHalf>(y[j], c, s, at.turn0, at.turn1);
       }
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float a = fabsf(y[j][e]);
-        if (a < INFINITY) most = fmaxf(most, a);
-        else y[j][e] = NAN;
-      }
+      for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(y[j][e]));  // NaN counts for nothing
+    }
+    if (__any_sync(0xffffffffu, !(most < INFINITY))) {  // nor do infinities, which become NaN
+      most = 0.f;
+#pragma unroll
+      for (int j = 0; j < kIters; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (fabsf(y[j][e]) < INFINITY) most = fmaxf(most, fabsf(y[j][e]));
+          else y[j][e] = NAN;
+        }
     }
     most = warp_max(most);
     if (together) {
@@ -523,7 +570,7 @@ cudaError_t launch_chunk_rope_store8(const dflash_geom &g, int layer, int n_rows
     f.hq = g.hq;
     // Rows of a CTA's window: single tokens are a block each, a prompt's rows share one.
     f.window = 1;
-    while (f.window < kMostWindow && n_rows > 512 * f.window) f.window *= 2;
+    while (f.window < kMostWindow && n_rows > 256 * f.window) f.window *= 2;
     const int at_once = 512 / g.head_dim;
     f.q_pieces = (g.hq + at_once - 1) / at_once;
     const int64_t kv_blocks =
