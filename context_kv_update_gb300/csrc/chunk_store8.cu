@@ -349,12 +349,25 @@ __global__ void __launch_bounds__(128, 4)
   const uint16_t *src = (kv ? p.s.v : p.s.k) + static_cast<int64_t>(h) * HD;
   const int64_t step = kv ? p.s.vs : p.s.ks;
 
+  // bit i: row i of the window is the first of its block
+  auto starts = [&](int i) {
+    const bool yes = i < p.window && s_block[1 + i] >= 0 && s_block[i] != s_block[1 + i];
+    return __ballot_sync(0xffffffffu, yes);
+  };
+  uint64_t left = starts(lane) | static_cast<uint64_t>(p.window > 32 ? starts(32 + lane) : 0u) << 32;
   int small = 0;  // runs that are one warp's, so far
-  for (int i = 0; i < p.window; ++i) {
+  for (; left; left &= left - 1) {
+    const int i = __ffsll(static_cast<long long>(left)) - 1;
     const int64_t id = s_block[1 + i];
-    if (id < 0 || s_block[i] == id) continue;
-    int n = 1;  // rows of the block
-    while (n <= block && s_block[1 + i + n] == id) ++n;
+    // rows of the block: up to the first that is another's
+    auto others = [&](int r) {
+      return __ballot_sync(0xffffffffu, r <= block && s_block[1 + i + min(r, block)] != id);
+    };
+    uint32_t end = others(lane + 1);
+    int n = end ? __ffs(end) : 33;
+    if (!end && (end = others(lane + 33)) != 0) n = 32 + __ffs(end);
+    else if (!end) n = 65;
+    n = min(n, block + 1);
     if (n > block) {  // more rows than slots
       if (threadIdx.x == 0 && hk == 0) raise_status(p.s.st, DFLASH_DEV_BAD_ROWS);
       n = block;
@@ -468,6 +481,7 @@ __global__ void __launch_bounds__(128, 4)
 struct Read8Params {
   Cache8 cache;
   int n_rows, rows, vecs, sides;  // rows of a CTA, 16 codes each of a row's K (or V), K and V
+  int wide_out;                   // 32-byte aligned rows
   const int32_t *page, *slot;
   uint16_t *out[2];
   int64_t stride[2];
@@ -513,8 +527,15 @@ __global__ void __launch_bounds__(256) chunk_read8_kernel(const __grid_constant_
         const float2 v = e4m3_values(w[b >> 1] >> (16 * (b & 1)));
         o[b] = ptx::pack_bf16x2(v.x * f, v.y * f);
       }
-      reinterpret_cast<uint4 *>(to[i])[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      reinterpret_cast<uint4 *>(to[i])[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      if (p.wide_out) {  // whole sectors
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to[i]),
+                     "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]),
+                     "r"(o[7])
+                     : "memory");
+      } else {
+        reinterpret_cast<uint4 *>(to[i])[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        reinterpret_cast<uint4 *>(to[i])[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
     }
   }
 }
@@ -613,6 +634,9 @@ cudaError_t launch_chunk_read8(const dflash_geom &g, int layer, int n_rows,
   p.out[1] = static_cast<uint16_t *>(v_out);
   p.stride[0] = k_stride;
   p.stride[1] = v_stride;
+  p.wide_out = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out) |
+                 2 * static_cast<uintptr_t>(k_stride | v_stride)) &
+                31u) == 0;
   p.st = st;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = config(attr, (n_rows + p.rows - 1) / p.rows, 256, s);
