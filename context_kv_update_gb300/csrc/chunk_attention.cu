@@ -860,6 +860,8 @@ cudaError_t launch_main(bool pair, const CUtensorMap &tm, const CUtensorMap &tq,
               : launch_form<HD, false, false>(tm, tq, p, grid, s);
 }
 
+int tile_shift(const dflash_geom &g, int B, int n_rows) { return pair_form(g, B, n_rows) ? 8 : 7; }
+
 }  // namespace
 
 // Segments the keys are cut into, by a model of the call's time in key tiles: a CTA
@@ -879,7 +881,7 @@ cudaError_t launch_main(bool pair, const CUtensorMap &tm, const CUtensorMap &tq,
 // 16384 keys 162 with one segment, 105 with two, 124 with three; over up to 2048 keys 31
 // and 32 with two; one token over 32768 keys 33 with 19).
 int chunk_attention_num_segments(const dflash_geom &g, int B, int n_rows, int window) {
-  return segments_of(g, B, n_rows, window, 7.0, 3.0, 1.5);
+  return segments_of(g, B, n_rows, window, tile_shift(g, B, n_rows), 7.0, 3.0, 1.5);
 }
 
 size_t chunk_attention_workspace_bytes(const dflash_geom &g, int B, int n_rows, int S) {
@@ -893,7 +895,7 @@ cudaError_t launch_chunk_attention(const dflash_geom &g, int B, int layer, int n
                                    const int32_t *kv, int32_t window, const float *sinks,
                                    float scale, int mask_mode, int S, void *ws, void *out,
                                    int64_t out_stride, int32_t *st, cudaStream_t s) {
-  ChunkParams p = chunk_params(g, B, layer, n_rows, q, q_stride, tbl, cu, ctx, kv, window, sinks,
+  ChunkParams p = chunk_params(g, tile_shift(g, B, n_rows), B, layer, n_rows, q, q_stride, tbl, cu, ctx, kv, window, sinks,
                                scale, mask_mode, S, ws, out, out_stride, st);
   CUtensorMap tm;
   const uint64_t pool_rows = static_cast<uint64_t>(g.num_layers) * g.num_pool_pages * 2 * g.nkv *
@@ -905,7 +907,7 @@ cudaError_t launch_chunk_attention(const dflash_geom &g, int B, int layer, int n
   p.q_boxes = 128 % p.G == 0 && static_cast<int64_t>(n_rows) * p.G > 64LL * B &&
               q_stride < (1LL << 38);
   if (p.q_boxes && (e = q_tensor_map(&tq, g, n_rows, q, q_stride)) != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(chunk_tiles(g, B, n_rows) * g.nkv), 1, S);
+  const dim3 grid(static_cast<unsigned>(chunk_tiles(g, B, n_rows, tile_shift(g, B, n_rows)) * g.nkv), 1, S);
   const bool pair = pair_form(g, B, n_rows);
   e = g.head_dim == 64 ? launch_main<64>(pair, tm, tq, p, grid, s)
                        : launch_main<128>(pair, tm, tq, p, grid, s);

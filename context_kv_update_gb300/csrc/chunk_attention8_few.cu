@@ -1,0 +1,569 @@
+// chunk_attention8_few.cu -- attention over a cache held in 8 bits where a work tile has few rows
+// (at most 64 of a token and head; single tokens, short drafts) and the key stream is the work.
+//
+// The kernel of chunk_attention8.cu with the products turned round: the 128 keys of a tile are
+// the rows of both results' operands, S^T = K Q^T and O^T = V^T P^T.  The tensor cores then do
+// work for N = 16, 32 or 64 rows instead of 128, K's tile is read from shared memory once for
+// both parts of Q, and a softmax thread is a key with N scores: 128 threads share what one warp
+// did for all keys of a tile (64 single tokens over up to 8192 keys: 219 us that way).
+//
+// The maximum over keys now runs across threads, so it is only taken when it is needed: a
+// thread weighs its scores with the reference it has, and where one exceeds it by 2^8 (a vote of
+// the group), or the accumulator's unit changes, the group takes the tile's maxima and scales
+// the accumulators (as a rule with its first tile alone).  A row's sum stays in the threads,
+// each its keys', until the end.
+//
+// Bound by HBM: see the launcher.
+#include "chunk8_roles.cuh"
+
+namespace dflash {
+namespace {
+
+template <int N>
+struct LayoutFew : Bars<N == 64 ? 3 : 4, 3, 2> {
+  using B = Bars<N == 64 ? 3 : 4, 3, 2>;
+  static constexpr int kHD = 128, kShift = N == 16 ? 4 : N == 32 ? 5 : 6;
+  static constexpr bool kPair = false;
+  static constexpr uint32_t kTile = kKT * kHD, kTile16 = 2 * kTile;
+  static constexpr uint32_t kK = 2 * N * 128;  // Q: N rows of hi, N of lo
+  static constexpr uint32_t kV = kK + B::kKs * kTile;
+  static constexpr uint32_t kWide = kV + B::kVs * kTile;
+  static constexpr uint32_t kP = kWide + B::kWides * kTile16;  // of each group: 128 keys of 128 bytes
+  static constexpr uint32_t kRowState = kP + 2 * kKT * 128;
+  static constexpr uint32_t kMeta = kRowState + (2 * N + 2 * N * 11 + 2) * 4 / 16 * 16 + 16;
+  static constexpr uint32_t kSortTiles = kMeta + kMetaBatch * kMetaBatches * sizeof(TileMeta);
+  static constexpr uint32_t kPlaces = kSortTiles + 4 * kSorted;
+  static constexpr uint32_t kWork = kPlaces + kSorted;
+  static constexpr uint32_t kAnswer = kWork + 2 * sizeof(Work);
+  static constexpr uint32_t kBars = kAnswer + 16;
+  static constexpr uint32_t kWords = kBars + 8 * B::kBarCount;
+  static constexpr uint32_t kBytes = 1024 + kWords + 16;
+  static_assert(kBytes <= kSmemMax, "");
+};
+
+// N columns of this warp's lanes.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&r)[N]) {
+  if constexpr (N == 64) {
+    ptx::tmem_ld64f_sync(taddr, r);
+  } else if constexpr (N == 32) {
+    ptx::tmem_ld32f_sync(taddr, r);
+  } else {
+    static_assert(N == 16, "");
+    uint32_t v[16];
+    ptx::tmem_ld16_sync(taddr, v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __uint_as_float(v[i]);
+  }
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+        "=f"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+
+template <int N, bool kMany>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_attn8_few_kernel(const __grid_constant__ CUtensorMap tm,
+                           const __grid_constant__ ChunkParams p,
+                           const __grid_constant__ Cache8 cache) {
+  using Lay = LayoutFew<N>;
+  constexpr int HD = 128, kKs = Lay::kKs, kWides = Lay::kWides;
+  // S^T: hi's scores, then lo's, as one product; 64 rows: both into the same columns, since a
+  // thread cannot hold 128 scores beside its sums.
+  constexpr bool kApart = N < 64;
+  constexpr int kCols = kApart ? 2 * N : N;
+  constexpr uint32_t kColOut = 256;  // S of group g at 128 g, O at 256 + 64 g
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                            ~static_cast<uintptr_t>(1023));
+  const uint32_t sm0 = ptx::smem_u32(sm);
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Lay::kWords);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tslot + 1);
+  float *q_scale = reinterpret_cast<float *>(sm + Lay::kRowState);  // of two works: [2][N]
+  int *sort_tiles = reinterpret_cast<int *>(sm + Lay::kSortTiles);
+  uint8_t *sort_places = sm + Lay::kPlaces;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Cta<Lay> cta = {sm, sm0, lane, abort_flag, reinterpret_cast<Work *>(sm + Lay::kWork),
+                        reinterpret_cast<TileMeta *>(sm + Lay::kMeta)};
+
+  if (threadIdx.x == 0) {
+    cta.init_bars();
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&tm);
+  }
+  if (warp == 8) {
+    ptx::tmem_alloc(ptx::smem_u32(tslot), kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tslot;
+  ptx::griddep_launch();
+  ptx::griddep_wait();
+
+  const bool sorted = kMany && p.B > 1 && p.B <= kSorted;
+  if (sorted) sort_requests<false>(p, Lay::kShift, sort_tiles, sort_places);
+
+  if (warp >= 12) {
+    regs_less<kWidenRegs>();
+    // ------------------------------------------------ Q's split, V's widening
+    const Widener<Lay> widener(warp, lane);
+    int at = 0, batches = 0;  // V tiles and batches of scales so far
+    uint32_t loads = 0u;
+    bool ok = true;
+    for (uint32_t w = 0; w == 0 || kMany; ++w) {
+      const Work d = cta.next_work(w);
+      cta.have_read();
+      if (d.nrow == 0) break;
+      if (d.n == 0 || !ok) continue;
+      // (rows past the work's are zeros: their scores exceed no reference)
+      ok = split_rows(cta, p, d, N, loads++,
+                      [&](int row, int u, const uint32_t *hi, const uint32_t *lo, int e) {
+        uint8_t *dst = sm + row * 128 + ((u ^ (row & 7)) << 4);
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(dst + N * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        if (u == 0) q_scale[(w & 1) * N + row] = exp2_int(e);
+      });
+      if (ok) ok = widen_tiles(cta, widener, d, at, batches);
+    }
+  } else if (warp >= 8) {
+    regs_less<kIssueRegs>();
+    if (warp == 8) {
+      schedule<kMany>(cta, p, sorted, sort_tiles, sort_places);
+    } else if (warp == 9) {
+      look_up_scales<kMany>(cta, p, cache);
+    } else if (warp == 10) {
+      load_tiles<kMany>(cta, p, tm);
+    } else {
+      // ---------------------------------------------- MMA issuer
+      constexpr uint32_t idesc_qk = idesc_of(128, kCols, 0, false);
+      constexpr uint32_t idesc_f16 = idesc_of(128, N, 0, true) | 1u << 15,  // V^T: dims contiguous
+          idesc_bf16 = idesc_of(128, N, 1, true) | 1u << 15;
+      // warp-uniform copies
+      const uint32_t tm0 = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t base = __shfl_sync(0xffffffffu, sm0, 0);
+      const uint64_t dq = ptx::desc_kmajor_sw128(base, 0);
+      const uint64_t dk = ptx::desc_kmajor_sw128(base + Lay::kK, 0);
+      const uint64_t dv = ptx::smem_desc(base + Lay::kWide, kChunkBytes, 1024, ptx::kSwizzle128B);
+      const uint64_t dp = ptx::smem_desc(base + Lay::kP, kChunkBytes, 1024, ptx::kSwizzle128B);
+      struct At {
+        uint32_t bar, phase;
+      };
+      int at_k = 0, at_v = 0, batches = 0;  // of K tiles, V tiles, batches of scales
+      uint32_t handed0 = 0u, handed1 = 0u, loads = 0u;  // phases of p_full and q_ready
+      bool ok = true;
+      auto slot = [&](int first, int at, int n) {
+        return At{cta.bar(first + at % n), static_cast<uint32_t>((at / n) & 1)};
+      };
+      // up to three barriers at the cost of one: each is polled by lanes of its own
+      auto wait = [&](At a, At b, At c) {
+        const At x = lane == 1 ? b : lane == 2 ? c : a;
+        const bool got = __all_sync(0xffffffffu, chunk_wait<true>(x.bar, x.phase, abort_flag));
+        ptx::tc_fence_after();
+        return got;
+      };
+      auto qk = [&](int g, int at) {  // S_g^T = K (hi, lo)^T
+        const uint64_t a = dk + (((at % kKs) * Lay::kTile) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < (kApart ? 4 : 8); ++ks)
+          mma_e4m3(tm0 + 128 * g, a + ((ks & 3) * 32 >> 4),
+                   dq + (((ks & 3) * 32 + (ks >> 2) * N * 128) >> 4), idesc_qk, ks > 0 ? 1u : 0u);
+        ptx::mma_commit(cta.bar(Lay::kSFull + g));
+        ptx::mma_commit(cta.bar(Lay::kKEmpty + at % kKs));
+      };
+      auto pv = [&](int g, int at, bool first, uint32_t idesc) {  // O_g^T (+)= V^T P^T
+        const uint64_t a = dv + (((at % kWides) * Lay::kTile16) >> 4);
+        const uint64_t b = dp + ((g * kKT * 128) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < kKT / 16; ++ks)
+          ptx::mma_bf16(tm0 + kColOut + 64 * g, a + ((ks * 2048) >> 4), b + ((ks * 2048) >> 4),
+                        idesc, (!first || ks > 0) ? 1u : 0u);
+        ptx::mma_commit(cta.bar(Lay::kWEmpty + at % kWides));
+      };
+      for (uint32_t w = 0; w == 0 || kMany; ++w) {
+        const Work d = cta.next_work(w);
+        cta.have_read();
+        if (d.nrow == 0) break;
+        const int tiles = __shfl_sync(0xffffffffu, d.n, 0);
+        if (!ok || tiles == 0) continue;
+        ok = wait(At{cta.bar(Lay::kQReady), loads & 1}, slot(Lay::kKFull, at_k, kKs),
+                  slot(Lay::kKFull, tiles > 1 ? at_k + 1 : at_k, kKs));
+        ++loads;
+        if (ok && elect_one()) {
+          qk(0, at_k);
+          if (tiles > 1) qk(1, at_k + 1);
+          if (tiles <= 2) ptx::mma_commit(cta.bar(Lay::kQEmpty));
+        }
+        __syncwarp();
+        for (int t = 0; ok && t < tiles; ++t) {
+          const bool more = t + 2 < tiles;
+          const int b = batches + t / kMetaBatch, g = t & 1;
+          const At v = slot(Lay::kWFull, at_v + t, kWides);
+          ok = wait(At{cta.bar(Lay::kPFull + g), (g ? handed1 : handed0) & 1}, v,
+                    more ? slot(Lay::kKFull, at_k + t + 2, kKs) : v);
+          if (!ok) break;
+          if (g) ++handed1; else ++handed0;
+          // (the widening warps and the group that handed P over have seen the tile's scales)
+          const uint32_t idesc =
+              __shfl_sync(0xffffffffu, cta.scales(b, t).far ? idesc_bf16 : idesc_f16, 0);
+          if (elect_one()) {
+            pv(g, at_v + t, t < 2, idesc);
+            if (more) {
+              qk(g, at_k + t + 2);
+              if (t + 2 == tiles - 1) ptx::mma_commit(cta.bar(Lay::kQEmpty));
+            } else {
+              ptx::mma_commit(cta.bar(Lay::kODone + g));
+            }
+          }
+          __syncwarp();
+          if ((t % kMetaBatch == kMetaBatch - 1 || t == tiles - 1) && lane == 0)
+            ptx::mbar_arrive(cta.bar(Lay::kMEmpty + b % kMetaBatches));
+        }
+        at_k += tiles;
+        at_v += tiles;
+        batches += (tiles + kMetaBatch - 1) / kMetaBatch;
+      }
+      if (!ok) {
+        if (elect_one()) ptx::mma_commit(cta.bar(Lay::kDrain));
+        __syncwarp();
+        volatile int dummy = 0;
+        chunk_wait<false>(cta.bar(Lay::kDrain), 0u, &dummy);
+      }
+    }
+  } else {
+    regs_more<kSoftmaxRegs>();
+    // ------------------------------------------------ softmax groups: a key a thread
+    const int g = warp >> 2, w4 = warp & 3;
+    const int tid = threadIdx.x & 127;  // TMEM lane = key of the tile, at the end a dim
+    const uint32_t lane_off = static_cast<uint32_t>(w4 * 32) << 16;
+    const uint32_t tm_s = tmem + 128 * g + lane_off;
+    // a group's rows: lo, hi, factor, reference (kLift - it), scaling; warps' maxima or sums [4]
+    float *rows = q_scale + 2 * N + g * 11 * N, *other = q_scale + 2 * N + (g ^ 1) * 11 * N;
+    int *row_lo = reinterpret_cast<int *>(rows), *row_hi = row_lo + N;
+    float *row_f = rows + 2 * N, *row_nm = rows + 3 * N, *row_corr = rows + 4 * N,
+          *part = rows + 5 * N, *row_m = rows + 9 * N, *row_l = rows + 10 * N;
+    float *units = q_scale + 2 * N + 22 * N;  // of the groups' accumulators
+    int batches = 0;
+    uint32_t loads = 0u, scores = 0u, outs0 = 0u, outs1 = 0u;  // of q_ready, s_full, o_done
+    bool ok = true;
+    for (uint32_t wk = 0; wk == 0 || kMany; ++wk) {
+      const volatile Work &d = cta.shared_work[wk & 1];
+      volatile int dummy = 0;
+      int nrow = 0, n = 0;
+      if (__all_sync(0xffffffffu,
+                     chunk_wait<false, 16>(cta.bar(Lay::kWorkFull), wk & 1, &dummy))) {
+        nrow = d.nrow;
+        n = d.n;
+      } else {
+        *abort_flag = 1;
+      }
+      cta.have_read();
+      if (nrow == 0) break;
+      if (n > 0) {
+        if (ok)
+          ok = __all_sync(0xffffffffu,
+                          chunk_wait<false>(cta.bar(Lay::kQReady), loads & 1, abort_flag));
+        ++loads;
+      }
+      const int row0 = d.row0, t0 = d.t0;
+      // keys that every row sees
+      int all_lo, all_hi, x;
+      key_range(p, d.c + row0 / p.G, d.kv, &x, &all_hi);
+      key_range(p, d.c + (row0 + nrow - 1) / p.G, d.kv, &all_lo, &x);
+      if (tid < N) {
+        const bool real = tid < nrow;
+        int lo = 0, hi = -1;
+        if (real) key_range(p, d.c + (row0 + tid) / p.G, d.kv, &lo, &hi);
+        row_lo[tid] = lo;
+        row_hi[tid] = hi;
+        row_f[tid] = real && ok && n > 0 ? q_scale[(wk & 1) * N + tid] * p.scale_log2 : 0.f;
+        row_m[tid] = real ? -INFINITY : 0.f;
+        row_nm[tid] = real ? INFINITY : 0.f;  // no reference yet: every score exceeds it
+      }
+      ptx::bar_sync(2 + g, 128);
+
+      float l[N];
+#pragma unroll
+      for (int r = 0; r < N; ++r) l[r] = 0.f;
+      int E = 0, left = 0;
+      auto hand_back = [&](int to_batch) {
+        __syncwarp();
+        for (; left < to_batch; ++left)
+          if (lane == 0) ptx::mbar_arrive(cta.bar(Lay::kMEmpty + (batches + left) % kMetaBatches));
+      };
+      for (int t = g; ok && t < n; t += 2) {
+        const int b = batches + t / kMetaBatch;
+        hand_back(t / kMetaBatch);
+        bool got = cta.arrived(Lay::kMFull, b, kMetaBatches) &&
+                   chunk_wait<false>(cta.bar(Lay::kSFull + g), scores & 1, abort_flag);
+        got = __all_sync(0xffffffffu, got);
+        ++scores;
+        ptx::tc_fence_after();
+        const TileMeta &tile = cta.scales(b, t);
+        const int kb = (t0 + t) * kKT, key = kb + tid;
+        const float kf = tile.k[tid >> 4];
+        const bool dead = (tile.bad >> (tid >> 4)) & 1;
+        const bool cut = !(all_lo <= kb && all_hi >= kb + kKT - 1);
+        const bool far = tile.far != 0;
+        float y[N];
+        // Scores, in powers of two: relative to the rows' references, or as they are.
+        auto weigh = [&](bool absolute) {
+          float sv[kCols];
+          tmem_ld<kCols>(tm_s, sv);
+#pragma unroll
+          for (int r = 0; r < N; r += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(row_f + r);
+            float4 nm = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (!absolute) nm = *reinterpret_cast<const float4 *>(row_nm + r);
+            const float fs[4] = {f.x, f.y, f.z, f.w}, ns[4] = {nm.x, nm.y, nm.z, nm.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float s = kApart ? sv[r + e] + sv[(kApart ? N : 0) + r + e] : sv[r + e];
+              y[r + e] = fmaf(s, fs[e] * kf, ns[e]);
+            }
+          }
+          if (cut) {
+#pragma unroll
+            for (int r = 0; r < N; ++r)
+              if (key < row_lo[r] || key > row_hi[r]) y[r] = -INFINITY;
+          }
+          if (dead) {
+#pragma unroll
+            for (int r = 0; r < N; ++r) y[r] = -INFINITY;
+          }
+        };
+        bool need = !got || tile.E != E;
+        if (got) {
+          weigh(false);
+          float top = y[0];
+#pragma unroll
+          for (int r = 1; r < N; ++r) top = fmaxf(top, y[r]);
+          need = need || top > 8.f + kLift;
+        }
+        // (A warp whose wait ran out votes too, and all end together: a barrier has no limit.)
+        if (ptx::bar_or(2 + g, 128, need)) {
+          if (ptx::bar_or(2 + g, 128, !got)) {
+            ok = false;
+            break;
+          }
+          weigh(true);
+#pragma unroll
+          for (int r = 0; r < N; ++r) {  // the warp's maximum, floats in the order of integers
+            int i = __float_as_int(y[r]);
+            i = __reduce_max_sync(0xffffffffu, i ^ (i >> 31 & 0x7fffffff));
+            if (lane == (r & 31)) part[w4 * N + r] = __int_as_float(i ^ (i >> 31 & 0x7fffffff));
+          }
+          ptx::bar_sync(2 + g, 128);
+          const float grown = ptx::ex2(static_cast<float>(E - tile.E));
+          if (tid < N) {
+            const float top = fmaxf(fmaxf(part[tid], part[N + tid]),
+                                    fmaxf(part[2 * N + tid], part[3 * N + tid]));
+            const float m = row_m[tid];
+            float now = m;
+            if (m == -INFINITY || top > m + 8.f) now = fmaxf(m, top);
+            row_corr[tid] = m == -INFINITY ? 1.f : ptx::ex2(m - now);
+            row_m[tid] = now;
+            if (tid < nrow) row_nm[tid] = now == -INFINITY ? INFINITY : kLift - now;
+          }
+          ptx::bar_sync(2 + g, 128);
+#pragma unroll
+          for (int r = 0; r < N; ++r) l[r] *= row_corr[r];
+          if (t >= 2) {  // the group's product before this S is complete
+            const uint32_t tm_o = tmem + kColOut + 64 * g + lane_off;
+#pragma unroll 1
+            for (int c = 0; c < N; c += 16) {
+              uint32_t ov[16];
+              ptx::tmem_ld16_sync(tm_o + c, ov);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                ov[e] = __float_as_uint(__uint_as_float(ov[e]) * (row_corr[c + e] * grown));
+              ptx::tmem_st16(tm_o + c, ov);
+            }
+            ptx::tmem_wait_st();
+          }
+          E = tile.E;
+          weigh(false);
+        }
+        uint32_t pk[N / 2];
+#pragma unroll
+        for (int r = 0; r < N; ++r) {
+          y[r] = ptx::ex2(y[r]);
+          l[r] += y[r];
+        }
+        if (far) {
+#pragma unroll
+          for (int r = 0; r < N / 2; ++r) pk[r] = ptx::pack_bf16x2(y[2 * r], y[2 * r + 1]);
+        } else {
+#pragma unroll
+          for (int r = 0; r < N / 2; ++r) pk[r] = pack_f16x2(y[2 * r], y[2 * r + 1]);
+        }
+        uint8_t *dst = sm + Lay::kP + g * kKT * 128 + tid * 128;
+#pragma unroll
+        for (int u = 0; u < N / 8; ++u)
+          *reinterpret_cast<uint4 *>(dst + ((u ^ (tid & 7)) << 4)) =
+              make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+        ptx::fence_proxy_async_smem();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(cta.bar(Lay::kPFull + g));
+      }
+      const int all = (n + kMetaBatch - 1) / kMetaBatch;
+      hand_back(all);
+      batches += all;
+      // ---------------------------------------------- epilogue
+      const bool had0 = n > 0, had1 = n > 1;  // groups with products
+      if (ok && had0)
+        ok = __all_sync(0xffffffffu,
+                        chunk_wait<false>(cta.bar(Lay::kODone), outs0 & 1, abort_flag));
+      if (ok && had1)
+        ok = __all_sync(0xffffffffu,
+                        chunk_wait<false>(cta.bar(Lay::kODone + 1), outs1 & 1, abort_flag));
+      ptx::tc_fence_after();
+      outs0 += had0;
+      outs1 += had1;
+      // Sums over the warp's keys: each step halves the rows a lane holds.
+#pragma unroll
+      for (int o = 16, c = N / 2; o > 0; o >>= 1, c >>= 1) {
+        if (c > 0) {
+#pragma unroll
+          for (int r = 0; r < c; ++r) {
+            const float give = lane & o ? l[r] : l[r + c], keep = lane & o ? l[r + c] : l[r];
+            l[r] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+          }
+        } else {
+          l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+        }
+      }
+      if constexpr (N == 16) {
+        if (!(lane & 1)) part[w4 * N + (lane >> 1)] = l[0];
+      } else {
+#pragma unroll
+        for (int r = 0; r < N / 32; ++r) part[w4 * N + lane * (N / 32) + r] = l[r];
+      }
+      ptx::bar_sync(2 + g, 128);
+      if (tid < N)
+        row_l[tid] = (part[tid] + part[N + tid]) + (part[2 * N + tid] + part[3 * N + tid]);
+      if (tid == 0) units[g] = exp2_int(min(max(E, -149), 127));
+      const bool broken = ptx::bar_or(1, 256, !ok);
+      ok = ok && !broken;
+      const int seg = d.seg;
+      // a row's factors of the two accumulators, by its thread of group 0
+      float *f0 = row_corr, *f1 = other + 4 * N;
+      if (g == 0 && tid < N) {
+        const float m0 = broken ? -INFINITY : row_m[tid], m1 = broken ? -INFINITY : other[9 * N + tid];
+        const bool any = tid < nrow && fmaxf(m0, m1) != -INFINITY;
+        const float m = fmaxf(m0, m1) - kLift;  // weights are relative to this
+        const float w0 = m0 == -INFINITY ? 0.f : ptx::ex2(m0 - kLift - m),
+                    w1 = m1 == -INFINITY ? 0.f : ptx::ex2(m1 - kLift - m);
+        const float sum = row_l[tid] * w0 + other[10 * N + tid] * w1;
+        const int flat = row0 + tid, tok = flat / p.G, h = d.kvh * p.G + flat - tok * p.G;
+        float gain = 1.f;
+        if (p.S == 1) {
+          float top = m, den = sum;
+          if (p.sinks && any) {
+            const float sk = p.sinks[h] * kLog2e;
+            top = fmaxf(m, sk);
+            den = sum * ptx::ex2(m - top) + ptx::ex2(sk - top);
+          }
+          gain = any ? ptx::ex2(m - top) / den : 0.f;
+        } else if (tid < nrow) {
+          const int64_t at = ((static_cast<int64_t>(d.a) + tok) * p.hq + h) * p.S + seg;
+          p.ws_m[at] = any ? m : -INFINITY;
+          p.ws_l[at] = any ? sum : 0.f;
+        }
+        f0[tid] = any ? w0 * units[0] * gain : 0.f;
+        f1[tid] = any ? w1 * units[1] * gain : 0.f;
+        row_nm[tid] = any ? 1.f : 0.f;
+      }
+      ptx::bar_sync(1, 256);
+      if (g) {  // (read where group 0 wrote)
+        f0 = other + 4 * N;
+        f1 = row_corr;
+      }
+      const float *has_keys = g ? other + 3 * N : row_nm;
+      // Half of the rows a group, a dim a thread.
+#pragma unroll 1
+      for (int c = g * (N / 2); c < (g + 1) * (N / 2); c += 8) {
+        if (c >= nrow) break;
+        float o[8] = {};
+        if (ok && had0) {
+          float v[8];
+          tmem_ld8(tmem + kColOut + lane_off + c, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = f0[c + e] != 0.f ? v[e] * f0[c + e] : 0.f;
+        }
+        if (ok && had1) {
+          float v[8];
+          tmem_ld8(tmem + kColOut + 64 + lane_off + c, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] += f1[c + e] != 0.f ? v[e] * f1[c + e] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (c + e >= nrow) break;
+          const int flat = row0 + c + e, tok = flat / p.G, h = d.kvh * p.G + flat - tok * p.G;
+          const int64_t orow = static_cast<int64_t>(d.a) + tok;
+          if (p.S == 1)
+            p.out[orow * p.os + static_cast<int64_t>(h) * HD + tid] = f32_to_bf16_rn(o[e]);
+          else if (has_keys[c + e] != 0.f)
+            p.ws_o[((orow * p.hq + h) * p.S + seg) * HD + tid] = o[e];
+        }
+      }
+      ptx::tc_fence_before();
+      ptx::bar_sync(1, 256);  // the accumulators and the rows' state were read
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) raise_status(p.st, DFLASH_DEV_WAIT_TIMEOUT);
+  if (warp == 8) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int N, bool kMany>
+cudaError_t launch_form(const CUtensorMap &tm, const ChunkParams &p, const Cache8 &cache, dim3 grid,
+                        cudaStream_t s) {
+  const cudaError_t e = ensure_smem_limit<chunk_attn8_few_kernel<N, kMany>>(kSmemMax);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = LayoutFew<N>::kBytes;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_attn8_few_kernel<N, kMany>, tm, p, cache);
+}
+
+template <int N>
+cudaError_t launch_rows(const CUtensorMap &tm, const ChunkParams &p, const Cache8 &cache, dim3 grid,
+                        cudaStream_t s) {
+  return static_cast<int64_t>(grid.x) * grid.z > device_sm_count()
+             ? launch_form<N, true>(tm, p, cache, grid, s)
+             : launch_form<N, false>(tm, p, cache, grid, s);
+}
+
+}  // namespace
+
+cudaError_t launch_attn8_few(int shift, const CUtensorMap &tm, const ChunkParams &p,
+                             const Cache8 &cache, dim3 grid, cudaStream_t s) {
+  return shift == 4   ? launch_rows<16>(tm, p, cache, grid, s)
+         : shift == 5 ? launch_rows<32>(tm, p, cache, grid, s)
+                      : launch_rows<64>(tm, p, cache, grid, s);
+}
+
+}  // namespace dflash

@@ -22,15 +22,6 @@ using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t,
                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiled encode_tiled_fn();
 
-namespace {
-
-constexpr int kKT = kAttnTileKeys;  // 128 keys per tile
-constexpr int kSmemMax = 227 * 1024;
-constexpr uint32_t kChunkBytes = kKT * 128;  // 64 dims of 128 rows, 128-byte swizzled
-constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 256;  // S of group g at 128 g, O at 256 + HD g
-constexpr float kLog2e = 1.4426950408889634f;
-
 struct ChunkParams {
   int B, n_rows, hq, nkv, G, wide_out, layer, NP, P, M, window, mask_mode, S;
   int box_rows, skip_tile, q_boxes;
@@ -45,6 +36,16 @@ struct ChunkParams {
   uint16_t *out;
   int32_t *st;
 };
+
+namespace {
+
+constexpr int kKT = kAttnTileKeys;  // 128 keys per tile
+constexpr int kSmemMax = 227 * 1024;
+constexpr uint32_t kChunkBytes = kKT * 128;  // 64 dims of 128 rows, 128-byte swizzled
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 256;  // S of group g at 128 g, O at 256 + HD g
+constexpr float kLog2e = 1.4426950408889634f;
+
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -421,38 +422,38 @@ inline bool pair_form(const dflash_geom &g, int B, int n_rows) {
   return static_cast<int64_t>(n_rows) * (g.hq / g.nkv) > 128LL * B;
 }
 
-// Work tiles of a chunk, at most.
-inline int64_t chunk_tiles(const dflash_geom &g, int B, int n_rows) {
-  return ((static_cast<int64_t>(n_rows) * (g.hq / g.nkv)) >> (pair_form(g, B, n_rows) ? 8 : 7)) + B;
+// Work tiles of a chunk, at most (of 2^shift rows).
+inline int64_t chunk_tiles(const dflash_geom &g, int B, int n_rows, int shift) {
+  return ((static_cast<int64_t>(n_rows) * (g.hq / g.nkv)) >> shift) + B;
 }
 
 // Work tiles of a call with one request.
-inline int64_t works_of_one(const dflash_geom &g, int n_rows) {
-  const int tr = pair_form(g, 1, n_rows) ? 256 : 128;
+inline int64_t works_of_one(const dflash_geom &g, int n_rows, int shift) {
+  const int tr = 1 << shift;
   return (static_cast<int64_t>(n_rows) * (g.hq / g.nkv) + tr - 1) / tr * g.nkv;
 }
 
 // Two segments of one request: its work tiles fill the SMs a whole number of times
 // but for some; each SM left over takes the tails of this many tiles, cut so that all end
 // together (1: halves).
-inline int tail_tiles(const dflash_geom &g, int B, int n_rows) {
+inline int tail_tiles(const dflash_geom &g, int B, int n_rows, int shift) {
   if (B != 1) return 1;
-  const int64_t works = works_of_one(g, n_rows), sms = device_sm_count();
+  const int64_t works = works_of_one(g, n_rows, shift), sms = device_sm_count();
   const int64_t idle = (works + sms - 1) / sms * sms - works;
   return idle == 0 ? 1 : static_cast<int>(std::min<int64_t>((works + idle - 1) / idle, 64));
 }
 
 // `fixed`: what a CTA costs beside its key tiles, `merge`: what the second launch does, both in
 // key tiles, of `tile_us` each where few rows stream them.
-inline int segments_of(const dflash_geom &g, int B, int n_rows, int window, double fixed,
+inline int segments_of(const dflash_geom &g, int B, int n_rows, int window, int shift, double fixed,
                        double merge, double tile_us) {
-  const double ctas = static_cast<double>(chunk_tiles(g, B, n_rows)) * g.nkv;
+  const double ctas = static_cast<double>(chunk_tiles(g, B, n_rows, shift)) * g.nkv;
   const double sms = device_sm_count();
   double longest = static_cast<double>(g.max_pages) * g.page_size / kKT;
   if (window > 0) longest = std::min(longest, (static_cast<double>(window) + n_rows) / kKT + 1.0);
   const double mean = B >= 4 ? 0.6 * longest : longest;
   const bool alike = B == 1 && longest * kKT >= 2.0 * n_rows;
-  const int64_t works = works_of_one(g, n_rows), left = works % device_sm_count();
+  const int64_t works = works_of_one(g, n_rows, shift), left = works % device_sm_count();
   // a segment's partial results, written and read: key tiles at 6 TB/s
   const double part = 8.0 * n_rows * g.hq * g.head_dim / (tile_us * 6e6);
   int best = 1;
@@ -460,7 +461,7 @@ inline int segments_of(const dflash_geom &g, int B, int n_rows, int window, doub
   for (int S = 1; S == 1 || (S <= 64 && 4 * S <= longest && ctas * (S - 1) <= 4 * sms); ++S) {
     double one = fixed + longest / S;
     if (S == 2 && alike)
-      one = fixed + main_tiles(static_cast<int>(longest), tail_tiles(g, B, n_rows));
+      one = fixed + main_tiles(static_cast<int>(longest), tail_tiles(g, B, n_rows, shift));
     double t = one;
     if (alike)
       t *= std::ceil(static_cast<double>(works) * (S == 2 && left ? 1 : S) / sms);
@@ -482,7 +483,8 @@ inline size_t workspace_of(const dflash_geom &g, int n_rows, int S) {
 }
 
 // What both kernels and the merge are given.
-inline ChunkParams chunk_params(const dflash_geom &g, int B, int layer, int n_rows, const void *q,
+inline ChunkParams chunk_params(const dflash_geom &g, int shift, int B, int layer, int n_rows,
+                                const void *q,
                                 int64_t q_stride, const int32_t *tbl, const int32_t *cu,
                                 const int32_t *ctx, const int32_t *kv, int32_t window,
                                 const float *sinks, float scale, int mask_mode, int S, void *ws,
@@ -503,7 +505,7 @@ inline ChunkParams chunk_params(const dflash_geom &g, int B, int layer, int n_ro
   p.mask_mode = mask_mode;
   p.S = S;
   p.box_rows = std::min(p.P, kKT);
-  p.tails = S == 2 ? tail_tiles(g, B, n_rows) : 1;
+  p.tails = S == 2 ? tail_tiles(g, B, n_rows, shift) : 1;
   p.skip_tile = attention_test_skip_tile_value();
   p.scale_log2 = scale * kLog2e;  // scale > 0 (validated by the caller)
   p.q = static_cast<const uint16_t *>(q);
