@@ -138,6 +138,21 @@ struct Cta {
   __device__ __forceinline__ bool arrived(int first, int at, int n) const {
     return chunk_wait<false>(bar(first + at % n), static_cast<uint32_t>((at / n) & 1), abort_flag);
   }
+  // Waits on up to three barriers at the cost of one: each is polled by lanes of its own.
+  struct At {
+    uint32_t bar, phase;
+  };
+  __device__ __forceinline__ At full(int first, int at, int n) const {
+    return At{bar(first + at % n), static_cast<uint32_t>((at / n) & 1)};
+  }
+  __device__ __forceinline__ At empty(int first, int at, int n) const {  // at >= n
+    return At{bar(first + at % n), static_cast<uint32_t>((at / n - 1) & 1)};
+  }
+  template <bool kSpin>
+  __device__ __forceinline__ bool wait(At a, At b, At e) const {
+    const At x = lane == 1 ? b : lane == 2 ? e : a;
+    return __all_sync(0xffffffffu, chunk_wait<kSpin>(x.bar, x.phase, abort_flag));
+  }
   __device__ __forceinline__ const TileMeta &scales(int batch, int t) const {
     return meta[batch % kMetaBatches * kMetaBatch + t % kMetaBatch];
   }
@@ -268,7 +283,9 @@ __device__ __forceinline__ void look_up_scales(const Cta<Lay> &c, const ChunkPar
 #pragma unroll
       for (int i = 0; i < kMetaBatch; ++i) {
         const int mx = __shfl_sync(0xffffffffu, top, 8 * i),
-                  mn = __shfl_sync(0xffffffffu, low, 8 * i), grown = max(E, mx);
+                  mn = __shfl_sync(0xffffffffu, low, 8 * i);
+        // (a little more than it must: the accumulators are scaled whenever it grows)
+        const int grown = mx > E ? min(mx + 2, 127) : E;
         far = far || (mn != kNone && mn < grown - 14);
         if (!far) E = grown;
         if (i == mine) {
@@ -508,8 +525,7 @@ struct Widener {
         if (i == 2) f = (v1 & 0xffffu) * 0x10001u;
         uint4 x[kSub];
 #pragma unroll
-        for (int e = 0; e < kSub; ++e)
-          x[e] = *reinterpret_cast<const uint4 *>(src + from[e] + i * 8 * Lay::kHD);
+        for (int e = 0; e < kSub; ++e) x[e] = *reinterpret_cast<const uint4 *>(src + from[e] + i * 8 * Lay::kHD);
 #pragma unroll
         for (int e = 0; e < kSub; ++e) {
           const uint32_t c[4] = {x[e].x, x[e].y, x[e].z, x[e].w};

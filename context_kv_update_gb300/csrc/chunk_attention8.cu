@@ -140,19 +140,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dk = ptx::smem_desc(base + Lay::kK, 16, 8 * HD,
                                        HD == 64 ? kSwizzle64B : ptx::kSwizzle128B);
     const uint64_t dv = ptx::smem_desc(base + Lay::kWide, kChunkBytes, 1024, ptx::kSwizzle128B);
-    struct At {
-      uint32_t bar, phase;
-    };
+    using At = typename Cta<Lay>::At;
     int at_k = 0, at_v = 0, batches = 0;  // of K tiles, V tiles, batches of scales
     uint32_t handed0 = 0u, handed1 = 0u, loads = 0u;  // phases of p_full and q_ready
     bool ok = true, pairs = false;
-    auto slot = [&](int first, int at, int n) {
-      return At{cta.bar(first + at % n), static_cast<uint32_t>((at / n) & 1)};
-    };
-    // up to three barriers at the cost of one: each is polled by lanes of its own
-    auto wait = [&](At a, At b, At c) {
-      const At x = lane == 1 ? b : lane == 2 ? c : a;
-      const bool got = __all_sync(0xffffffffu, chunk_wait<true>(x.bar, x.phase, abort_flag));
+    auto slot = [&](int first, int at, int n) { return cta.full(first, at, n); };
+    auto wait = [&](At a, At b, At e) {
+      const bool got = cta.template wait<true>(a, b, e);
       ptx::tc_fence_after();
       return got;
     };
@@ -299,8 +293,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = split ? g : 0; ok && t < n; t += step) {
         const int b = batches + t / kMetaBatch;
         hand_back(t / kMetaBatch);
-        ok = cta.arrived(Lay::kMFull, b, kMetaBatches) &&
-             chunk_wait<false>(cta.bar(Lay::kSFull + g), scores & 1, abort_flag);
+        const typename Cta<Lay>::At s_full = {cta.bar(Lay::kSFull + g), scores & 1};
+        ok = (t % kMetaBatch >= step || cta.arrived(Lay::kMFull, b, kMetaBatches)) &&
+                   chunk_wait<false>(s_full.bar, s_full.phase, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ++scores;

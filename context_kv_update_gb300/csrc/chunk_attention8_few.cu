@@ -154,19 +154,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dk = ptx::desc_kmajor_sw128(base + Lay::kK, 0);
       const uint64_t dv = ptx::smem_desc(base + Lay::kWide, kChunkBytes, 1024, ptx::kSwizzle128B);
       const uint64_t dp = ptx::smem_desc(base + Lay::kP, kChunkBytes, 1024, ptx::kSwizzle128B);
-      struct At {
-        uint32_t bar, phase;
-      };
+      using At = typename Cta<Lay>::At;
       int at_k = 0, at_v = 0, batches = 0;  // of K tiles, V tiles, batches of scales
       uint32_t handed0 = 0u, handed1 = 0u, loads = 0u;  // phases of p_full and q_ready
       bool ok = true;
-      auto slot = [&](int first, int at, int n) {
-        return At{cta.bar(first + at % n), static_cast<uint32_t>((at / n) & 1)};
-      };
-      // up to three barriers at the cost of one: each is polled by lanes of its own
+      auto slot = [&](int first, int at, int n) { return cta.full(first, at, n); };
       auto wait = [&](At a, At b, At c) {
-        const At x = lane == 1 ? b : lane == 2 ? c : a;
-        const bool got = __all_sync(0xffffffffu, chunk_wait<true>(x.bar, x.phase, abort_flag));
+        const bool got = cta.template wait<true>(a, b, c);
         ptx::tc_fence_after();
         return got;
       };
@@ -302,8 +296,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = g; ok && t < n; t += 2) {
         const int b = batches + t / kMetaBatch;
         hand_back(t / kMetaBatch);
-        bool got = cta.arrived(Lay::kMFull, b, kMetaBatches) &&
-                   chunk_wait<false>(cta.bar(Lay::kSFull + g), scores & 1, abort_flag);
+        const typename Cta<Lay>::At s_full = {cta.bar(Lay::kSFull + g), scores & 1};
+        bool got = (t % kMetaBatch >= 2 || cta.arrived(Lay::kMFull, b, kMetaBatches)) &&
+                   chunk_wait<false>(s_full.bar, s_full.phase, abort_flag);
         got = __all_sync(0xffffffffu, got);
         ++scores;
         ptx::tc_fence_after();
@@ -318,16 +313,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto weigh = [&](bool absolute) {
           float sv[kCols];
           tmem_ld<kCols>(tm_s, sv);
+          const float2 kf2 = make_float2(kf, kf);
 #pragma unroll
           for (int r = 0; r < N; r += 4) {
             const float4 f = *reinterpret_cast<const float4 *>(row_f + r);
             float4 nm = make_float4(0.f, 0.f, 0.f, 0.f);
             if (!absolute) nm = *reinterpret_cast<const float4 *>(row_nm + r);
-            const float fs[4] = {f.x, f.y, f.z, f.w}, ns[4] = {nm.x, nm.y, nm.z, nm.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float s = kApart ? sv[r + e] + sv[(kApart ? N : 0) + r + e] : sv[r + e];
-              y[r + e] = fmaf(s, fs[e] * kf, ns[e]);
+            for (int e = 0; e < 4; e += 2) {
+              const int x = r + e, low = kApart ? N + x : x;
+              float2 v = make_float2(sv[x], sv[x + 1]);
+              if (kApart) v = add2(v, make_float2(sv[low], sv[low + 1]));
+              v = fma2(v, mul2(e ? make_float2(f.z, f.w) : make_float2(f.x, f.y), kf2),
+                       e ? make_float2(nm.z, nm.w) : make_float2(nm.x, nm.y));
+              y[x] = v.x;
+              y[x + 1] = v.y;
             }
           }
           if (cut) {
@@ -340,13 +340,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int r = 0; r < N; ++r) y[r] = -INFINITY;
           }
         };
-        bool need = !got || tile.E != E;
-        if (got) {
+        bool need = !got || t < 2 || tile.E != E;
+        if (!need) {
           weigh(false);
           float top = y[0];
 #pragma unroll
           for (int r = 1; r < N; ++r) top = fmaxf(top, y[r]);
-          need = need || top > 8.f + kLift;
+          need = top > 8.f + kLift;
         }
         // (A warp whose wait ran out votes too, and all end together: a barrier has no limit.)
         if (ptx::bar_or(2 + g, 128, need)) {
@@ -375,7 +375,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ptx::bar_sync(2 + g, 128);
 #pragma unroll
-          for (int r = 0; r < N; ++r) l[r] *= row_corr[r];
+          for (int r = 0; r < N; r += 4) {
+            const float4 c = *reinterpret_cast<const float4 *>(row_corr + r);
+            l[r] *= c.x;
+            l[r + 1] *= c.y;
+            l[r + 2] *= c.z;
+            l[r + 3] *= c.w;
+          }
           if (t >= 2) {  // the group's product before this S is complete
             const uint32_t tm_o = tmem + kColOut + 64 * g + lane_off;
 #pragma unroll 1
@@ -390,13 +396,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tmem_wait_st();
           }
           E = tile.E;
-          weigh(false);
+#pragma unroll
+          for (int r = 0; r < N; r += 4) {
+            const float4 nm = *reinterpret_cast<const float4 *>(row_nm + r);
+            const float ns[4] = {nm.x, nm.y, nm.z, nm.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)  // a row that has seen no key sees none here
+              y[r + e] = ns[e] == INFINITY ? -INFINITY : y[r + e] + ns[e];
+          }
         }
         uint32_t pk[N / 2];
 #pragma unroll
-        for (int r = 0; r < N; ++r) {
-          y[r] = ptx::ex2(y[r]);
-          l[r] += y[r];
+        for (int r = 0; r < N; r += 2) {
+          const float2 w = make_float2(ptx::ex2(y[r]), ptx::ex2(y[r + 1])),
+                       sum = add2(make_float2(l[r], l[r + 1]), w);
+          y[r] = w.x;
+          y[r + 1] = w.y;
+          l[r] = sum.x;
+          l[r + 1] = sum.y;
         }
         if (far) {
 #pragma unroll
