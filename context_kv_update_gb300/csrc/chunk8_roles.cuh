@@ -8,7 +8,7 @@
 namespace dflash {
 
 // Work tiles of 2^shift rows for the kernel of few rows (heads of 128).
-constexpr int kLeastFewShift = 4, kMostFewShift = 6;
+constexpr int kLeastFewShift = 4, kMostFewShift = 5;
 cudaError_t launch_attn8_few(int shift, const CUtensorMap &tm, const ChunkParams &p,
                              const Cache8 &cache, dim3 grid, cudaStream_t s);
 
@@ -50,7 +50,7 @@ constexpr uint32_t idesc_of(int M, int N, uint32_t format, bool b_mn_major) {
   return (1u << 4) | (format << 7) | (format << 10) | ((b_mn_major ? 1u : 0u) << 16) |
          ((static_cast<uint32_t>(N) >> 3) << 17) | ((static_cast<uint32_t>(M) >> 4) << 24);
 }
-constexpr uint32_t kSwizzle64B = 4;
+constexpr uint32_t kSwizzle64B = 4, kSwizzle32B = 6;
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
@@ -164,19 +164,19 @@ struct Cta {
     init(Lay::kKFull, Lay::kKs, 1);
     init(Lay::kKEmpty, Lay::kKs, 1);
     init(Lay::kVFull, Lay::kVs, 1);
-    init(Lay::kVEmpty, Lay::kVs, 4);  // the widening warps
-    init(Lay::kWFull, Lay::kWides, 4);
+    init(Lay::kVEmpty, Lay::kVs, Lay::kWideners);  // the widening warps
+    init(Lay::kWFull, Lay::kWides, Lay::kWideners);
     init(Lay::kWEmpty, Lay::kWides, 1);
     init(Lay::kMFull, kMetaBatches, 1);
-    init(Lay::kMEmpty, kMetaBatches, 13);  // softmax, widening and issuing warps
+    init(Lay::kMEmpty, kMetaBatches, 8 + Lay::kWideners + 1);  // softmax, widening, issuing warps
     init(Lay::kSFull, 2, 1);
     init(Lay::kPFull, 2, 4);  // one arrival per warp of the group
     init(Lay::kODone, 2, 1);
-    init(Lay::kQReady, 1, 4);
+    init(Lay::kQReady, 1, Lay::kWideners);
     init(Lay::kQEmpty, 1, 1);
     init(Lay::kDrain, 1, 1);
     init(Lay::kWorkFull, 1, 1);
-    init(Lay::kWorkRead, 1, 15);  // every other warp
+    init(Lay::kWorkRead, 1, 11 + Lay::kWideners);  // every other warp
     init(Lay::kClaim, 1, 1);
   }
 };
@@ -316,15 +316,35 @@ __device__ __forceinline__ void look_up_scales(const Cta<Lay> &c, const ChunkPar
   }
 }
 
-// Loads K's and V's tiles.
+// A place in a ring of N slots and the phase of its next use, for a barrier that a use waits on
+// before (kBefore: the slot is free) or after it (its contents are there).
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t phase;
+  __device__ __forceinline__ explicit Ring(bool before) : phase(before ? 1u : 0u) {}
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// Loads K's and V's tiles.  The warp has a dozen others beside it and a tile's time for two loads:
+// what can be is worked out once for many tiles.
 template <bool kMany, class Lay>
 __device__ __forceinline__ void load_tiles(const Cta<Lay> &c, const ChunkParams &p,
                                            const CUtensorMap &tm) {
   const int lane = c.lane;
-  // A lane per box (page rows).  Boxes without a visible key and pages outside the pool are
-  // not loaded.  The next work is claimed once the loads come to the last kAhead tiles.
+  // A lane a box (page rows).  Boxes without a visible key and pages outside the pool are not
+  // loaded.  The next work is claimed once the loads come to the last kAhead tiles.
   constexpr int kAhead = 3;
-  const int boxes = kKT / p.box_rows;
+  const int shift = 31 - __clz(kKT / p.box_rows), boxes = 1 << shift, per = 32 >> shift;
+  const uint32_t box_bytes = p.box_rows * Lay::kHD;
+  const int kv_rows = p.nkv * p.P;  // from a key's row to its value's
+  Ring<Lay::kKs> ring_k(true);
+  Ring<Lay::kVs> ring_v(true);
   int at_k = 0, at_v = 0;
   bool ok = true;
   for (uint32_t w = 0; w == 0 || kMany; ++w) {
@@ -337,71 +357,76 @@ __device__ __forceinline__ void load_tiles(const Cta<Lay> &c, const ChunkParams 
     const int n = d.n;
     const uint64_t pol =
         d.total <= (1 << Lay::kShift) ? ptx::policy_evict_first() : ptx::policy_evict_normal();
-    auto fetch = [&](int t) {  // page of box `lane` of tile t, -1 where it is not loaded
-      int page = -1;
-      if (lane < boxes && t < n) {
-        const int key0 = (d.t0 + t) * kKT + lane * p.box_rows;
+    // Pages of 32 boxes at once, a lookup ahead of the one in use.  Lane boxes * i + b: the pool's
+    // row where box b of tile t + i begins in K, -1 where it is not loaded.
+    auto look = [&](int t) {
+      int row = -1;
+      t += lane >> shift;
+      if (t < n) {
+        const int key0 = (d.t0 + t) * kKT + (lane & (boxes - 1)) * p.box_rows;
         if (key0 <= d.hi_max && key0 + p.box_rows > d.lo_min) {
-          page = p.tbl[static_cast<int64_t>(d.r) * p.M + key0 / p.P];
-          if (page >= p.NP) page = -1;
+          const int place = key0 / p.P, page = p.tbl[static_cast<int64_t>(d.r) * p.M + place];
+          if (page >= 0 && page < p.NP)
+            row = static_cast<int>(
+                ((static_cast<int64_t>(p.layer) * p.NP + page) * 2 * p.nkv + d.kvh) * p.P + key0 -
+                place * p.P);
         }
       }
-      return page;
+      return row;
     };
-    auto load = [&](int t, int kv, int page) {
+    int rows = look(0), ahead = look(per), behind = -1, base = 0;  // `rows` from tile base on
+    auto box_row = [&](int t) {
+      if (t >= base + per) {  // (a K: V is up to two tiles behind it)
+        behind = rows;
+        rows = ahead;
+        base += per;
+        ahead = look(base + per);
+      }
+      const int from = ((t - base) << shift) + lane;
+      const int row = __shfl_sync(0xffffffffu, t < base ? behind : rows, from & 31);
+      return lane < boxes ? row : -1;
+    };
+    auto load = [&](auto &ring, int empty, int full, uint32_t tiles, int row, bool skip) {
       if (!ok) return;
-      int &at = kv ? at_v : at_k;
-      const int slots = kv ? Lay::kVs : Lay::kKs, slot = at % slots;
-      bool got = true;
-      if (lane == 0) got = c.reuse(kv ? Lay::kVEmpty : Lay::kKEmpty, at, slots);
-      ok = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
+      ok = __all_sync(0xffffffffu,
+                      chunk_wait<false>(c.bar(empty + ring.slot), ring.phase, c.abort_flag));
       if (!ok) return;
-      const bool skip = t == p.skip_tile && kv == 0;
-      const uint32_t full = c.bar((kv ? Lay::kVFull : Lay::kKFull) + slot);
-      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * p.box_rows * Lay::kHD;
-      if (lane == 0 && !skip) ptx::mbar_arrive_expect_tx(full, bytes);
+      const uint32_t bar = c.bar(full + ring.slot);
+      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, row >= 0)) * box_bytes;
+      if (lane == 0 && !skip) ptx::mbar_arrive_expect_tx(bar, bytes);
       __syncwarp();
-      if (lane < boxes && page >= 0 && !skip) {
-        const int key0 = (d.t0 + t) * kKT + lane * p.box_rows;
-        const int64_t row =
-            (((static_cast<int64_t>(p.layer) * p.NP + page) * 2 + kv) * p.nkv + d.kvh) * p.P +
-            key0 % p.P;
-        ptx::tma_load_2d_hint(c.sm0 + (kv ? Lay::kV : Lay::kK) + slot * Lay::kTile +
-                                  lane * p.box_rows * Lay::kHD,
-                              &tm, 0, static_cast<int32_t>(row), full, pol);
-      }
-      ++at;
+      if (row >= 0 && !skip)
+        ptx::tma_load_2d_hint(c.sm0 + tiles + ring.slot * Lay::kTile + lane * box_bytes, &tm, 0, row,
+                              bar, pol);
+      ring.next();
     };
-    // a tile's pages are looked up at least one load ahead of their use
-    if (Lay::kPair && d.nrow > 128) {
-      int cur = fetch(0);
-      for (int t = 0; t < n; ++t) {
-        const int nxt = fetch(t + 1);
-        if (t == max(n - kAhead, 0)) c.have_read();
-        load(t, 0, cur);
-        load(t, 1, cur);
-        cur = nxt;
-      }
-    } else {
-      int pa = fetch(0), pb = fetch(1);
-      load(0, 0, pa);
-      if (n > 1) load(1, 0, pb);
-      for (int t = 0; t < n; ++t) {
-        const int pc = fetch(t + 2);
-        if (t == max(n - kAhead, 0)) c.have_read();
-        load(t, 1, pa);
-        if (t + 2 < n) load(t + 2, 0, pc);
-        pa = pb;
-        pb = pc;
-      }
+    auto load_k = [&](int t) {
+      load(ring_k, Lay::kKEmpty, Lay::kKFull, Lay::kK, box_row(t), t == p.skip_tile);
+      at_k += ok;
+    };
+    auto load_v = [&](int t) {
+      const int row = box_row(t);
+      load(ring_v, Lay::kVEmpty, Lay::kVFull, Lay::kV, row < 0 ? -1 : row + kv_rows, false);
+      at_v += ok;
+    };
+    // two row tiles: K0 V0 K1 V1 ...; one: K0 K1 V0 K2 V1 K3 ... and the last two tiles' V
+    const int lead = Lay::kPair && d.nrow > 128 ? 0 : 2;
+    for (int t = 0; t < min(lead, n); ++t) load_k(t);
+    for (int t = 0; t < n; ++t) {
+      if (t == max(n - kAhead, 0)) c.have_read();
+      if (lead == 0) load_k(t);
+      load_v(t);
+      if (lead && t + lead < n) load_k(t + lead);
     }
   }
   if (*c.abort_flag && lane == 0) {  // wind down: the last copies land before the CTA ends
     volatile int dummy = 0;
     for (int i = max(at_k - Lay::kKs, 0); i < at_k; ++i)
-      chunk_wait<false>(c.bar(Lay::kKFull + i % Lay::kKs), static_cast<uint32_t>((i / Lay::kKs) & 1), &dummy);
+      chunk_wait<false>(c.bar(Lay::kKFull + i % Lay::kKs), static_cast<uint32_t>((i / Lay::kKs) & 1),
+                        &dummy);
     for (int i = max(at_v - Lay::kVs, 0); i < at_v; ++i)
-      chunk_wait<false>(c.bar(Lay::kVFull + i % Lay::kVs), static_cast<uint32_t>((i / Lay::kVs) & 1), &dummy);
+      chunk_wait<false>(c.bar(Lay::kVFull + i % Lay::kVs), static_cast<uint32_t>((i / Lay::kVs) & 1),
+                        &dummy);
   }
 }
 
@@ -446,14 +471,15 @@ __device__ __forceinline__ int split_q(const uint4 (&x)[N / 8], uint32_t (&hi)[N
   return e;
 }
 
-// A work's rows of Q, split: eight lanes a row, the next rows' loads under these, 16 rows of the
-// four warps at once, `rows` in all (those past the work's are zeros).  store(row, u, hi, lo, e)
+// A work's rows of Q, split: eight lanes a row, the next rows' loads under these, four rows a
+// warp at once, `rows` in all (those past the work's are zeros).  store(row, u, hi, lo, e)
 // takes a lane's part u of a row.  `loads` works before this one had their Q here.
 template <class Lay, class Store>
 __device__ __forceinline__ bool split_rows(const Cta<Lay> &c, const ChunkParams &p, const Work &d,
                                            int rows, uint32_t loads, Store store) {
   constexpr int HD = Lay::kHD, kLoads = HD / 64;  // of 8 values
-  const int lane = c.lane, warp = (threadIdx.x >> 5) & 3;
+  constexpr int kStep = 4 * Lay::kWideners;
+  const int lane = c.lane, warp = (threadIdx.x >> 5) - 12;
   const int tok0 = d.row0 / p.G, rem0 = d.row0 - tok0 * p.G, u = lane & 7;
   auto fetch = [&](int row, uint4(&x)[kLoads]) {
 #pragma unroll
@@ -473,9 +499,9 @@ __device__ __forceinline__ bool split_rows(const Cta<Lay> &c, const ChunkParams 
                                                               c.abort_flag)))
     return false;
 #pragma unroll 1
-  for (; row - (lane >> 3) < rows; row += 16) {
+  for (; row - (lane >> 3) < rows; row += kStep) {
     uint4 ahead[kLoads];
-    fetch(row + 16, ahead);
+    fetch(row + kStep, ahead);
     uint32_t hi[2 * kLoads], lo[2 * kLoads];
     const int e = split_q<8 * kLoads>(x, hi, lo);
     if (row < rows) store(row, u, hi, lo, e);
@@ -488,13 +514,13 @@ __device__ __forceinline__ bool split_rows(const Cta<Lay> &c, const ChunkParams 
   return true;
 }
 
-// Widens V's tiles to 16 bits: the calling warp's 32 rows.
+// Widens V's tiles to 16 bits: the calling warp's share of the rows, 32 or 16.
 template <class Lay>
 struct Widener {
-  static constexpr int kSub = Lay::kHD / 64;
+  static constexpr int kSub = Lay::kHD / 64, kRows = 128 / Lay::kWideners;
   uint32_t from[kSub], to[kSub][2];
   int wr, row8[kSub];  // the warp's first row; the lane's of every eight
-  __device__ __forceinline__ Widener(int warp, int lane) : wr(32 * (warp & 3)) {
+  __device__ __forceinline__ Widener(int warp, int lane) : wr(kRows * (warp - 12)) {
     // A lane's 16 codes of every eight rows (heads of 64: once; 128: twice).  Eight lanes read and
     // write 16 bytes each of different banks: 64: of rows r and r + 1; 128: of r and r ^ 5, since
     // a row's chunks arrive at their number xor r, and leave at twice it xor r.
@@ -510,18 +536,18 @@ struct Widener {
   }
   __device__ __forceinline__ void tile(const Work &d, int t, const TileMeta &tile,
                                        const uint8_t *src, uint8_t *dst) const {
-    const uint32_t v0 = tile.v[2 * (wr >> 5)], v1 = tile.v[2 * (wr >> 5) + 1];
+    const uint32_t v0 = tile.v[wr / 16], v1 = tile.v[wr / 16 + kRows / 16 - 1];
     const int kb = (d.t0 + t) * kKT + wr;
     // Rows that no row of the work sees, and those of pages outside the pool, become zeros:
     // a weight of 0 does not silence a NaN.
-    const bool whole = kb >= d.lo_min && kb + 31 <= d.hi_max && (v0 & v1) >> 24;
+    const bool whole = kb >= d.lo_min && kb + kRows - 1 <= d.hi_max && (v0 & v1) >> 24;
     const bool far = tile.far != 0;
     // Short loops: in a long run of instructions that other warps' code has driven out of the
     // cache each takes three cycles or four.
     if (whole && !far) {
       uint32_t f = (v0 & 0xffffu) * 0x10001u;
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kRows / 8; ++i) {
         if (i == 2) f = (v1 & 0xffffu) * 0x10001u;
         uint4 x[kSub];
 #pragma unroll
@@ -542,7 +568,7 @@ struct Widener {
       }
     } else {
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kRows / 8; ++i) {
         const uint32_t v = i < 2 ? v0 : v1, f = (v & 0xffffu) * 0x10001u;
         const float scale = scale8_value(v >> 16 & 255u);
 #pragma unroll

@@ -31,7 +31,7 @@ namespace {
 template <int HD, bool kPairs>
 struct Layout8 : Bars<HD == 64 ? 6 : kPairs ? 3 : 4, HD == 64 ? 4 : kPairs ? 2 : 3, 2> {
   using B = Bars<HD == 64 ? 6 : kPairs ? 3 : 4, HD == 64 ? 4 : kPairs ? 2 : 3, 2>;
-  static constexpr int kHD = HD, kShift = kPairs ? 8 : 7;
+  static constexpr int kHD = HD, kShift = kPairs ? 8 : 7, kWideners = 4;
   static constexpr bool kPair = kPairs;
   static constexpr uint32_t kTile = kKT * HD, kTile16 = 2 * kTile;
   static constexpr uint32_t kK = (kPair ? 2 : 1) * kTile16;
@@ -542,11 +542,8 @@ cudaError_t launch_main(bool pair, const CUtensorMap &tm, const ChunkParams &p,
 // kernel of chunk_attention8_few.cu.
 int tile_shift(const dflash_geom &g, int B, int n_rows) {
   const int64_t rows = static_cast<int64_t>(n_rows) * (g.hq / g.nkv);
-  if (g.head_dim == 128 && rows <= (1LL << kMostFewShift) * B) {
-    int shift = kLeastFewShift;
-    while (rows > (1LL << shift) * B) ++shift;
-    return shift;
-  }
+  if (g.head_dim == 128 && rows <= 64LL * B)
+    return rows <= (1LL << kLeastFewShift) * B ? kLeastFewShift : kMostFewShift;
   return pair_form(g, B, n_rows) ? 8 : 7;
 }
 

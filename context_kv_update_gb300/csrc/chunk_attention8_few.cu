@@ -3,7 +3,7 @@
 //
 // The kernel of chunk_attention8.cu with the products turned round: the 128 keys of a tile are
 // the rows of both results' operands, S^T = K Q^T and O^T = V^T P^T.  The tensor cores then do
-// work for N = 16, 32 or 64 rows instead of 128, K's tile is read from shared memory once for
+// work for N = 16 or 32 rows instead of 128, K's tile is read from shared memory once for
 // both parts of Q, and a softmax thread is a key with N scores: 128 threads share what one warp
 // did for all keys of a tile (64 single tokens over up to 8192 keys: 219 us that way).
 //
@@ -19,18 +19,27 @@
 namespace dflash {
 namespace {
 
+// 20 warps: as in chunk_attention8.cu, but eight that widen V.  640 threads launch with 96
+// registers each: 256 x 128 + 128 x 64 + 256 x 80 = 640 x 96.
+constexpr int kFewThreads = 640;
+// A row's weights carry 2^4 and may exceed its reference by 2^11 more: fp16 holds 2^15, and its
+// smallest step is 2^-28 of the reference's weight.
+constexpr float kFewLift = 4.f, kFewLag = 11.f;
+constexpr int kFewSoftmaxRegs = 128, kFewIssueRegs = 64, kFewWidenRegs = 80;
+static_assert(256 * (kFewSoftmaxRegs + kFewWidenRegs) + 128 * kFewIssueRegs <= kFewThreads * 96, "");
+
 template <int N>
-struct LayoutFew : Bars<N == 64 ? 3 : 4, 3, 2> {
-  using B = Bars<N == 64 ? 3 : 4, 3, 2>;
-  static constexpr int kHD = 128, kShift = N == 16 ? 4 : N == 32 ? 5 : 6;
+struct LayoutFew : Bars<3, 3, 3> {
+  using B = Bars<3, 3, 3>;
+  static constexpr int kHD = 128, kShift = N == 16 ? 4 : 5, kWideners = 8;
   static constexpr bool kPair = false;
   static constexpr uint32_t kTile = kKT * kHD, kTile16 = 2 * kTile;
   static constexpr uint32_t kK = 2 * N * 128;  // Q: N rows of hi, N of lo
   static constexpr uint32_t kV = kK + B::kKs * kTile;
   static constexpr uint32_t kWide = kV + B::kVs * kTile;
-  static constexpr uint32_t kP = kWide + B::kWides * kTile16;  // of each group: 128 keys of 128 bytes
-  static constexpr uint32_t kRowState = kP + 2 * kKT * 128;
-  static constexpr uint32_t kMeta = kRowState + (2 * N + 2 * N * 11 + 2) * 4 / 16 * 16 + 16;
+  static constexpr uint32_t kP = kWide + B::kWides * kTile16;  // of each group: 128 keys of N weights
+  static constexpr uint32_t kRowState = kP + 2 * kKT * 2 * N;
+  static constexpr uint32_t kMeta = kRowState + (2 * N + 2 * N * 11 + 12) * 4;
   static constexpr uint32_t kSortTiles = kMeta + kMetaBatch * kMetaBatches * sizeof(TileMeta);
   static constexpr uint32_t kPlaces = kSortTiles + 4 * kSorted;
   static constexpr uint32_t kWork = kPlaces + kSorted;
@@ -44,9 +53,7 @@ struct LayoutFew : Bars<N == 64 ? 3 : 4, 3, 2> {
 // N columns of this warp's lanes.
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&r)[N]) {
-  if constexpr (N == 64) {
-    ptx::tmem_ld64f_sync(taddr, r);
-  } else if constexpr (N == 32) {
+  if constexpr (N == 32) {
     ptx::tmem_ld32f_sync(taddr, r);
   } else {
     static_assert(N == 16, "");
@@ -68,17 +75,14 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&r)[8]) {
 }
 
 template <int N, bool kMany>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kFewThreads, 1)
     chunk_attn8_few_kernel(const __grid_constant__ CUtensorMap tm,
                            const __grid_constant__ ChunkParams p,
                            const __grid_constant__ Cache8 cache) {
   using Lay = LayoutFew<N>;
   constexpr int HD = 128, kKs = Lay::kKs, kWides = Lay::kWides;
-  // S^T: hi's scores, then lo's, as one product; 64 rows: both into the same columns, since a
-  // thread cannot hold 128 scores beside its sums.
-  constexpr bool kApart = N < 64;
-  constexpr int kCols = kApart ? 2 * N : N;
-  constexpr uint32_t kColOut = 256;  // S of group g at 128 g, O at 256 + 64 g
+  // S^T of group g at 128 g (hi's scores, then lo's, as one product), O^T at 256 + 128 g
+  constexpr uint32_t kColOut = 256;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                             ~static_cast<uintptr_t>(1023));
@@ -113,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (sorted) sort_requests<false>(p, Lay::kShift, sort_tiles, sort_places);
 
   if (warp >= 12) {
-    regs_less<kWidenRegs>();
+    regs_less<kFewWidenRegs>();
     // ------------------------------------------------ Q's split, V's widening
     const Widener<Lay> widener(warp, lane);
     int at = 0, batches = 0;  // V tiles and batches of scales so far
@@ -135,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) ok = widen_tiles(cta, widener, d, at, batches);
     }
   } else if (warp >= 8) {
-    regs_less<kIssueRegs>();
+    regs_less<kFewIssueRegs>();
     if (warp == 8) {
       schedule<kMany>(cta, p, sorted, sort_tiles, sort_places);
     } else if (warp == 9) {
@@ -144,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_tiles<kMany>(cta, p, tm);
     } else {
       // ---------------------------------------------- MMA issuer
-      constexpr uint32_t idesc_qk = idesc_of(128, kCols, 0, false);
+      constexpr uint32_t idesc_qk = idesc_of(128, 2 * N, 0, false);
       constexpr uint32_t idesc_f16 = idesc_of(128, N, 0, true) | 1u << 15,  // V^T: dims contiguous
           idesc_bf16 = idesc_of(128, N, 1, true) | 1u << 15;
       // warp-uniform copies
@@ -153,7 +157,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dq = ptx::desc_kmajor_sw128(base, 0);
       const uint64_t dk = ptx::desc_kmajor_sw128(base + Lay::kK, 0);
       const uint64_t dv = ptx::smem_desc(base + Lay::kWide, kChunkBytes, 1024, ptx::kSwizzle128B);
-      const uint64_t dp = ptx::smem_desc(base + Lay::kP, kChunkBytes, 1024, ptx::kSwizzle128B);
+      // P: keys of 2 N contiguous bytes
+      const uint64_t dp = ptx::smem_desc(base + Lay::kP, kChunkBytes, 16 * N,
+                                         N == 32 ? kSwizzle64B : kSwizzle32B);
       using At = typename Cta<Lay>::At;
       int at_k = 0, at_v = 0, batches = 0;  // of K tiles, V tiles, batches of scales
       uint32_t handed0 = 0u, handed1 = 0u, loads = 0u;  // phases of p_full and q_ready
@@ -167,18 +173,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto qk = [&](int g, int at) {  // S_g^T = K (hi, lo)^T
         const uint64_t a = dk + (((at % kKs) * Lay::kTile) >> 4);
 #pragma unroll
-        for (int ks = 0; ks < (kApart ? 4 : 8); ++ks)
-          mma_e4m3(tm0 + 128 * g, a + ((ks & 3) * 32 >> 4),
-                   dq + (((ks & 3) * 32 + (ks >> 2) * N * 128) >> 4), idesc_qk, ks > 0 ? 1u : 0u);
+        for (int ks = 0; ks < HD / 32; ++ks)
+          mma_e4m3(tm0 + 128 * g, a + (ks * 32 >> 4), dq + (ks * 32 >> 4), idesc_qk,
+                   ks > 0 ? 1u : 0u);
         ptx::mma_commit(cta.bar(Lay::kSFull + g));
         ptx::mma_commit(cta.bar(Lay::kKEmpty + at % kKs));
       };
       auto pv = [&](int g, int at, bool first, uint32_t idesc) {  // O_g^T (+)= V^T P^T
         const uint64_t a = dv + (((at % kWides) * Lay::kTile16) >> 4);
-        const uint64_t b = dp + ((g * kKT * 128) >> 4);
+        const uint64_t b = dp + ((g * kKT * 2 * N) >> 4);
 #pragma unroll
         for (int ks = 0; ks < kKT / 16; ++ks)
-          ptx::mma_bf16(tm0 + kColOut + 64 * g, a + ((ks * 2048) >> 4), b + ((ks * 2048) >> 4),
+          ptx::mma_bf16(tm0 + kColOut + 128 * g, a + ((ks * 2048) >> 4), b + ((ks * 32 * N) >> 4),
                         idesc, (!first || ks > 0) ? 1u : 0u);
         ptx::mma_commit(cta.bar(Lay::kWEmpty + at % kWides));
       };
@@ -233,18 +239,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    regs_more<kSoftmaxRegs>();
+    regs_more<kFewSoftmaxRegs>();
     // ------------------------------------------------ softmax groups: a key a thread
     const int g = warp >> 2, w4 = warp & 3;
     const int tid = threadIdx.x & 127;  // TMEM lane = key of the tile, at the end a dim
     const uint32_t lane_off = static_cast<uint32_t>(w4 * 32) << 16;
     const uint32_t tm_s = tmem + 128 * g + lane_off;
-    // a group's rows: lo, hi, factor, reference (kLift - it), scaling; warps' maxima or sums [4]
+    // a group's rows: lo, hi, factor, kFewLift - reference, scaling; the warps' maxima [4]; reference,
+    // what was added to the scores; of both groups, units of the accumulators; rows that moved, and
+    // that have no reference
     float *rows = q_scale + 2 * N + g * 11 * N, *other = q_scale + 2 * N + (g ^ 1) * 11 * N;
     int *row_lo = reinterpret_cast<int *>(rows), *row_hi = row_lo + N;
     float *row_f = rows + 2 * N, *row_nm = rows + 3 * N, *row_corr = rows + 4 * N,
-          *part = rows + 5 * N, *row_m = rows + 9 * N, *row_l = rows + 10 * N;
-    float *units = q_scale + 2 * N + 22 * N;  // of the groups' accumulators
+          *part = rows + 5 * N, *row_m = rows + 9 * N, *row_delta = rows + 10 * N;
+    float *units = q_scale + 2 * N + 22 * N;
+    uint32_t *marks = reinterpret_cast<uint32_t *>(units) + 4 + 4 * g;  // of the groups' accumulators
     int batches = 0;
     uint32_t loads = 0u, scores = 0u, outs0 = 0u, outs1 = 0u;  // of q_ready, s_full, o_done
     bool ok = true;
@@ -284,10 +293,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ptx::bar_sync(2 + g, 128);
 
-      float l[N];
+      float l[N];  // this key's share of the rows' sums
 #pragma unroll
       for (int r = 0; r < N; ++r) l[r] = 0.f;
       int E = 0, left = 0;
+      bool fresh = true;  // some row has no reference yet
       auto hand_back = [&](int to_batch) {
         __syncwarp();
         for (; left < to_batch; ++left)
@@ -311,8 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         float y[N];
         // Scores, in powers of two: relative to the rows' references, or as they are.
         auto weigh = [&](bool absolute) {
-          float sv[kCols];
-          tmem_ld<kCols>(tm_s, sv);
+          float low[N];
+          tmem_ld<N>(tm_s, y);
+          tmem_ld<N>(tm_s + N, low);
           const float2 kf2 = make_float2(kf, kf);
 #pragma unroll
           for (int r = 0; r < N; r += 4) {
@@ -321,10 +332,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!absolute) nm = *reinterpret_cast<const float4 *>(row_nm + r);
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
-              const int x = r + e, low = kApart ? N + x : x;
-              float2 v = make_float2(sv[x], sv[x + 1]);
-              if (kApart) v = add2(v, make_float2(sv[low], sv[low + 1]));
-              v = fma2(v, mul2(e ? make_float2(f.z, f.w) : make_float2(f.x, f.y), kf2),
+              const int x = r + e;
+              const float2 v =
+                  fma2(add2(make_float2(y[x], y[x + 1]), make_float2(low[x], low[x + 1])),
+                       mul2(e ? make_float2(f.z, f.w) : make_float2(f.x, f.y), kf2),
                        e ? make_float2(nm.z, nm.w) : make_float2(nm.x, nm.y));
               y[x] = v.x;
               y[x + 1] = v.y;
@@ -340,13 +351,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int r = 0; r < N; ++r) y[r] = -INFINITY;
           }
         };
-        bool need = !got || t < 2 || tile.E != E;
-        if (!need) {
+        bool need = !got || fresh || tile.E != E;
+        if (got && !fresh) {
           weigh(false);
           float top = y[0];
 #pragma unroll
           for (int r = 1; r < N; ++r) top = fmaxf(top, y[r]);
-          need = top > 8.f + kLift;
+          need = need || top > kFewLag + kFewLift;
         }
         // (A warp whose wait ran out votes too, and all end together: a barrier has no limit.)
         if (ptx::bar_or(2 + g, 128, need)) {
@@ -354,64 +365,88 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          weigh(true);
+          // Rows whose scores exceed their reference (in some lane; all in a tile where a row
+          // has none yet), the warp's maxima of them, floats in the order of integers.
+          if (fresh) weigh(true);
+          float most = -INFINITY;
 #pragma unroll
-          for (int r = 0; r < N; ++r) {  // the warp's maximum, floats in the order of integers
-            int i = __float_as_int(y[r]);
-            i = __reduce_max_sync(0xffffffffu, i ^ (i >> 31 & 0x7fffffff));
-            if (lane == (r & 31)) part[w4 * N + r] = __int_as_float(i ^ (i >> 31 & 0x7fffffff));
+          for (int r = 0; r < N; ++r) {
+            if (fresh || __any_sync(0xffffffffu, y[r] > kFewLag + kFewLift)) {
+              int i = __float_as_int(y[r]);
+              i = __reduce_max_sync(0xffffffffu, i ^ (i >> 31 & 0x7fffffff));
+              if (lane == r) most = __int_as_float(i ^ (i >> 31 & 0x7fffffff));
+            }
           }
+          if (lane < N) part[w4 * N + lane] = most;
           ptx::bar_sync(2 + g, 128);
           const float grown = ptx::ex2(static_cast<float>(E - tile.E));
-          if (tid < N) {
-            const float top = fmaxf(fmaxf(part[tid], part[N + tid]),
-                                    fmaxf(part[2 * N + tid], part[3 * N + tid]));
-            const float m = row_m[tid];
-            float now = m;
-            if (m == -INFINITY || top > m + 8.f) now = fmaxf(m, top);
-            row_corr[tid] = m == -INFINITY ? 1.f : ptx::ex2(m - now);
-            row_m[tid] = now;
-            if (tid < nrow) row_nm[tid] = now == -INFINITY ? INFINITY : kLift - now;
+          if (w4 == 0) {  // a thread a row
+            const bool row = tid < N;
+            float m = 0.f, now = 0.f;
+            if (row) {
+              const float top = fmaxf(fmaxf(part[tid], part[N + tid]),
+                                      fmaxf(part[2 * N + tid], part[3 * N + tid]));
+              const float before = row_nm[tid], x = fresh ? top : top - before;
+              m = now = row_m[tid];
+              if (m == -INFINITY || x > m + kFewLag) now = fmaxf(m, x);
+              const float nm = tid >= nrow ? 0.f : now == -INFINITY ? INFINITY : kFewLift - now;
+              row_corr[tid] = m == -INFINITY ? 1.f : ptx::ex2(m - now);
+              row_delta[tid] = fresh ? nm : nm == before ? 0.f : nm - before;
+              row_m[tid] = now;
+              row_nm[tid] = nm;
+            }
+            const uint32_t moved = __ballot_sync(0xffffffffu, row && m != -INFINITY && now != m),
+                           none = __ballot_sync(0xffffffffu, row && now == -INFINITY);
+            if (lane == 0) {
+              marks[0] = moved;
+              marks[1] = none;
+            }
           }
           ptx::bar_sync(2 + g, 128);
 #pragma unroll
           for (int r = 0; r < N; r += 4) {
-            const float4 c = *reinterpret_cast<const float4 *>(row_corr + r);
-            l[r] *= c.x;
-            l[r + 1] *= c.y;
-            l[r + 2] *= c.z;
-            l[r + 3] *= c.w;
+            const float4 f = *reinterpret_cast<const float4 *>(row_corr + r);
+            l[r] *= f.x;
+            l[r + 1] *= f.y;
+            l[r + 2] *= f.z;
+            l[r + 3] *= f.w;
           }
           if (t >= 2) {  // the group's product before this S is complete
-            const uint32_t tm_o = tmem + kColOut + 64 * g + lane_off;
+            const uint32_t tm_o = tmem + kColOut + 128 * g + lane_off;
 #pragma unroll 1
             for (int c = 0; c < N; c += 16) {
+              if (!((marks[0] >> c) & 0xffffu) && tile.E == E) continue;
               uint32_t ov[16];
               ptx::tmem_ld16_sync(tm_o + c, ov);
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                ov[e] = __float_as_uint(__uint_as_float(ov[e]) * (row_corr[c + e] * grown));
+              for (int e = 0; e < 16; e += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(row_corr + c + e);
+                const float fs[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  ov[e + i] = __float_as_uint(__uint_as_float(ov[e + i]) * (fs[i] * grown));
+              }
               ptx::tmem_st16(tm_o + c, ov);
             }
             ptx::tmem_wait_st();
           }
           E = tile.E;
+          fresh = marks[1] != 0;
 #pragma unroll
           for (int r = 0; r < N; r += 4) {
-            const float4 nm = *reinterpret_cast<const float4 *>(row_nm + r);
-            const float ns[4] = {nm.x, nm.y, nm.z, nm.w};
+            const float4 dl = *reinterpret_cast<const float4 *>(row_delta + r);
+            const float ds[4] = {dl.x, dl.y, dl.z, dl.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)  // a row that has seen no key sees none here
-              y[r + e] = ns[e] == INFINITY ? -INFINITY : y[r + e] + ns[e];
+              y[r + e] = ds[e] == INFINITY ? -INFINITY : y[r + e] + ds[e];
           }
         }
         uint32_t pk[N / 2];
 #pragma unroll
         for (int r = 0; r < N; r += 2) {
-          const float2 w = make_float2(ptx::ex2(y[r]), ptx::ex2(y[r + 1])),
-                       sum = add2(make_float2(l[r], l[r + 1]), w);
-          y[r] = w.x;
-          y[r + 1] = w.y;
+          y[r] = ptx::ex2(y[r]);
+          y[r + 1] = ptx::ex2(y[r + 1]);
+          const float2 sum = add2(make_float2(l[r], l[r + 1]), make_float2(y[r], y[r + 1]));
           l[r] = sum.x;
           l[r + 1] = sum.y;
         }
@@ -422,10 +457,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int r = 0; r < N / 2; ++r) pk[r] = pack_f16x2(y[2 * r], y[2 * r + 1]);
         }
-        uint8_t *dst = sm + Lay::kP + g * kKT * 128 + tid * 128;
+        uint8_t *dst = sm + Lay::kP + (g * kKT + tid) * 2 * N;
+        const int swap = N == 32 ? tid >> 1 & 3 : tid >> 2 & 1;
 #pragma unroll
         for (int u = 0; u < N / 8; ++u)
-          *reinterpret_cast<uint4 *>(dst + ((u ^ (tid & 7)) << 4)) =
+          *reinterpret_cast<uint4 *>(dst + ((u ^ swap) << 4)) =
               make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
@@ -459,15 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
         }
       }
-      if constexpr (N == 16) {
-        if (!(lane & 1)) part[w4 * N + (lane >> 1)] = l[0];
-      } else {
-#pragma unroll
-        for (int r = 0; r < N / 32; ++r) part[w4 * N + lane * (N / 32) + r] = l[r];
-      }
-      ptx::bar_sync(2 + g, 128);
-      if (tid < N)
-        row_l[tid] = (part[tid] + part[N + tid]) + (part[2 * N + tid] + part[3 * N + tid]);
+      if (N == 32 || !(lane & 1)) part[w4 * N + (N == 32 ? lane : lane >> 1)] = l[0];
       if (tid == 0) units[g] = exp2_int(min(max(E, -149), 127));
       const bool broken = ptx::bar_or(1, 256, !ok);
       ok = ok && !broken;
@@ -477,10 +505,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (g == 0 && tid < N) {
         const float m0 = broken ? -INFINITY : row_m[tid], m1 = broken ? -INFINITY : other[9 * N + tid];
         const bool any = tid < nrow && fmaxf(m0, m1) != -INFINITY;
-        const float m = fmaxf(m0, m1) - kLift;  // weights are relative to this
-        const float w0 = m0 == -INFINITY ? 0.f : ptx::ex2(m0 - kLift - m),
-                    w1 = m1 == -INFINITY ? 0.f : ptx::ex2(m1 - kLift - m);
-        const float sum = row_l[tid] * w0 + other[10 * N + tid] * w1;
+        const float m = fmaxf(m0, m1) - kFewLift;  // weights are relative to this
+        const float w0 = m0 == -INFINITY ? 0.f : ptx::ex2(m0 - kFewLift - m),
+                    w1 = m1 == -INFINITY ? 0.f : ptx::ex2(m1 - kFewLift - m);
+        const float *p1 = other + 5 * N;
+        const float sum0 = (part[tid] + part[N + tid]) + (part[2 * N + tid] + part[3 * N + tid]),
+                    sum1 = (p1[tid] + p1[N + tid]) + (p1[2 * N + tid] + p1[3 * N + tid]);
+        const float sum = sum0 * w0 + sum1 * w1;
         const int flat = row0 + tid, tok = flat / p.G, h = d.kvh * p.G + flat - tok * p.G;
         float gain = 1.f;
         if (p.S == 1) {
@@ -519,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok && had1) {
           float v[8];
-          tmem_ld8(tmem + kColOut + 64 + lane_off + c, v);
+          tmem_ld8(tmem + kColOut + 128 + lane_off + c, v);
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[e] += f1[c + e] != 0.f ? v[e] * f1[c + e] : 0.f;
         }
@@ -556,7 +587,7 @@ cudaError_t launch_form(const CUtensorMap &tm, const ChunkParams &p, const Cache
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kFewThreads);
   cfg.dynamicSmemBytes = LayoutFew<N>::kBytes;
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -578,9 +609,8 @@ cudaError_t launch_rows(const CUtensorMap &tm, const ChunkParams &p, const Cache
 
 cudaError_t launch_attn8_few(int shift, const CUtensorMap &tm, const ChunkParams &p,
                              const Cache8 &cache, dim3 grid, cudaStream_t s) {
-  return shift == 4   ? launch_rows<16>(tm, p, cache, grid, s)
-         : shift == 5 ? launch_rows<32>(tm, p, cache, grid, s)
-                      : launch_rows<64>(tm, p, cache, grid, s);
+  return shift == 4 ? launch_rows<16>(tm, p, cache, grid, s)
+                    : launch_rows<32>(tm, p, cache, grid, s);
 }
 
 }  // namespace dflash
