@@ -91,13 +91,14 @@ __device__ __forceinline__ void regs_less() {
 
 // Barriers, by their place: rings of K's tiles, of V's, of V's in 16 bits, of scales (full, empty),
 // then the softmax groups', Q's, the works'.
-template <int kK, int kV, int kW>
+template <int kK, int kV, int kW, int kS>
 struct Bars {
-  static constexpr int kKs = kK, kVs = kV, kWides = kW;
+  static constexpr int kKs = kK, kVs = kV, kWides = kW, kScores = kS;
   static constexpr int kKFull = 0, kKEmpty = kKFull + kKs, kVFull = kKEmpty + kKs,
                        kVEmpty = kVFull + kVs, kWFull = kVEmpty + kVs, kWEmpty = kWFull + kWides,
                        kMFull = kWEmpty + kWides, kMEmpty = kMFull + kMetaBatches,
-                       kSFull = kMEmpty + kMetaBatches, kPFull = kSFull + 2, kODone = kPFull + 2,
+                       kSFull = kMEmpty + kMetaBatches, kPFull = kSFull + kScores,
+                       kPDone = kPFull + 2, kODone = kPDone + 2,
                        kQReady = kODone + 2, kQEmpty = kQReady + 1, kDrain = kQEmpty + 1,
                        kWorkFull = kDrain + 1, kWorkRead = kWorkFull + 1, kClaim = kWorkRead + 1,
                        kBarCount = kClaim + 1;
@@ -169,8 +170,9 @@ struct Cta {
     init(Lay::kWEmpty, Lay::kWides, 1);
     init(Lay::kMFull, kMetaBatches, 1);
     init(Lay::kMEmpty, kMetaBatches, 8 + Lay::kWideners + 1);  // softmax, widening, issuing warps
-    init(Lay::kSFull, 2, 1);
+    init(Lay::kSFull, Lay::kScores, 1);
     init(Lay::kPFull, 2, 4);  // one arrival per warp of the group
+    init(Lay::kPDone, 2, 1);
     init(Lay::kODone, 2, 1);
     init(Lay::kQReady, 1, Lay::kWideners);
     init(Lay::kQEmpty, 1, 1);
@@ -376,7 +378,7 @@ __device__ __forceinline__ void load_tiles(const Cta<Lay> &c, const ChunkParams 
     };
     int rows = look(0), ahead = look(per), behind = -1, base = 0;  // `rows` from tile base on
     auto box_row = [&](int t) {
-      if (t >= base + per) {  // (a K: V is up to two tiles behind it)
+      if (t >= base + per) {  // (a K: V is up to four tiles behind it, as many as `per` is at least)
         behind = rows;
         rows = ahead;
         base += per;
@@ -409,8 +411,8 @@ __device__ __forceinline__ void load_tiles(const Cta<Lay> &c, const ChunkParams 
       load(ring_v, Lay::kVEmpty, Lay::kVFull, Lay::kV, row < 0 ? -1 : row + kv_rows, false);
       at_v += ok;
     };
-    // two row tiles: K0 V0 K1 V1 ...; one: K0 K1 V0 K2 V1 K3 ... and the last two tiles' V
-    const int lead = Lay::kPair && d.nrow > 128 ? 0 : 2;
+    // two row tiles: K0 V0 K1 V1 ...; one: K0 K1 V0 K2 V1 K3 ... and the last tiles' V
+    const int lead = Lay::kPair && d.nrow > 128 ? 0 : Lay::kScores;
     for (int t = 0; t < min(lead, n); ++t) load_k(t);
     for (int t = 0; t < n; ++t) {
       if (t == max(n - kAhead, 0)) c.have_read();

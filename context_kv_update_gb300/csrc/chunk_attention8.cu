@@ -29,8 +29,8 @@ namespace {
 // Shared memory: Q tiles; rings of K's tiles, of V's, and of V's in 16 bits; factors of Q's rows;
 // scales; barriers; the work in hand.
 template <int HD, bool kPairs>
-struct Layout8 : Bars<HD == 64 ? 6 : kPairs ? 3 : 4, HD == 64 ? 4 : kPairs ? 2 : 3, 2> {
-  using B = Bars<HD == 64 ? 6 : kPairs ? 3 : 4, HD == 64 ? 4 : kPairs ? 2 : 3, 2>;
+struct Layout8 : Bars<HD == 64 ? 6 : kPairs ? 3 : 4, HD == 64 ? 4 : kPairs ? 2 : 3, 2, 2> {
+  using B = Bars<HD == 64 ? 6 : kPairs ? 3 : 4, HD == 64 ? 4 : kPairs ? 2 : 3, 2, 2>;
   static constexpr int kHD = HD, kShift = kPairs ? 8 : 7, kWideners = 4;
   static constexpr bool kPair = kPairs;
   static constexpr uint32_t kTile = kKT * HD, kTile16 = 2 * kTile;

@@ -29,8 +29,8 @@ constexpr int kFewSoftmaxRegs = 128, kFewIssueRegs = 64, kFewWidenRegs = 80;
 static_assert(256 * (kFewSoftmaxRegs + kFewWidenRegs) + 128 * kFewIssueRegs <= kFewThreads * 96, "");
 
 template <int N>
-struct LayoutFew : Bars<3, 3, 3> {
-  using B = Bars<3, 3, 3>;
+struct LayoutFew : Bars<3, 3, 3, 4> {
+  using B = Bars<3, 3, 3, 4>;
   static constexpr int kHD = 128, kShift = N == 16 ? 4 : 5, kWideners = 8;
   static constexpr bool kPair = false;
   static constexpr uint32_t kTile = kKT * kHD, kTile16 = 2 * kTile;
@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                            const __grid_constant__ Cache8 cache) {
   using Lay = LayoutFew<N>;
   constexpr int HD = 128, kKs = Lay::kKs, kWides = Lay::kWides;
-  // S^T of group g at 128 g (hi's scores, then lo's, as one product), O^T at 256 + 128 g
+  // S^T of tile t at 64 (t % 4) (hi's scores, then lo's, as one product), O^T of group g at
+  // 256 + 128 g
   constexpr uint32_t kColOut = 256;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -170,13 +171,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         ptx::tc_fence_after();
         return got;
       };
-      auto qk = [&](int g, int at) {  // S_g^T = K (hi, lo)^T
+      auto qk = [&](int t, int at) {  // S^T = K (hi, lo)^T, of the work's tile t
         const uint64_t a = dk + (((at % kKs) * Lay::kTile) >> 4);
 #pragma unroll
         for (int ks = 0; ks < HD / 32; ++ks)
-          mma_e4m3(tm0 + 128 * g, a + (ks * 32 >> 4), dq + (ks * 32 >> 4), idesc_qk,
+          mma_e4m3(tm0 + 64 * (t & 3), a + (ks * 32 >> 4), dq + (ks * 32 >> 4), idesc_qk,
                    ks > 0 ? 1u : 0u);
-        ptx::mma_commit(cta.bar(Lay::kSFull + g));
+        ptx::mma_commit(cta.bar(Lay::kSFull + (t & 3)));
         ptx::mma_commit(cta.bar(Lay::kKEmpty + at % kKs));
       };
       auto pv = [&](int g, int at, bool first, uint32_t idesc) {  // O_g^T (+)= V^T P^T
@@ -187,6 +188,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           ptx::mma_bf16(tm0 + kColOut + 128 * g, a + ((ks * 2048) >> 4), b + ((ks * 32 * N) >> 4),
                         idesc, (!first || ks > 0) ? 1u : 0u);
         ptx::mma_commit(cta.bar(Lay::kWEmpty + at % kWides));
+        ptx::mma_commit(cta.bar(Lay::kPDone + g));
       };
       for (uint32_t w = 0; w == 0 || kMany; ++w) {
         const Work d = cta.next_work(w);
@@ -194,21 +196,25 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         if (d.nrow == 0) break;
         const int tiles = __shfl_sync(0xffffffffu, d.n, 0);
         if (!ok || tiles == 0) continue;
-        ok = wait(At{cta.bar(Lay::kQReady), loads & 1}, slot(Lay::kKFull, at_k, kKs),
-                  slot(Lay::kKFull, tiles > 1 ? at_k + 1 : at_k, kKs));
+        // Scores run four tiles ahead of the weights.
+        ok = wait(At{cta.bar(Lay::kQReady), loads & 1}, At{cta.bar(Lay::kQReady), loads & 1},
+                  At{cta.bar(Lay::kQReady), loads & 1});
         ++loads;
-        if (ok && elect_one()) {
-          qk(0, at_k);
-          if (tiles > 1) qk(1, at_k + 1);
-          if (tiles <= 2) ptx::mma_commit(cta.bar(Lay::kQEmpty));
+        for (int t = 0; ok && t < min(tiles, 4); ++t) {
+          const At k = slot(Lay::kKFull, at_k + t, kKs);
+          ok = wait(k, k, k);
+          if (ok && elect_one()) {
+            qk(t, at_k + t);
+            if (t == tiles - 1) ptx::mma_commit(cta.bar(Lay::kQEmpty));
+          }
+          __syncwarp();
         }
-        __syncwarp();
         for (int t = 0; ok && t < tiles; ++t) {
-          const bool more = t + 2 < tiles;
+          const bool more = t + 4 < tiles;
           const int b = batches + t / kMetaBatch, g = t & 1;
           const At v = slot(Lay::kWFull, at_v + t, kWides);
           ok = wait(At{cta.bar(Lay::kPFull + g), (g ? handed1 : handed0) & 1}, v,
-                    more ? slot(Lay::kKFull, at_k + t + 2, kKs) : v);
+                    more ? slot(Lay::kKFull, at_k + t + 4, kKs) : v);
           if (!ok) break;
           if (g) ++handed1; else ++handed0;
           // (the widening warps and the group that handed P over have seen the tile's scales)
@@ -217,11 +223,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           if (elect_one()) {
             pv(g, at_v + t, t < 2, idesc);
             if (more) {
-              qk(g, at_k + t + 2);
-              if (t + 2 == tiles - 1) ptx::mma_commit(cta.bar(Lay::kQEmpty));
-            } else {
-              ptx::mma_commit(cta.bar(Lay::kODone + g));
+              qk(t + 4, at_k + t + 4);
+              if (t + 4 == tiles - 1) ptx::mma_commit(cta.bar(Lay::kQEmpty));
             }
+            if (t + 2 >= tiles) ptx::mma_commit(cta.bar(Lay::kODone + g));
           }
           __syncwarp();
           if ((t % kMetaBatch == kMetaBatch - 1 || t == tiles - 1) && lane == 0)
@@ -244,7 +249,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const int g = warp >> 2, w4 = warp & 3;
     const int tid = threadIdx.x & 127;  // TMEM lane = key of the tile, at the end a dim
     const uint32_t lane_off = static_cast<uint32_t>(w4 * 32) << 16;
-    const uint32_t tm_s = tmem + 128 * g + lane_off;
     // a group's rows: lo, hi, factor, kFewLift - reference, scaling; the warps' maxima [4]; reference,
     // what was added to the scores; of both groups, units of the accumulators; rows that moved, and
     // that have no reference
@@ -255,7 +259,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     float *units = q_scale + 2 * N + 22 * N;
     uint32_t *marks = reinterpret_cast<uint32_t *>(units) + 4 + 4 * g;  // of the groups' accumulators
     int batches = 0;
-    uint32_t loads = 0u, scores = 0u, outs0 = 0u, outs1 = 0u;  // of q_ready, s_full, o_done
+    uint32_t loads = 0u, outs0 = 0u, outs1 = 0u, products = 0u;  // of q_ready, o_done, p_done
+    uint32_t scores = 0u;  // bit b: the phase of S buffer b
     bool ok = true;
     for (uint32_t wk = 0; wk == 0 || kMany; ++wk) {
       const volatile Work &d = cta.shared_work[wk & 1];
@@ -298,6 +303,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       for (int r = 0; r < N; ++r) l[r] = 0.f;
       int E = 0, left = 0;
       bool fresh = true;  // some row has no reference yet
+      bool lost = false;  // a wait ran out: the group ends together with the next tile's vote
+      // The group's product before, which read P and wrote O.
+      auto product_done = [&] {
+        return products == 0 ||
+               __all_sync(0xffffffffu, chunk_wait<false>(cta.bar(Lay::kPDone + g),
+                                                         (products - 1) & 1, abort_flag));
+      };
       auto hand_back = [&](int to_batch) {
         __syncwarp();
         for (; left < to_batch; ++left)
@@ -306,11 +318,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       for (int t = g; ok && t < n; t += 2) {
         const int b = batches + t / kMetaBatch;
         hand_back(t / kMetaBatch);
-        const typename Cta<Lay>::At s_full = {cta.bar(Lay::kSFull + g), scores & 1};
+        const int buffer = t & 3;
+        const uint32_t tm_s = tmem + 64 * buffer + lane_off;
+        const typename Cta<Lay>::At s_full = {cta.bar(Lay::kSFull + buffer), scores >> buffer & 1};
         bool got = (t % kMetaBatch >= 2 || cta.arrived(Lay::kMFull, b, kMetaBatches)) &&
                    chunk_wait<false>(s_full.bar, s_full.phase, abort_flag);
-        got = __all_sync(0xffffffffu, got);
-        ++scores;
+        got = __all_sync(0xffffffffu, got && !lost);
+        scores ^= 1u << buffer;
         ptx::tc_fence_after();
         const TileMeta &tile = cta.scales(b, t);
         const int kb = (t0 + t) * kKT, key = kb + tid;
@@ -411,7 +425,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             l[r + 2] *= f.z;
             l[r + 3] *= f.w;
           }
-          if (t >= 2) {  // the group's product before this S is complete
+          if (t >= 2) {
+            lost |= !product_done();
             const uint32_t tm_o = tmem + kColOut + 128 * g + lane_off;
 #pragma unroll 1
             for (int c = 0; c < N; c += 16) {
@@ -457,6 +472,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
           for (int r = 0; r < N / 2; ++r) pk[r] = pack_f16x2(y[2 * r], y[2 * r + 1]);
         }
+        if (t >= 2) lost |= !product_done();
+        ++products;
         uint8_t *dst = sm + Lay::kP + (g * kKT + tid) * 2 * N;
         const int swap = N == 32 ? tid >> 1 & 3 : tid >> 2 & 1;
 #pragma unroll
@@ -466,8 +483,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(cta.bar(Lay::kPFull + g));
+        if (lane == 0 && !lost) ptx::mbar_arrive(cta.bar(Lay::kPFull + g));
       }
+      ok = ok && !lost;
       const int all = (n + kMetaBatch - 1) / kMetaBatch;
       hand_back(all);
       batches += all;
