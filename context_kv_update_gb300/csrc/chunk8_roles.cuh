@@ -183,14 +183,99 @@ struct Cta {
   }
 };
 
-// Finds the CTA's works: its own block's, then those of blocks that have not started.
+// Scales of a work's key tiles: false where a wait ran out.
+template <class Lay>
+__device__ __forceinline__ bool look_up_scales(const Cta<Lay> &c, const ChunkParams &p,
+                                               const Cache8 &cache, const Work &d, int &batches) {
+  const int lane = c.lane;
+  // Lane 8 i + g: 16 keys g of tile i of four.  Pages are looked up two batches ahead, scales
+  // one.
+  const int mine = lane >> 3, g16 = 16 * (lane & 7);
+  const int shift = 31 - __clz(cache.block), blocks = cache.P >> shift;
+  bool ok = true;
+  auto key_of = [&](int t) { return (d.t0 + t + mine) * kKT + g16; };
+  auto look = [&](int t) {  // the page, -1 where it is none of the pool, -2 where no key is seen
+    const int key = key_of(t);
+    if (t + mine >= d.n || key > d.hi_max || key + 15 < d.lo_min) return -2;
+    const int page = p.tbl[static_cast<int64_t>(d.r) * p.M + key / cache.P];
+    return page >= 0 && page < cache.NP ? page : -1;
+  };
+  auto fetch = [&](int t, int page) {
+    if (page < 0) return 0u;
+    const uint8_t *k = cache.scales + cache.head(page, 0, d.kvh) * blocks +
+                       (key_of(t) % cache.P >> shift);
+    return static_cast<uint32_t>(k[0]) |
+           static_cast<uint32_t>(k[static_cast<int64_t>(cache.nkv) * blocks]) << 8;
+  };
+  constexpr int kNone = 1000;
+  int E = -kNone;
+  bool far = false, any_bad = false;
+  int page = look(0), page1 = look(kMetaBatch);
+  uint32_t bytes = fetch(0, page);
+  for (int t = 0; ok && t < d.n; t += kMetaBatch) {
+    const uint32_t bytes1 = fetch(t + kMetaBatch, page1);
+    const int page2 = look(t + 2 * kMetaBatch);
+    ok = __all_sync(0xffffffffu, c.reuse(Lay::kMEmpty, batches, kMetaBatches));
+    if (!ok) break;
+    const uint32_t kb = bytes & 255u, vb = bytes >> 8;
+    const bool counts = page >= 0 && vb != 255u;
+    int top = counts ? static_cast<int>(vb) - 127 : -kNone,
+        low = counts ? static_cast<int>(vb) - 127 : kNone;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      low = min(low, __shfl_xor_sync(0xffffffffu, low, o));
+    }
+    int my_E = 0, my_far = 0;
+#pragma unroll
+    for (int i = 0; i < kMetaBatch; ++i) {
+      const int mx = __shfl_sync(0xffffffffu, top, 8 * i),
+                mn = __shfl_sync(0xffffffffu, low, 8 * i);
+      // (a little more than it must: the accumulators are scaled whenever it grows)
+      const int grown = mx > E ? min(mx + 2, 127) : E;
+      far = far || (mn != kNone && mn < grown - 14);
+      if (!far) E = grown;
+      if (i == mine) {
+        my_E = far || E == -kNone ? 0 : E;
+        my_far = far;
+      }
+    }
+    const uint32_t bad = __ballot_sync(0xffffffffu, page == -1);
+    any_bad |= bad != 0;
+    TileMeta &m = c.meta[batches % kMetaBatches * kMetaBatch + mine];
+    m.k[lane & 7] = page >= 0 ? scale8_value(kb) : 1.f;
+    const uint32_t factor =
+        vb == 255u ? 0x7fffu : static_cast<uint32_t>(15 + static_cast<int>(vb) - 127 - my_E) << 10;
+    m.v[lane & 7] = page >= 0 ? (factor & 0xffffu) | vb << 16 | 1u << 24 : 0u;
+    if ((lane & 7) == 0) {
+      m.E = my_E;
+      m.far = my_far;
+      m.bad = static_cast<int>(bad >> (8 * mine) & 255u);
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(c.bar(Lay::kMFull + batches % kMetaBatches));
+    ++batches;
+    page = page1;
+    page1 = page2;
+    bytes = bytes1;
+  }
+  if (any_bad && lane == 0) raise_status(p.st, DFLASH_DEV_BAD_PAGE);
+  return ok;
+}
+
+// Finds the CTA's works (its own block's, then those of blocks that have not started), and looks
+// up their scales: done with one's, while its last tiles are worked on, the warp is free for the
+// next.
 template <bool kMany, class Lay>
-__device__ __forceinline__ void schedule(const Cta<Lay> &c, const ChunkParams &p, bool sorted,
-                                         const int *sort_tiles, const uint8_t *sort_places) {
+__device__ __forceinline__ void schedule(const Cta<Lay> &c, const ChunkParams &p,
+                                         const Cache8 &cache, bool sorted, const int *sort_tiles,
+                                         const uint8_t *sort_places) {
   const int lane = c.lane;
   int block = blockIdx.x, seg = blockIdx.z;
   bool have = true, last = !kMany;
   uint32_t claims = 0;
+  int batches = 0;  // of scales
+  bool ok = true;
   Order order = {};
   if (sorted) order = read_order(p, lane, sort_tiles, sort_places);
   for (uint32_t w = 0;; ++w) {
@@ -224,97 +309,13 @@ __device__ __forceinline__ void schedule(const Cta<Lay> &c, const ChunkParams &p
       ptx::mbar_arrive(c.bar(Lay::kWorkFull));
     }
     __syncwarp();
-    if (d.nrow == 0 || !kMany) break;
+    if (d.nrow == 0) break;
+    if (d.n > 0 && ok) ok = look_up_scales(c, p, cache, d, batches);
+    if (!kMany) break;
     volatile int dummy = 0;
     if (!__all_sync(0xffffffffu, chunk_wait<false, 4>(c.bar(Lay::kWorkRead), w & 1, &dummy)) ||
         *c.abort_flag)
       last = true;
-  }
-}
-
-// Scales of a work's key tiles.
-template <bool kMany, class Lay>
-__device__ __forceinline__ void look_up_scales(const Cta<Lay> &c, const ChunkParams &p,
-                                               const Cache8 &cache) {
-  const int lane = c.lane;
-  // Lane 8 i + g: 16 keys g of tile i of four.  Pages are looked up two batches ahead, scales
-  // one.
-  const int mine = lane >> 3, g16 = 16 * (lane & 7);
-  const int shift = 31 - __clz(cache.block), blocks = cache.P >> shift;
-  int batches = 0;
-  bool ok = true;
-  for (uint32_t w = 0; w == 0 || kMany; ++w) {
-    const Work d = c.next_work(w);
-    c.have_read();
-    if (d.nrow == 0) break;
-    if (d.n == 0 || !ok) continue;
-    auto key_of = [&](int t) { return (d.t0 + t + mine) * kKT + g16; };
-    auto look = [&](int t) {  // the page, -1 where it is none of the pool, -2 where no key is seen
-      const int key = key_of(t);
-      if (t + mine >= d.n || key > d.hi_max || key + 15 < d.lo_min) return -2;
-      const int page = p.tbl[static_cast<int64_t>(d.r) * p.M + key / cache.P];
-      return page >= 0 && page < cache.NP ? page : -1;
-    };
-    auto fetch = [&](int t, int page) {
-      if (page < 0) return 0u;
-      const uint8_t *k = cache.scales + cache.head(page, 0, d.kvh) * blocks +
-                         (key_of(t) % cache.P >> shift);
-      return static_cast<uint32_t>(k[0]) |
-             static_cast<uint32_t>(k[static_cast<int64_t>(cache.nkv) * blocks]) << 8;
-    };
-    constexpr int kNone = 1000;
-    int E = -kNone;
-    bool far = false, any_bad = false;
-    int page = look(0), page1 = look(kMetaBatch);
-    uint32_t bytes = fetch(0, page);
-    for (int t = 0; ok && t < d.n; t += kMetaBatch) {
-      const uint32_t bytes1 = fetch(t + kMetaBatch, page1);
-      const int page2 = look(t + 2 * kMetaBatch);
-      ok = __all_sync(0xffffffffu, c.reuse(Lay::kMEmpty, batches, kMetaBatches));
-      if (!ok) break;
-      const uint32_t kb = bytes & 255u, vb = bytes >> 8;
-      const bool counts = page >= 0 && vb != 255u;
-      int top = counts ? static_cast<int>(vb) - 127 : -kNone,
-          low = counts ? static_cast<int>(vb) - 127 : kNone;
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) {
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        low = min(low, __shfl_xor_sync(0xffffffffu, low, o));
-      }
-      int my_E = 0, my_far = 0;
-#pragma unroll
-      for (int i = 0; i < kMetaBatch; ++i) {
-        const int mx = __shfl_sync(0xffffffffu, top, 8 * i),
-                  mn = __shfl_sync(0xffffffffu, low, 8 * i);
-        // (a little more than it must: the accumulators are scaled whenever it grows)
-        const int grown = mx > E ? min(mx + 2, 127) : E;
-        far = far || (mn != kNone && mn < grown - 14);
-        if (!far) E = grown;
-        if (i == mine) {
-          my_E = far || E == -kNone ? 0 : E;
-          my_far = far;
-        }
-      }
-      const uint32_t bad = __ballot_sync(0xffffffffu, page == -1);
-      any_bad |= bad != 0;
-      TileMeta &m = c.meta[batches % kMetaBatches * kMetaBatch + mine];
-      m.k[lane & 7] = page >= 0 ? scale8_value(kb) : 1.f;
-      const uint32_t factor =
-          vb == 255u ? 0x7fffu : static_cast<uint32_t>(15 + static_cast<int>(vb) - 127 - my_E) << 10;
-      m.v[lane & 7] = page >= 0 ? (factor & 0xffffu) | vb << 16 | 1u << 24 : 0u;
-      if ((lane & 7) == 0) {
-        m.E = my_E;
-        m.far = my_far;
-        m.bad = static_cast<int>(bad >> (8 * mine) & 255u);
-      }
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(c.bar(Lay::kMFull + batches % kMetaBatches));
-      ++batches;
-      page = page1;
-      page1 = page2;
-      bytes = bytes1;
-    }
-    if (any_bad && lane == 0) raise_status(p.st, DFLASH_DEV_BAD_PAGE);
   }
 }
 
@@ -333,34 +334,34 @@ struct Ring {
   }
 };
 
-// Loads K's and V's tiles.  The warp has a dozen others beside it and a tile's time for two loads:
-// what can be is worked out once for many tiles.
-template <bool kMany, class Lay>
+// Loads K's (kV false) or V's tiles.  A load takes its warp some 700 cycles with a dozen others
+// beside it, half of what a tile may take: a warp for each of the two, and what can be is
+// worked out once for many tiles.
+template <bool kMany, bool kV, class Lay>
 __device__ __forceinline__ void load_tiles(const Cta<Lay> &c, const ChunkParams &p,
                                            const CUtensorMap &tm) {
   const int lane = c.lane;
   // A lane a box (page rows).  Boxes without a visible key and pages outside the pool are not
-  // loaded.  The next work is claimed once the loads come to the last kAhead tiles.
-  constexpr int kAhead = 3;
+  // loaded.  The next work is claimed once V's loads come to the last kAhead tiles.
+  constexpr int kAhead = 3, kSlots = kV ? Lay::kVs : Lay::kKs;
+  constexpr int kEmpty = kV ? Lay::kVEmpty : Lay::kKEmpty, kFull = kV ? Lay::kVFull : Lay::kKFull;
   const int shift = 31 - __clz(kKT / p.box_rows), boxes = 1 << shift, per = 32 >> shift;
   const uint32_t box_bytes = p.box_rows * Lay::kHD;
-  const int kv_rows = p.nkv * p.P;  // from a key's row to its value's
-  Ring<Lay::kKs> ring_k(true);
-  Ring<Lay::kVs> ring_v(true);
-  int at_k = 0, at_v = 0;
+  Ring<kSlots> ring(true);
+  int loaded = 0;
   bool ok = true;
   for (uint32_t w = 0; w == 0 || kMany; ++w) {
     const Work d = c.next_work(w);
-    if (d.nrow == 0 || d.n == 0 || !ok) {
+    if (!kV || d.nrow == 0 || d.n == 0 || !ok) {
       c.have_read();
       if (d.nrow == 0) break;
-      continue;
+      if (d.n == 0 || !ok) continue;
     }
     const int n = d.n;
     const uint64_t pol =
         d.total <= (1 << Lay::kShift) ? ptx::policy_evict_first() : ptx::policy_evict_normal();
     // Pages of 32 boxes at once, a lookup ahead of the one in use.  Lane boxes * i + b: the pool's
-    // row where box b of tile t + i begins in K, -1 where it is not loaded.
+    // row where box b of tile t + i begins, -1 where it is not loaded.
     auto look = [&](int t) {
       int row = -1;
       t += lane >> shift;
@@ -370,65 +371,43 @@ __device__ __forceinline__ void load_tiles(const Cta<Lay> &c, const ChunkParams 
           const int place = key0 / p.P, page = p.tbl[static_cast<int64_t>(d.r) * p.M + place];
           if (page >= 0 && page < p.NP)
             row = static_cast<int>(
-                ((static_cast<int64_t>(p.layer) * p.NP + page) * 2 * p.nkv + d.kvh) * p.P + key0 -
-                place * p.P);
+                (((static_cast<int64_t>(p.layer) * p.NP + page) * 2 + kV) * p.nkv + d.kvh) * p.P +
+                key0 - place * p.P);
         }
       }
       return row;
     };
-    int rows = look(0), ahead = look(per), behind = -1, base = 0;  // `rows` from tile base on
-    auto box_row = [&](int t) {
-      if (t >= base + per) {  // (a K: V is up to four tiles behind it, as many as `per` is at least)
-        behind = rows;
+    int rows = look(0), ahead = look(per), next = per;
+    for (int t = 0; t < n; ++t) {
+      if (kV && t == max(n - kAhead, 0)) c.have_read();
+      if (t == next) {
         rows = ahead;
-        base += per;
-        ahead = look(base + per);
+        next += per;
+        ahead = look(next);
       }
-      const int from = ((t - base) << shift) + lane;
-      const int row = __shfl_sync(0xffffffffu, t < base ? behind : rows, from & 31);
-      return lane < boxes ? row : -1;
-    };
-    auto load = [&](auto &ring, int empty, int full, uint32_t tiles, int row, bool skip) {
-      if (!ok) return;
-      ok = __all_sync(0xffffffffu,
-                      chunk_wait<false>(c.bar(empty + ring.slot), ring.phase, c.abort_flag));
-      if (!ok) return;
-      const uint32_t bar = c.bar(full + ring.slot);
+      int row = __shfl_sync(0xffffffffu, rows, ((t << shift) + lane) & 31);
+      if (lane >= boxes) row = -1;
+      if (ok)
+        ok = __all_sync(0xffffffffu,
+                        chunk_wait<false>(c.bar(kEmpty + ring.slot), ring.phase, c.abort_flag));
+      if (!ok) continue;
+      const bool skip = !kV && t == p.skip_tile;
+      const uint32_t bar = c.bar(kFull + ring.slot);
       const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, row >= 0)) * box_bytes;
       if (lane == 0 && !skip) ptx::mbar_arrive_expect_tx(bar, bytes);
       __syncwarp();
       if (row >= 0 && !skip)
-        ptx::tma_load_2d_hint(c.sm0 + tiles + ring.slot * Lay::kTile + lane * box_bytes, &tm, 0, row,
-                              bar, pol);
+        ptx::tma_load_2d_hint(c.sm0 + (kV ? Lay::kV : Lay::kK) + ring.slot * Lay::kTile +
+                                  lane * box_bytes,
+                              &tm, 0, row, bar, pol);
       ring.next();
-    };
-    auto load_k = [&](int t) {
-      load(ring_k, Lay::kKEmpty, Lay::kKFull, Lay::kK, box_row(t), t == p.skip_tile);
-      at_k += ok;
-    };
-    auto load_v = [&](int t) {
-      const int row = box_row(t);
-      load(ring_v, Lay::kVEmpty, Lay::kVFull, Lay::kV, row < 0 ? -1 : row + kv_rows, false);
-      at_v += ok;
-    };
-    // two row tiles: K0 V0 K1 V1 ...; one: K0 K1 V0 K2 V1 K3 ... and the last tiles' V
-    const int lead = Lay::kPair && d.nrow > 128 ? 0 : Lay::kScores;
-    for (int t = 0; t < min(lead, n); ++t) load_k(t);
-    for (int t = 0; t < n; ++t) {
-      if (t == max(n - kAhead, 0)) c.have_read();
-      if (lead == 0) load_k(t);
-      load_v(t);
-      if (lead && t + lead < n) load_k(t + lead);
+      ++loaded;
     }
   }
   if (*c.abort_flag && lane == 0) {  // wind down: the last copies land before the CTA ends
     volatile int dummy = 0;
-    for (int i = max(at_k - Lay::kKs, 0); i < at_k; ++i)
-      chunk_wait<false>(c.bar(Lay::kKFull + i % Lay::kKs), static_cast<uint32_t>((i / Lay::kKs) & 1),
-                        &dummy);
-    for (int i = max(at_v - Lay::kVs, 0); i < at_v; ++i)
-      chunk_wait<false>(c.bar(Lay::kVFull + i % Lay::kVs), static_cast<uint32_t>((i / Lay::kVs) & 1),
-                        &dummy);
+    for (int i = max(loaded - kSlots, 0); i < loaded; ++i)
+      chunk_wait<false>(c.bar(kFull + i % kSlots), static_cast<uint32_t>((i / kSlots) & 1), &dummy);
   }
 }
 

@@ -124,11 +124,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 8) {
     regs_less<kIssueRegs>();
     if (warp == 8) {
-      schedule<kMany>(cta, p, sorted, sort_tiles, sort_places);
+      load_tiles<kMany, true>(cta, p, tm);
     } else if (warp == 9) {
-      look_up_scales<kMany>(cta, p, cache);
+      schedule<kMany>(cta, p, cache, sorted, sort_tiles, sort_places);
     } else if (warp == 10) {
-      load_tiles<kMany>(cta, p, tm);
+      load_tiles<kMany, false>(cta, p, tm);
     } else {
     // ------------------------------------------------ MMA issuer
     constexpr uint32_t idesc_qk = idesc_of(128, kKT, 0, false);

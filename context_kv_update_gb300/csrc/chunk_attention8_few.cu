@@ -29,10 +29,9 @@ constexpr int kFewSoftmaxRegs = 128, kFewIssueRegs = 64, kFewWidenRegs = 80;
 static_assert(256 * (kFewSoftmaxRegs + kFewWidenRegs) + 128 * kFewIssueRegs <= kFewThreads * 96, "");
 
 template <int N>
-struct LayoutFew : Bars<3, 3, 3, 4> {
-  using B = Bars<3, 3, 3, 4>;
+struct LayoutFew : Bars<3, N == 16 ? 6 : 5, 2, 4> {
+  using B = Bars<3, N == 16 ? 6 : 5, 2, 4>;
   static constexpr int kHD = 128, kShift = N == 16 ? 4 : 5, kWideners = 8;
-  static constexpr bool kPair = false;
   static constexpr uint32_t kTile = kKT * kHD, kTile16 = 2 * kTile;
   static constexpr uint32_t kK = 2 * N * 128;  // Q: N rows of hi, N of lo
   static constexpr uint32_t kV = kK + B::kKs * kTile;
@@ -142,11 +141,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   } else if (warp >= 8) {
     regs_less<kFewIssueRegs>();
     if (warp == 8) {
-      schedule<kMany>(cta, p, sorted, sort_tiles, sort_places);
+      load_tiles<kMany, true>(cta, p, tm);
     } else if (warp == 9) {
-      look_up_scales<kMany>(cta, p, cache);
+      schedule<kMany>(cta, p, cache, sorted, sort_tiles, sort_places);
     } else if (warp == 10) {
-      load_tiles<kMany>(cta, p, tm);
+      load_tiles<kMany, false>(cta, p, tm);
     } else {
       // ---------------------------------------------- MMA issuer
       constexpr uint32_t idesc_qk = idesc_of(128, 2 * N, 0, false);
