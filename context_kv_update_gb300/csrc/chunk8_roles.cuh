@@ -154,6 +154,18 @@ struct Cta {
     const At x = lane == 1 ? b : lane == 2 ? e : a;
     return __all_sync(0xffffffffu, chunk_wait<kSpin>(x.bar, x.phase, abort_flag));
   }
+  // Whether the phase is over, without a wait.
+  __device__ __forceinline__ bool passed(int i, uint32_t phase) const {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar(i)), "r"(phase)
+        : "memory");
+    return __all_sync(0xffffffffu, done != 0);
+  }
   __device__ __forceinline__ const TileMeta &scales(int batch, int t) const {
     return meta[batch % kMetaBatches * kMetaBatch + t % kMetaBatch];
   }
@@ -580,9 +592,9 @@ struct Widener {
 };
 
 // All V tiles of a work, and its scales handed back: `at` tiles and `batches` of scales so far.
-template <class Lay>
+template <class Lay, class Early>
 __device__ __forceinline__ bool widen_tiles(const Cta<Lay> &c, const Widener<Lay> &widener,
-                                            const Work &d, int &at, int &batches) {
+                                            const Work &d, int &at, int &batches, Early early) {
   int left = 0;  // batches handed back
   auto hand_back = [&](int to_batch) {
     __syncwarp();
@@ -598,6 +610,7 @@ __device__ __forceinline__ bool widen_tiles(const Cta<Lay> &c, const Widener<Lay
          c.arrived(Lay::kVFull, at, Lay::kVs) && c.reuse(Lay::kWEmpty, at, Lay::kWides);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
+    early(t);
     widener.tile(d, t, c.scales(b, t), c.sm + Lay::kV + raw * Lay::kTile,
                  c.sm + Lay::kWide + slot * Lay::kTile16);
     ptx::fence_proxy_async_smem();

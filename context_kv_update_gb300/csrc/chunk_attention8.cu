@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (u == 0) q_scale[(w & 1) * 256 + row] = exp2_int(e);
       });
-      if (ok) ok = widen_tiles(cta, widener, d, at, batches);
+      if (ok) ok = widen_tiles(cta, widener, d, at, batches, [](int) {});
     }
   } else if (warp >= 8) {
     regs_less<kIssueRegs>();

@@ -73,6 +73,13 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&r)[8]) {
       : "memory");
 }
 
+// The warp's largest; NaN where all are.
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 template <int N, bool kMany>
 __global__ void __launch_bounds__(kFewThreads, 1)
     chunk_attn8_few_kernel(const __grid_constant__ CUtensorMap tm,
@@ -123,20 +130,34 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     int at = 0, batches = 0;  // V tiles and batches of scales so far
     uint32_t loads = 0u;
     bool ok = true;
-    for (uint32_t w = 0; w == 0 || kMany; ++w) {
-      const Work d = cta.next_work(w);
-      cta.have_read();
-      if (d.nrow == 0) break;
-      if (d.n == 0 || !ok) continue;
-      // (rows past the work's are zeros: their scores exceed no reference)
-      ok = split_rows(cta, p, d, N, loads++,
-                      [&](int row, int u, const uint32_t *hi, const uint32_t *lo, int e) {
+    // (rows past the work's are zeros: their scores exceed no reference)
+    auto split = [&](const Work &d, uint32_t w) {
+      return split_rows(cta, p, d, N, loads++,
+                        [&](int row, int u, const uint32_t *hi, const uint32_t *lo, int e) {
         uint8_t *dst = sm + row * 128 + ((u ^ (row & 7)) << 4);
         *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4 *>(dst + N * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         if (u == 0) q_scale[(w & 1) * N + row] = exp2_int(e);
       });
-      if (ok) ok = widen_tiles(cta, widener, d, at, batches);
+    };
+    bool here = false;  // this work's Q
+    for (uint32_t w = 0; w == 0 || kMany; ++w) {
+      const Work d = cta.next_work(w);
+      cta.have_read();
+      if (d.nrow == 0) break;
+      if (d.n == 0 || !ok) continue;
+      if (!here) ok = split(d, w);
+      here = false;
+      // The next work's Q before the last two tiles, where it is known by then and the scores of
+      // this one are done: at its end, with loads of 2000 cycles, all would wait for it.
+      auto early = [&](int t) {
+        if (!kMany || here || t < d.n - 2 || !cta.passed(Lay::kWorkFull, (w + 1) & 1) ||
+            !cta.passed(Lay::kQEmpty, (loads - 1) & 1))
+          return;
+        const Work e = cta.next_work(w + 1);
+        if (e.n > 0) here = split(e, w + 1);
+      };
+      if (ok) ok = widen_tiles(cta, widener, d, at, batches, early);
     }
   } else if (warp >= 8) {
     regs_less<kFewIssueRegs>();
@@ -191,14 +212,16 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       };
       for (uint32_t w = 0; w == 0 || kMany; ++w) {
         const Work d = cta.next_work(w);
-        cta.have_read();
-        if (d.nrow == 0) break;
         const int tiles = __shfl_sync(0xffffffffu, d.n, 0);
+        if (ok && tiles > 0) {
+          const At q = {cta.bar(Lay::kQReady), loads & 1};
+          ok = wait(q, q, q);
+          ++loads;
+        }
+        cta.have_read();  // (after the wait: two works' Q later its phase would be the same again)
+        if (d.nrow == 0) break;
         if (!ok || tiles == 0) continue;
         // Scores run four tiles ahead of the weights.
-        ok = wait(At{cta.bar(Lay::kQReady), loads & 1}, At{cta.bar(Lay::kQReady), loads & 1},
-                  At{cta.bar(Lay::kQReady), loads & 1});
-        ++loads;
         for (int t = 0; ok && t < min(tiles, 4); ++t) {
           const At k = slot(Lay::kKFull, at_k + t, kKs);
           ok = wait(k, k, k);
@@ -251,7 +274,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     // a group's rows: lo, hi, factor, kFewLift - reference, scaling; the warps' maxima [4]; reference,
     // what was added to the scores; of both groups, units of the accumulators; rows that moved, and
     // that have no reference
-    float *rows = q_scale + 2 * N + g * 11 * N, *other = q_scale + 2 * N + (g ^ 1) * 11 * N;
+    float *rows = q_scale + 2 * N + g * 11 * N;
     int *row_lo = reinterpret_cast<int *>(rows), *row_hi = row_lo + N;
     float *row_f = rows + 2 * N, *row_nm = rows + 3 * N, *row_corr = rows + 4 * N,
           *part = rows + 5 * N, *row_m = rows + 9 * N, *row_delta = rows + 10 * N;
@@ -272,14 +295,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       } else {
         *abort_flag = 1;
       }
-      cta.have_read();
-      if (nrow == 0) break;
-      if (n > 0) {
-        if (ok)
-          ok = __all_sync(0xffffffffu,
-                          chunk_wait<false>(cta.bar(Lay::kQReady), loads & 1, abort_flag));
+      if (n > 0 && ok) {
+        ok = __all_sync(0xffffffffu,
+                        chunk_wait<false>(cta.bar(Lay::kQReady), loads & 1, abort_flag));
         ++loads;
       }
+      cta.have_read();  // (after the wait, as the issuing warp)
+      if (nrow == 0) break;
       const int row0 = d.row0, t0 = d.t0;
       // keys that every row sees
       int all_lo, all_hi, x;
@@ -293,7 +315,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         row_hi[tid] = hi;
         row_f[tid] = real && ok && n > 0 ? q_scale[(wk & 1) * N + tid] * p.scale_log2 : 0.f;
         row_m[tid] = real ? -INFINITY : 0.f;
-        row_nm[tid] = real ? INFINITY : 0.f;  // no reference yet: every score exceeds it
+        row_nm[tid] = 0.f;
       }
       ptx::bar_sync(2 + g, 128);
 
@@ -331,9 +353,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         const bool dead = (tile.bad >> (tid >> 4)) & 1;
         const bool cut = !(all_lo <= kb && all_hi >= kb + kKT - 1);
         const bool far = tile.far != 0;
-        float y[N];
-        // Scores, in powers of two: relative to the rows' references, or as they are.
-        auto weigh = [&](bool absolute) {
+        float y[N] = {};
+        if (got) {  // scores, in powers of two: relative to the rows' references where they have one
           float low[N];
           tmem_ld<N>(tm_s, y);
           tmem_ld<N>(tm_s + N, low);
@@ -341,8 +362,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
           for (int r = 0; r < N; r += 4) {
             const float4 f = *reinterpret_cast<const float4 *>(row_f + r);
-            float4 nm = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (!absolute) nm = *reinterpret_cast<const float4 *>(row_nm + r);
+            const float4 nm = *reinterpret_cast<const float4 *>(row_nm + r);
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
               const int x = r + e;
@@ -363,32 +383,22 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
             for (int r = 0; r < N; ++r) y[r] = -INFINITY;
           }
-        };
-        bool need = !got || fresh || tile.E != E;
-        if (got && !fresh) {
-          weigh(false);
-          float top = y[0];
-#pragma unroll
-          for (int r = 1; r < N; ++r) top = fmaxf(top, y[r]);
-          need = need || top > kFewLag + kFewLift;
         }
+        float top = y[0];
+#pragma unroll
+        for (int r = 1; r < N; ++r) top = fmaxf(top, y[r]);
+        const bool need = !got || tile.E != E || top > kFewLag + kFewLift;
         // (A warp whose wait ran out votes too, and all end together: a barrier has no limit.)
-        if (ptx::bar_or(2 + g, 128, need)) {
+        if (fresh || ptx::bar_or(2 + g, 128, need)) {
           if (ptx::bar_or(2 + g, 128, !got)) {
             ok = false;
             break;
           }
-          // Rows whose scores exceed their reference (in some lane; all in a tile where a row
-          // has none yet), the warp's maxima of them, floats in the order of integers.
-          if (fresh) weigh(true);
-          float most = -INFINITY;
+          float most = -INFINITY;  // the rows' largest, of the warp's keys
 #pragma unroll
           for (int r = 0; r < N; ++r) {
-            if (fresh || __any_sync(0xffffffffu, y[r] > kFewLag + kFewLift)) {
-              int i = __float_as_int(y[r]);
-              i = __reduce_max_sync(0xffffffffu, i ^ (i >> 31 & 0x7fffffff));
-              if (lane == r) most = __int_as_float(i ^ (i >> 31 & 0x7fffffff));
-            }
+            const float x = warp_max(y[r]);
+            if (lane == r) most = x;
           }
           if (lane < N) part[w4 * N + lane] = most;
           ptx::bar_sync(2 + g, 128);
@@ -397,14 +407,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             const bool row = tid < N;
             float m = 0.f, now = 0.f;
             if (row) {
-              const float top = fmaxf(fmaxf(part[tid], part[N + tid]),
-                                      fmaxf(part[2 * N + tid], part[3 * N + tid]));
-              const float before = row_nm[tid], x = fresh ? top : top - before;
+              const float before = row_nm[tid], x = fmaxf(fmaxf(part[tid], part[N + tid]),
+                                                          fmaxf(part[2 * N + tid],
+                                                                part[3 * N + tid])) - before;
               m = now = row_m[tid];
               if (m == -INFINITY || x > m + kFewLag) now = fmaxf(m, x);
-              const float nm = tid >= nrow ? 0.f : now == -INFINITY ? INFINITY : kFewLift - now;
+              const float nm = tid >= nrow || now == -INFINITY ? 0.f : kFewLift - now;
               row_corr[tid] = m == -INFINITY ? 1.f : ptx::ex2(m - now);
-              row_delta[tid] = fresh ? nm : nm == before ? 0.f : nm - before;
+              row_delta[tid] = nm - before;
               row_m[tid] = now;
               row_nm[tid] = nm;
             }
@@ -416,15 +426,15 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             }
           }
           ptx::bar_sync(2 + g, 128);
-#pragma unroll
-          for (int r = 0; r < N; r += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(row_corr + r);
-            l[r] *= f.x;
-            l[r + 1] *= f.y;
-            l[r + 2] *= f.z;
-            l[r + 3] *= f.w;
-          }
           if (t >= 2) {
+#pragma unroll
+            for (int r = 0; r < N; r += 4) {
+              const float4 f = *reinterpret_cast<const float4 *>(row_corr + r);
+              l[r] *= f.x;
+              l[r + 1] *= f.y;
+              l[r + 2] *= f.z;
+              l[r + 3] *= f.w;
+            }
             lost |= !product_done();
             const uint32_t tm_o = tmem + kColOut + 128 * g + lane_off;
 #pragma unroll 1
@@ -449,10 +459,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
           for (int r = 0; r < N; r += 4) {
             const float4 dl = *reinterpret_cast<const float4 *>(row_delta + r);
-            const float ds[4] = {dl.x, dl.y, dl.z, dl.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)  // a row that has seen no key sees none here
-              y[r + e] = ds[e] == INFINITY ? -INFINITY : y[r + e] + ds[e];
+            y[r] += dl.x;
+            y[r + 1] += dl.y;
+            y[r + 2] += dl.z;
+            y[r + 3] += dl.w;
           }
         }
         uint32_t pk[N / 2];
@@ -489,19 +499,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       hand_back(all);
       batches += all;
       // ---------------------------------------------- epilogue
+      // (while the last products run: the rows' sums, and each group a thread a row for their
+      // factors of the two accumulators and where they are written)
       const bool had0 = n > 0, had1 = n > 1;  // groups with products
-      if (ok && had0)
-        ok = __all_sync(0xffffffffu,
-                        chunk_wait<false>(cta.bar(Lay::kODone), outs0 & 1, abort_flag));
-      if (ok && had1)
-        ok = __all_sync(0xffffffffu,
-                        chunk_wait<false>(cta.bar(Lay::kODone + 1), outs1 & 1, abort_flag));
-      ptx::tc_fence_after();
-      outs0 += had0;
-      outs1 += had1;
-      // Sums over the warp's keys: each step halves the rows a lane holds.
 #pragma unroll
-      for (int o = 16, c = N / 2; o > 0; o >>= 1, c >>= 1) {
+      for (int o = 16, c = N / 2; o > 0; o >>= 1, c >>= 1) {  // halves the rows a lane holds
         if (c > 0) {
 #pragma unroll
           for (int r = 0; r < c; ++r) {
@@ -514,22 +516,26 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
       if (N == 32 || !(lane & 1)) part[w4 * N + (N == 32 ? lane : lane >> 1)] = l[0];
       if (tid == 0) units[g] = exp2_int(min(max(E, -149), 127));
-      const bool broken = ptx::bar_or(1, 256, !ok);
-      ok = ok && !broken;
-      const int seg = d.seg;
-      // a row's factors of the two accumulators, by its thread of group 0
-      float *f0 = row_corr, *f1 = other + 4 * N;
-      if (g == 0 && tid < N) {
-        const float m0 = broken ? -INFINITY : row_m[tid], m1 = broken ? -INFINITY : other[9 * N + tid];
+      ok = !ptx::bar_or(1, 256, !ok);
+      float *f0 = row_corr, *f1 = row_delta;
+      int64_t *row_at = reinterpret_cast<int64_t *>(row_lo);  // (lo and hi are done with)
+      if (tid < N) {
+        const float *g0 = q_scale + 2 * N, *g1 = g0 + 11 * N;
+        const float m0 = ok ? g0[9 * N + tid] : -INFINITY, m1 = ok ? g1[9 * N + tid] : -INFINITY;
         const bool any = tid < nrow && fmaxf(m0, m1) != -INFINITY;
         const float m = fmaxf(m0, m1) - kFewLift;  // weights are relative to this
         const float w0 = m0 == -INFINITY ? 0.f : ptx::ex2(m0 - kFewLift - m),
                     w1 = m1 == -INFINITY ? 0.f : ptx::ex2(m1 - kFewLift - m);
-        const float *p1 = other + 5 * N;
-        const float sum0 = (part[tid] + part[N + tid]) + (part[2 * N + tid] + part[3 * N + tid]),
-                    sum1 = (p1[tid] + p1[N + tid]) + (p1[2 * N + tid] + p1[3 * N + tid]);
+        float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+        for (int i = 5; i < 9; ++i) {
+          sum0 += g0[i * N + tid];
+          sum1 += g1[i * N + tid];
+        }
         const float sum = sum0 * w0 + sum1 * w1;
         const int flat = row0 + tid, tok = flat / p.G, h = d.kvh * p.G + flat - tok * p.G;
+        const int64_t orow = static_cast<int64_t>(d.a) + tok;
+        int64_t to = orow * p.os + static_cast<int64_t>(h) * HD;
         float gain = 1.f;
         if (p.S == 1) {
           float top = m, den = sum;
@@ -539,25 +545,31 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             den = sum * ptx::ex2(m - top) + ptx::ex2(sk - top);
           }
           gain = any ? ptx::ex2(m - top) / den : 0.f;
-        } else if (tid < nrow) {
-          const int64_t at = ((static_cast<int64_t>(d.a) + tok) * p.hq + h) * p.S + seg;
-          p.ws_m[at] = any ? m : -INFINITY;
-          p.ws_l[at] = any ? sum : 0.f;
+        } else {
+          const int64_t at = (orow * p.hq + h) * p.S + d.seg;
+          to = any ? at * HD : -1;
+          if (tid < nrow && g == 0) {
+            p.ws_m[at] = any ? m : -INFINITY;
+            p.ws_l[at] = any ? sum : 0.f;
+          }
         }
         f0[tid] = any ? w0 * units[0] * gain : 0.f;
         f1[tid] = any ? w1 * units[1] * gain : 0.f;
-        row_nm[tid] = any ? 1.f : 0.f;
+        row_at[tid] = tid < nrow ? to : -1;  // -1: not written
       }
-      ptx::bar_sync(1, 256);
-      if (g) {  // (read where group 0 wrote)
-        f0 = other + 4 * N;
-        f1 = row_corr;
-      }
-      const float *has_keys = g ? other + 3 * N : row_nm;
+      ptx::bar_sync(2 + g, 128);
+      if (ok && had0)
+        ok = __all_sync(0xffffffffu,
+                        chunk_wait<false>(cta.bar(Lay::kODone), outs0 & 1, abort_flag));
+      if (ok && had1)
+        ok = __all_sync(0xffffffffu,
+                        chunk_wait<false>(cta.bar(Lay::kODone + 1), outs1 & 1, abort_flag));
+      ptx::tc_fence_after();
+      outs0 += had0;
+      outs1 += had1;
       // Half of the rows a group, a dim a thread.
 #pragma unroll 1
-      for (int c = g * (N / 2); c < (g + 1) * (N / 2); c += 8) {
-        if (c >= nrow) break;
+      for (int c = g * (N / 2); c < min((g + 1) * (N / 2), nrow); c += 8) {
         float o[8] = {};
         if (ok && had0) {
           float v[8];
@@ -573,13 +585,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          if (c + e >= nrow) break;
-          const int flat = row0 + c + e, tok = flat / p.G, h = d.kvh * p.G + flat - tok * p.G;
-          const int64_t orow = static_cast<int64_t>(d.a) + tok;
+          const int64_t to = row_at[c + e] + tid;
+          if (to < tid) continue;
           if (p.S == 1)
-            p.out[orow * p.os + static_cast<int64_t>(h) * HD + tid] = f32_to_bf16_rn(o[e]);
-          else if (has_keys[c + e] != 0.f)
-            p.ws_o[((orow * p.hq + h) * p.S + seg) * HD + tid] = o[e];
+            p.out[to] = f32_to_bf16_rn(o[e]);
+          else
+            p.ws_o[to] = o[e];
         }
       }
       ptx::tc_fence_before();
