@@ -20,6 +20,7 @@ constexpr int kThreads = 512;
 // the others give them up: 2 x 128 x 184 + 128 x 64 + 128 x 80 = 65536.
 constexpr int kSoftmaxRegs = 184, kIssueRegs = 64, kWidenRegs = 80;
 static_assert(256 * kSoftmaxRegs + 128 * (kIssueRegs + kWidenRegs) <= kThreads * 128, "");
+constexpr int kWidenTeam = 4;  // warps that widen a tile of V
 constexpr int kMetaBatch = 4, kMetaBatches = 4;  // key tiles looked up at once, of that many more
 // P's weights carry 2^7: fp16's smallest steps are further below a row's largest weight then.
 // (The reference maximum lags by up to 2^8, and 2^15 is still an fp16 number.)
@@ -156,15 +157,7 @@ struct Cta {
   }
   // Whether the phase is over, without a wait.
   __device__ __forceinline__ bool passed(int i, uint32_t phase) const {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar(i)), "r"(phase)
-        : "memory");
-    return __all_sync(0xffffffffu, done != 0);
+    return __all_sync(0xffffffffu, ptx::mbar_test(bar(i), phase));
   }
   __device__ __forceinline__ const TileMeta &scales(int batch, int t) const {
     return meta[batch % kMetaBatches * kMetaBatch + t % kMetaBatch];
@@ -177,8 +170,8 @@ struct Cta {
     init(Lay::kKFull, Lay::kKs, 1);
     init(Lay::kKEmpty, Lay::kKs, 1);
     init(Lay::kVFull, Lay::kVs, 1);
-    init(Lay::kVEmpty, Lay::kVs, Lay::kWideners);  // the widening warps
-    init(Lay::kWFull, Lay::kWides, Lay::kWideners);
+    init(Lay::kVEmpty, Lay::kVs, kWidenTeam);
+    init(Lay::kWFull, Lay::kWides, kWidenTeam);
     init(Lay::kWEmpty, Lay::kWides, 1);
     init(Lay::kMFull, kMetaBatches, 1);
     init(Lay::kMEmpty, kMetaBatches, 8 + Lay::kWideners + 1);  // softmax, widening, issuing warps
@@ -399,9 +392,19 @@ __device__ __forceinline__ void load_tiles(const Cta<Lay> &c, const ChunkParams 
       }
       int row = __shfl_sync(0xffffffffu, rows, ((t << shift) + lane) & 31);
       if (lane >= boxes) row = -1;
-      if (ok)
-        ok = __all_sync(0xffffffffu,
-                        chunk_wait<false>(c.bar(kEmpty + ring.slot), ring.phase, c.abort_flag));
+      if (ok) {
+        int bar = kEmpty + ring.slot;
+        uint32_t phase = ring.phase;
+        bool used = true;
+        if (!kV && Lay::kScores == 4) {  // the scores are done: one barrier tells who waits for them too
+          const int before = loaded - kSlots;
+          used = before >= 0;
+          bar = Lay::kSFull + (before & 3);
+          phase = before >> 2 & 1;
+        }
+        ok = !used ||
+             __all_sync(0xffffffffu, chunk_wait<false>(c.bar(bar), phase, c.abort_flag));
+      }
       if (!ok) continue;
       const bool skip = !kV && t == p.skip_tile;
       const uint32_t bar = c.bar(kFull + ring.slot);
@@ -510,10 +513,10 @@ __device__ __forceinline__ bool split_rows(const Cta<Lay> &c, const ChunkParams 
 // Widens V's tiles to 16 bits: the calling warp's share of the rows, 32 or 16.
 template <class Lay>
 struct Widener {
-  static constexpr int kSub = Lay::kHD / 64, kRows = 128 / Lay::kWideners;
+  static constexpr int kSub = Lay::kHD / 64, kRows = 128 / kWidenTeam;
   uint32_t from[kSub], to[kSub][2];
   int wr, row8[kSub];  // the warp's first row; the lane's of every eight
-  __device__ __forceinline__ Widener(int warp, int lane) : wr(kRows * (warp - 12)) {
+  __device__ __forceinline__ Widener(int warp, int lane) : wr(kRows * (warp % kWidenTeam)) {
     // A lane's 16 codes of every eight rows (heads of 64: once; 128: twice).  Eight lanes read and
     // write 16 bytes each of different banks: 64: of rows r and r + 1; 128: of r and r ^ 5, since
     // a row's chunks arrive at their number xor r, and leave at twice it xor r.
@@ -595,6 +598,9 @@ struct Widener {
 template <class Lay, class Early>
 __device__ __forceinline__ bool widen_tiles(const Cta<Lay> &c, const Widener<Lay> &widener,
                                             const Work &d, int &at, int &batches, Early early) {
+  // A team takes every kTeams-th tile.
+  constexpr int kTeams = Lay::kWideners / kWidenTeam;
+  const int team = (threadIdx.x >> 5) / kWidenTeam - 12 / kWidenTeam;
   int left = 0;  // batches handed back
   auto hand_back = [&](int to_batch) {
     __syncwarp();
@@ -603,11 +609,11 @@ __device__ __forceinline__ bool widen_tiles(const Cta<Lay> &c, const Widener<Lay
   };
   bool ok = true;
 #pragma unroll 1
-  for (int t = 0; t < d.n; ++t) {
-    const int b = batches + t / kMetaBatch, raw = at % Lay::kVs, slot = at % Lay::kWides;
+  for (int t = (at ^ team) & (kTeams - 1); t < d.n; t += kTeams) {
+    const int b = batches + t / kMetaBatch, v = at + t, raw = v % Lay::kVs, slot = v % Lay::kWides;
     hand_back(t / kMetaBatch);
-    ok = (t % kMetaBatch != 0 || c.arrived(Lay::kMFull, b, kMetaBatches)) &&
-         c.arrived(Lay::kVFull, at, Lay::kVs) && c.reuse(Lay::kWEmpty, at, Lay::kWides);
+    ok = (t % kMetaBatch >= kTeams || c.arrived(Lay::kMFull, b, kMetaBatches)) &&
+         c.arrived(Lay::kVFull, v, Lay::kVs) && c.reuse(Lay::kWEmpty, v, Lay::kWides);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
     early(t);
@@ -619,8 +625,8 @@ __device__ __forceinline__ bool widen_tiles(const Cta<Lay> &c, const Widener<Lay
       ptx::mbar_arrive(c.bar(Lay::kWFull + slot));
       ptx::mbar_arrive(c.bar(Lay::kVEmpty + raw));
     }
-    ++at;
   }
+  at += d.n;
   const int all = (d.n + kMetaBatch - 1) / kMetaBatch;
   hand_back(all);
   batches += all;

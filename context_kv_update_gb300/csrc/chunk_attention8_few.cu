@@ -29,8 +29,8 @@ constexpr int kFewSoftmaxRegs = 128, kFewIssueRegs = 64, kFewWidenRegs = 80;
 static_assert(256 * (kFewSoftmaxRegs + kFewWidenRegs) + 128 * kFewIssueRegs <= kFewThreads * 96, "");
 
 template <int N>
-struct LayoutFew : Bars<3, N == 16 ? 6 : 5, 2, 4> {
-  using B = Bars<3, N == 16 ? 6 : 5, 2, 4>;
+struct LayoutFew : Bars<3, N == 16 ? 4 : 3, 3, 4> {
+  using B = Bars<3, N == 16 ? 4 : 3, 3, 4>;
   static constexpr int kHD = 128, kShift = N == 16 ? 4 : 5, kWideners = 8;
   static constexpr uint32_t kTile = kKT * kHD, kTile16 = 2 * kTile;
   static constexpr uint32_t kK = 2 * N * 128;  // Q: N rows of hi, N of lo
@@ -182,33 +182,33 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       const uint64_t dp = ptx::smem_desc(base + Lay::kP, kChunkBytes, 16 * N,
                                          N == 32 ? kSwizzle64B : kSwizzle32B);
       using At = typename Cta<Lay>::At;
-      int at_k = 0, at_v = 0, batches = 0;  // of K tiles, V tiles, batches of scales
+      int at = 0, batches = 0;  // tiles and batches of scales before this work
+      Ring<kKs> keys(false);
+      Ring<kWides> wide(false);
       uint32_t handed0 = 0u, handed1 = 0u, loads = 0u;  // phases of p_full and q_ready
       bool ok = true;
-      auto slot = [&](int first, int at, int n) { return cta.full(first, at, n); };
       auto wait = [&](At a, At b, At c) {
         const bool got = cta.template wait<true>(a, b, c);
         ptx::tc_fence_after();
         return got;
       };
-      auto qk = [&](int t, int at) {  // S^T = K (hi, lo)^T, of the work's tile t
-        const uint64_t a = dk + (((at % kKs) * Lay::kTile) >> 4);
+      auto qk = [&](int t) {  // S^T = K (hi, lo)^T, of the work's tile t: K's slot is free then too
+        const int buffer = (at + t) & 3;
+        const uint64_t a = dk + ((keys.slot * Lay::kTile) >> 4);
 #pragma unroll
         for (int ks = 0; ks < HD / 32; ++ks)
-          mma_e4m3(tm0 + 64 * (t & 3), a + (ks * 32 >> 4), dq + (ks * 32 >> 4), idesc_qk,
+          mma_e4m3(tm0 + 64 * buffer, a + (ks * 32 >> 4), dq + (ks * 32 >> 4), idesc_qk,
                    ks > 0 ? 1u : 0u);
-        ptx::mma_commit(cta.bar(Lay::kSFull + (t & 3)));
-        ptx::mma_commit(cta.bar(Lay::kKEmpty + at % kKs));
+        ptx::mma_commit(cta.bar(Lay::kSFull + buffer));
       };
-      auto pv = [&](int g, int at, bool first, uint32_t idesc) {  // O_g^T (+)= V^T P^T
-        const uint64_t a = dv + (((at % kWides) * Lay::kTile16) >> 4);
+      auto pv = [&](int g, bool first, uint32_t idesc) {  // O_g^T (+)= V^T P^T: P is free then too
+        const uint64_t a = dv + ((wide.slot * Lay::kTile16) >> 4);
         const uint64_t b = dp + ((g * kKT * 2 * N) >> 4);
 #pragma unroll
         for (int ks = 0; ks < kKT / 16; ++ks)
           ptx::mma_bf16(tm0 + kColOut + 128 * g, a + ((ks * 2048) >> 4), b + ((ks * 32 * N) >> 4),
                         idesc, (!first || ks > 0) ? 1u : 0u);
-        ptx::mma_commit(cta.bar(Lay::kWEmpty + at % kWides));
-        ptx::mma_commit(cta.bar(Lay::kPDone + g));
+        ptx::mma_commit(cta.bar(Lay::kWEmpty + wide.slot));
       };
       for (uint32_t w = 0; w == 0 || kMany; ++w) {
         const Work d = cta.next_work(w);
@@ -223,39 +223,41 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         if (!ok || tiles == 0) continue;
         // Scores run four tiles ahead of the weights.
         for (int t = 0; ok && t < min(tiles, 4); ++t) {
-          const At k = slot(Lay::kKFull, at_k + t, kKs);
+          const At k = {cta.bar(Lay::kKFull + keys.slot), keys.phase};
           ok = wait(k, k, k);
           if (ok && elect_one()) {
-            qk(t, at_k + t);
+            qk(t);
             if (t == tiles - 1) ptx::mma_commit(cta.bar(Lay::kQEmpty));
           }
           __syncwarp();
+          keys.next();
         }
         for (int t = 0; ok && t < tiles; ++t) {
           const bool more = t + 4 < tiles;
           const int b = batches + t / kMetaBatch, g = t & 1;
-          const At v = slot(Lay::kWFull, at_v + t, kWides);
+          const At v = {cta.bar(Lay::kWFull + wide.slot), wide.phase};
           ok = wait(At{cta.bar(Lay::kPFull + g), (g ? handed1 : handed0) & 1}, v,
-                    more ? slot(Lay::kKFull, at_k + t + 4, kKs) : v);
+                    more ? At{cta.bar(Lay::kKFull + keys.slot), keys.phase} : v);
           if (!ok) break;
           if (g) ++handed1; else ++handed0;
           // (the widening warps and the group that handed P over have seen the tile's scales)
           const uint32_t idesc =
               __shfl_sync(0xffffffffu, cta.scales(b, t).far ? idesc_bf16 : idesc_f16, 0);
           if (elect_one()) {
-            pv(g, at_v + t, t < 2, idesc);
+            pv(g, t < 2, idesc);
             if (more) {
-              qk(t + 4, at_k + t + 4);
+              qk(t + 4);
               if (t + 4 == tiles - 1) ptx::mma_commit(cta.bar(Lay::kQEmpty));
             }
             if (t + 2 >= tiles) ptx::mma_commit(cta.bar(Lay::kODone + g));
           }
           __syncwarp();
+          wide.next();
+          if (more) keys.next();
           if ((t % kMetaBatch == kMetaBatch - 1 || t == tiles - 1) && lane == 0)
             ptx::mbar_arrive(cta.bar(Lay::kMEmpty + b % kMetaBatches));
         }
-        at_k += tiles;
-        at_v += tiles;
+        at += tiles;
         batches += (tiles + kMetaBatch - 1) / kMetaBatch;
       }
       if (!ok) {
@@ -281,8 +283,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     float *units = q_scale + 2 * N + 22 * N;
     uint32_t *marks = reinterpret_cast<uint32_t *>(units) + 4 + 4 * g;  // of the groups' accumulators
     int batches = 0;
-    uint32_t loads = 0u, outs0 = 0u, outs1 = 0u, products = 0u;  // of q_ready, o_done, p_done
-    uint32_t scores = 0u;  // bit b: the phase of S buffer b
+    int at = 0;  // tiles before this work
+    uint32_t loads = 0u, outs0 = 0u, outs1 = 0u;  // of q_ready, o_done
     bool ok = true;
     for (uint32_t wk = 0; wk == 0 || kMany; ++wk) {
       const volatile Work &d = cta.shared_work[wk & 1];
@@ -325,11 +327,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       int E = 0, left = 0;
       bool fresh = true;  // some row has no reference yet
       bool lost = false;  // a wait ran out: the group ends together with the next tile's vote
-      // The group's product before, which read P and wrote O.
-      auto product_done = [&] {
-        return products == 0 ||
-               __all_sync(0xffffffffu, chunk_wait<false>(cta.bar(Lay::kPDone + g),
-                                                         (products - 1) & 1, abort_flag));
+      // The group's product two tiles before, which read P and wrote O.  (A work's first tiles
+      // follow a work whose products are all done.)
+      auto product_done = [&](int t) {
+        return t < 2 || __all_sync(0xffffffffu, cta.arrived(Lay::kWEmpty, at + t - 2, kWides));
       };
       auto hand_back = [&](int to_batch) {
         __syncwarp();
@@ -339,13 +340,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       for (int t = g; ok && t < n; t += 2) {
         const int b = batches + t / kMetaBatch;
         hand_back(t / kMetaBatch);
-        const int buffer = t & 3;
+        const int buffer = (at + t) & 3;
         const uint32_t tm_s = tmem + 64 * buffer + lane_off;
-        const typename Cta<Lay>::At s_full = {cta.bar(Lay::kSFull + buffer), scores >> buffer & 1};
         bool got = (t % kMetaBatch >= 2 || cta.arrived(Lay::kMFull, b, kMetaBatches)) &&
-                   chunk_wait<false>(s_full.bar, s_full.phase, abort_flag);
+                   cta.arrived(Lay::kSFull, at + t, 4);
         got = __all_sync(0xffffffffu, got && !lost);
-        scores ^= 1u << buffer;
         ptx::tc_fence_after();
         const TileMeta &tile = cta.scales(b, t);
         const int kb = (t0 + t) * kKT, key = kb + tid;
@@ -435,7 +434,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
               l[r + 2] *= f.z;
               l[r + 3] *= f.w;
             }
-            lost |= !product_done();
+            lost |= !product_done(t);
             const uint32_t tm_o = tmem + kColOut + 128 * g + lane_off;
 #pragma unroll 1
             for (int c = 0; c < N; c += 16) {
@@ -481,8 +480,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
           for (int r = 0; r < N / 2; ++r) pk[r] = pack_f16x2(y[2 * r], y[2 * r + 1]);
         }
-        if (t >= 2) lost |= !product_done();
-        ++products;
+        lost |= !product_done(t);
         uint8_t *dst = sm + Lay::kP + (g * kKT + tid) * 2 * N;
         const int swap = N == 32 ? tid >> 1 & 3 : tid >> 2 & 1;
 #pragma unroll
@@ -494,6 +492,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         __syncwarp();
         if (lane == 0 && !lost) ptx::mbar_arrive(cta.bar(Lay::kPFull + g));
       }
+      at += n;
       ok = ok && !lost;
       const int all = (n + kMetaBatch - 1) / kMetaBatch;
       hand_back(all);
