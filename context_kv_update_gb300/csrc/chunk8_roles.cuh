@@ -99,7 +99,7 @@ struct Bars {
                        kVEmpty = kVFull + kVs, kWFull = kVEmpty + kVs, kWEmpty = kWFull + kWides,
                        kMFull = kWEmpty + kWides, kMEmpty = kMFull + kMetaBatches,
                        kSFull = kMEmpty + kMetaBatches, kPFull = kSFull + kScores,
-                       kPDone = kPFull + 2, kODone = kPDone + 2,
+                       kODone = kPFull + 2,
                        kQReady = kODone + 2, kQEmpty = kQReady + 1, kDrain = kQEmpty + 1,
                        kWorkFull = kDrain + 1, kWorkRead = kWorkFull + 1, kClaim = kWorkRead + 1,
                        kBarCount = kClaim + 1;
@@ -147,9 +147,6 @@ struct Cta {
   __device__ __forceinline__ At full(int first, int at, int n) const {
     return At{bar(first + at % n), static_cast<uint32_t>((at / n) & 1)};
   }
-  __device__ __forceinline__ At empty(int first, int at, int n) const {  // at >= n
-    return At{bar(first + at % n), static_cast<uint32_t>((at / n - 1) & 1)};
-  }
   template <bool kSpin>
   __device__ __forceinline__ bool wait(At a, At b, At e) const {
     const At x = lane == 1 ? b : lane == 2 ? e : a;
@@ -177,9 +174,8 @@ struct Cta {
     init(Lay::kMEmpty, kMetaBatches, 8 + Lay::kWideners + 1);  // softmax, widening, issuing warps
     init(Lay::kSFull, Lay::kScores, 1);
     init(Lay::kPFull, 2, 4);  // one arrival per warp of the group
-    init(Lay::kPDone, 2, 1);
     init(Lay::kODone, 2, 1);
-    init(Lay::kQReady, 1, Lay::kWideners);
+    init(Lay::kQReady, 1, 8);  // the warps that split Q
     init(Lay::kQEmpty, 1, 1);
     init(Lay::kDrain, 1, 1);
     init(Lay::kWorkFull, 1, 1);
@@ -467,42 +463,46 @@ __device__ __forceinline__ int split_q(const uint4 (&x)[N / 8], uint32_t (&hi)[N
   return e;
 }
 
-// A work's rows of Q, split: eight lanes a row, the next rows' loads under these, four rows a
-// warp at once, `rows` in all (those past the work's are zeros).  store(row, u, hi, lo, e)
-// takes a lane's part u of a row.  `loads` works before this one had their Q here.
+// Part u of eight of a work's row of Q (zeros past the work's rows); tok0: the first row's token.
+template <int HD>
+__device__ __forceinline__ void fetch_row(const ChunkParams &p, const Work &d, int tok0, int row,
+                                          int u, uint4 (&x)[HD / 64]) {
+#pragma unroll
+  for (int i = 0; i < HD / 64; ++i) x[i] = make_uint4(0, 0, 0, 0);
+  if (row >= d.nrow) return;
+  const int f = d.row0 - tok0 * p.G + row, tok = p.G == 1 ? f : static_cast<int>(__umulhi(f, p.g_inv));
+  const uint16_t *src = p.q + (d.a + tok0 + tok) * p.qs +
+                        static_cast<int64_t>(d.kvh * p.G + f - tok * p.G) * HD + u * (HD / 8);
+#pragma unroll
+  for (int i = 0; i < HD / 64; ++i) x[i] = reinterpret_cast<const uint4 *>(src)[i];
+}
+
+// A work's rows of Q, split by eight warps: eight lanes a row, 32 rows at once and the loads of 128
+// in flight.  store(row, u, hi, lo, e) takes a lane's part u of a row.  `loads` works before this
+// one had their Q here.
 template <class Lay, class Store>
 __device__ __forceinline__ bool split_rows(const Cta<Lay> &c, const ChunkParams &p, const Work &d,
-                                           int rows, uint32_t loads, Store store) {
-  constexpr int HD = Lay::kHD, kLoads = HD / 64;  // of 8 values
-  constexpr int kStep = 4 * Lay::kWideners;
-  const int lane = c.lane, warp = (threadIdx.x >> 5) - 12;
-  const int tok0 = d.row0 / p.G, rem0 = d.row0 - tok0 * p.G, u = lane & 7;
-  auto fetch = [&](int row, uint4(&x)[kLoads]) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) x[i] = make_uint4(0, 0, 0, 0);
-    if (row >= d.nrow) return;
-    const int f = rem0 + row, tok = p.G == 1 ? f : static_cast<int>(__umulhi(f, p.g_inv));
-    const uint16_t *src = p.q + (d.a + tok0 + tok) * p.qs +
-                          static_cast<int64_t>(d.kvh * p.G + f - tok * p.G) * HD + u * 8 * kLoads;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) x[i] = reinterpret_cast<const uint4 *>(src)[i];
-  };
-  uint4 x[kLoads];
+                                           uint32_t loads, Store store) {
+  constexpr int HD = Lay::kHD, kLoads = HD / 64, kAhead = 4;
+  const int lane = c.lane, warp = threadIdx.x >> 5, tok0 = d.row0 / p.G, u = lane & 7;
+  uint4 x[kAhead][kLoads];
   int row = 4 * warp + (lane >> 3);
-  fetch(row, x);
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch_row<HD>(p, d, tok0, row + 32 * i, u, x[i]);
   // the last scores of the work before are done
   if (loads > 0 && !__all_sync(0xffffffffu, chunk_wait<false>(c.bar(Lay::kQEmpty), (loads - 1) & 1,
                                                               c.abort_flag)))
     return false;
 #pragma unroll 1
-  for (; row - (lane >> 3) < rows; row += kStep) {
-    uint4 ahead[kLoads];
-    fetch(row + kStep, ahead);
+  for (; row - (lane >> 3) < d.nrow; row += 32) {
     uint32_t hi[2 * kLoads], lo[2 * kLoads];
-    const int e = split_q<8 * kLoads>(x, hi, lo);
-    if (row < rows) store(row, u, hi, lo, e);
+    const int e = split_q<8 * kLoads>(x[0], hi, lo);
+    if (row < d.nrow) store(row, u, hi, lo, e);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) x[i] = ahead[i];
+    for (int i = 0; i < kAhead - 1; ++i)
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) x[i][k] = x[i + 1][k];
+    fetch_row<HD>(p, d, tok0, row + 32 * kAhead, u, x[kAhead - 1]);
   }
   ptx::fence_proxy_async_smem();
   __syncwarp();

@@ -91,35 +91,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 12) {
     regs_less<kWidenRegs>();
-    // ------------------------------------------------ Q's split, V's widening
+    // ------------------------------------------------ V's widening
     const Widener<Lay> widener(warp, lane);
     int at = 0, batches = 0;  // V tiles and batches of scales so far
-    uint32_t loads = 0u;
     bool ok = true;
     for (uint32_t w = 0; w == 0 || kMany; ++w) {
       const Work d = cta.next_work(w);
       cta.have_read();
       if (d.nrow == 0) break;
-      if (d.n == 0 || !ok) continue;
-      ok = split_rows(cta, p, d, d.nrow, loads++,
-                      [&](int row, int u, const uint32_t *hi, const uint32_t *lo, int e) {
-        // HD 128: hi and lo in the two halves of 64 columns; 64: side by side in one
-        uint8_t *dst = sm + (row >> 7) * Lay::kTile16 + (row & 127) * 128;
-        if constexpr (HD == 128) {
-          const int at16 = (u ^ (row & 7)) << 4;
-          *reinterpret_cast<uint4 *>(dst + at16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4 *>(dst + kChunkBytes + at16) =
-              make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        } else {
-          const int half = (u & 1) * 8;
-          *reinterpret_cast<uint2 *>(dst + (((u >> 1) ^ (row & 7)) << 4) + half) =
-              make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2 *>(dst + (((4 + (u >> 1)) ^ (row & 7)) << 4) + half) =
-              make_uint2(lo[0], lo[1]);
-        }
-        if (u == 0) q_scale[(w & 1) * 256 + row] = exp2_int(e);
-      });
-      if (ok) ok = widen_tiles(cta, widener, d, at, batches, [](int) {});
+      if (d.n > 0 && ok) ok = widen_tiles(cta, widener, d, at, batches, [](int) {});
     }
   } else if (warp >= 8) {
     regs_less<kIssueRegs>();
@@ -242,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     regs_more<kSoftmaxRegs>();
-    // ------------------------------------------------ softmax groups
+    // ------------------------------------------------ softmax groups, which split Q first
     const int g = warp >> 2;
     const int tid = threadIdx.x & 127;  // TMEM lane = row of the group's tile
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -275,7 +255,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (real) key_range(p, d.c + (d.row0 + rt) / p.G, d.kv, &lo, &hi);
       const bool active = (split ? 0 : 128 * g) + (warp & 3) * 32 < nrow;  // the warp holds rows
       float row_scale = 0.f;  // of the row's scores
-      if (n > 0) {
+      if (n > 0 && ok) {
+        ok = split_rows(cta, p, cta.shared_work[wk & 1], loads,
+                        [&](int row, int u, const uint32_t *hi, const uint32_t *lo, int e) {
+          // HD 128: hi and lo in the two halves of 64 columns; 64: side by side in one
+          uint8_t *dst = sm + (row >> 7) * Lay::kTile16 + (row & 127) * 128;
+          if constexpr (HD == 128) {
+            const int at16 = (u ^ (row & 7)) << 4;
+            *reinterpret_cast<uint4 *>(dst + at16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(dst + kChunkBytes + at16) =
+                make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          } else {
+            const int half = (u & 1) * 8;
+            *reinterpret_cast<uint2 *>(dst + (((u >> 1) ^ (row & 7)) << 4) + half) =
+                make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2 *>(dst + (((4 + (u >> 1)) ^ (row & 7)) << 4) + half) =
+                make_uint2(lo[0], lo[1]);
+          }
+          if (u == 0) q_scale[(wk & 1) * 256 + row] = exp2_int(e);
+        });
         if (ok)
           ok = __all_sync(0xffffffffu, chunk_wait<false>(cta.bar(Lay::kQReady), loads & 1, abort_flag));
         ++loads;
@@ -542,7 +540,7 @@ cudaError_t launch_main(bool pair, const CUtensorMap &tm, const ChunkParams &p,
 // kernel of chunk_attention8_few.cu.
 int tile_shift(const dflash_geom &g, int B, int n_rows) {
   const int64_t rows = static_cast<int64_t>(n_rows) * (g.hq / g.nkv);
-  if (g.head_dim == 128 && rows <= 64LL * B)
+  if (g.head_dim == 128 && rows <= 32LL * B)
     return rows <= (1LL << kLeastFewShift) * B ? kLeastFewShift : kMostFewShift;
   return pair_form(g, B, n_rows) ? 8 : 7;
 }

@@ -130,34 +130,55 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     int at = 0, batches = 0;  // V tiles and batches of scales so far
     uint32_t loads = 0u;
     bool ok = true;
-    // (rows past the work's are zeros: their scores exceed no reference)
-    auto split = [&](const Work &d, uint32_t w) {
-      return split_rows(cta, p, d, N, loads++,
-                        [&](int row, int u, const uint32_t *hi, const uint32_t *lo, int e) {
+    // Eight lanes a row; rows past the work's are zeros: their scores exceed no reference.
+    static_assert(N <= 4 * Lay::kWideners, "");
+    const int row = 4 * (warp - 12) + (lane >> 3), u = lane & 7;
+    uint4 q[2];
+    auto fetch = [&](const Work &d) { fetch_row<HD>(p, d, d.row0 / p.G, row, u, q); };
+    auto split = [&](uint32_t w) {
+      uint32_t hi[4], lo[4];
+      const int e = split_q<16>(q, hi, lo);
+      if (row < N) {
         uint8_t *dst = sm + row * 128 + ((u ^ (row & 7)) << 4);
         *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4 *>(dst + N * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         if (u == 0) q_scale[(w & 1) * N + row] = exp2_int(e);
-      });
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(cta.bar(Lay::kQReady));
+      ++loads;
     };
-    bool here = false;  // this work's Q
+    enum { kNone, kFetched, kSplit } have = kNone;  // this work's Q
     for (uint32_t w = 0; w == 0 || kMany; ++w) {
       const Work d = cta.next_work(w);
       cta.have_read();
       if (d.nrow == 0) break;
       if (d.n == 0 || !ok) continue;
-      if (!here) ok = split(d, w);
-      here = false;
-      // The next work's Q before the last two tiles, where it is known by then and the scores of
-      // this one are done: at its end, with loads of 2000 cycles, all would wait for it.
+      if (have == kNone) fetch(d);
+      if (have != kSplit) {
+        ok = loads == 0 || __all_sync(0xffffffffu, chunk_wait<false>(cta.bar(Lay::kQEmpty),
+                                                                     (loads - 1) & 1, abort_flag));
+        if (!ok) continue;
+        split(w);
+      }
+      have = kNone;
+      // The next work's Q between the last tiles, where it is known by then: fetched, and split
+      // once the scores of this work are done.  At the end all would wait for it, 2000 cycles.
       auto early = [&](int t) {
-        if (!kMany || here || t < d.n - 2 || !cta.passed(Lay::kWorkFull, (w + 1) & 1) ||
-            !cta.passed(Lay::kQEmpty, (loads - 1) & 1))
-          return;
-        const Work e = cta.next_work(w + 1);
-        if (e.n > 0) here = split(e, w + 1);
+        if (!kMany || have == kSplit || t < d.n - 3) return;
+        if (have == kNone && cta.passed(Lay::kWorkFull, (w + 1) & 1)) {
+          const Work e = cta.next_work(w + 1);
+          if (e.n > 0) {
+            fetch(e);
+            have = kFetched;
+          }
+        } else if (have == kFetched && cta.passed(Lay::kQEmpty, (loads - 1) & 1)) {
+          split(w + 1);
+          have = kSplit;
+        }
       };
-      if (ok) ok = widen_tiles(cta, widener, d, at, batches, early);
+      ok = widen_tiles(cta, widener, d, at, batches, early);
     }
   } else if (warp >= 8) {
     regs_less<kFewIssueRegs>();
