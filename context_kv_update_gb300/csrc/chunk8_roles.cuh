@@ -70,17 +70,6 @@ __device__ __forceinline__ uint32_t e4m3_f16x2(uint32_t pair) {
   return r;
 }
 
-// 128 columns in two loads (the compiler takes none of more registers than a thread launches
-// with), one wait.
-__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&r)[128]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%128];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, %96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%129];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31]), "=f"(r[32]), "=f"(r[33]), "=f"(r[34]), "=f"(r[35]), "=f"(r[36]), "=f"(r[37]), "=f"(r[38]), "=f"(r[39]), "=f"(r[40]), "=f"(r[41]), "=f"(r[42]), "=f"(r[43]), "=f"(r[44]), "=f"(r[45]), "=f"(r[46]), "=f"(r[47]), "=f"(r[48]), "=f"(r[49]), "=f"(r[50]), "=f"(r[51]), "=f"(r[52]), "=f"(r[53]), "=f"(r[54]), "=f"(r[55]), "=f"(r[56]), "=f"(r[57]), "=f"(r[58]), "=f"(r[59]), "=f"(r[60]), "=f"(r[61]), "=f"(r[62]), "=f"(r[63]), "=f"(r[64]), "=f"(r[65]), "=f"(r[66]), "=f"(r[67]), "=f"(r[68]), "=f"(r[69]), "=f"(r[70]), "=f"(r[71]), "=f"(r[72]), "=f"(r[73]), "=f"(r[74]), "=f"(r[75]), "=f"(r[76]), "=f"(r[77]), "=f"(r[78]), "=f"(r[79]), "=f"(r[80]), "=f"(r[81]), "=f"(r[82]), "=f"(r[83]), "=f"(r[84]), "=f"(r[85]), "=f"(r[86]), "=f"(r[87]), "=f"(r[88]), "=f"(r[89]), "=f"(r[90]), "=f"(r[91]), "=f"(r[92]), "=f"(r[93]), "=f"(r[94]), "=f"(r[95]), "=f"(r[96]), "=f"(r[97]), "=f"(r[98]), "=f"(r[99]), "=f"(r[100]), "=f"(r[101]), "=f"(r[102]), "=f"(r[103]), "=f"(r[104]), "=f"(r[105]), "=f"(r[106]), "=f"(r[107]), "=f"(r[108]), "=f"(r[109]), "=f"(r[110]), "=f"(r[111]), "=f"(r[112]), "=f"(r[113]), "=f"(r[114]), "=f"(r[115]), "=f"(r[116]), "=f"(r[117]), "=f"(r[118]), "=f"(r[119]), "=f"(r[120]), "=f"(r[121]), "=f"(r[122]), "=f"(r[123]), "=f"(r[124]), "=f"(r[125]), "=f"(r[126]), "=f"(r[127])
-      : "r"(taddr), "r"(taddr + 64)
-      : "memory");
-}
 template <int N>
 __device__ __forceinline__ void regs_more() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -426,39 +415,55 @@ __device__ __forceinline__ void load_tiles(const Cta<Lay> &c, const ChunkParams 
 template <int N>
 __device__ __forceinline__ int split_q(const uint4 (&x)[N / 8], uint32_t (&hi)[N / 4],
                                        uint32_t (&lo)[N / 4]) {
-  float y[N], most = 0.f;
+  // the largest magnitude, on the numbers' bits, two at a time
+  uint32_t most2 = 0u;
 #pragma unroll
   for (int i = 0; i < N / 8; ++i) {
     const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      y[8 * i + 2 * e] = __uint_as_float(v[e] << 16);
-      y[8 * i + 2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
+    for (int e = 0; e < 4; ++e) most2 = __vmaxu2(most2, v[e] & 0x7fff7fffu);
+  }
+  uint32_t most = max(most2 & 0xffffu, most2 >> 16);
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  // Numbers that are not finite become NaN, and the others keep their size.
+  const bool finite = __all_sync(0xffffffffu, most < 0x7f80u);
+  if (!finite) {
+    most = 0;
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) {
+      const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t m = v[e >> 1] >> (16 * (e & 1)) & 0x7fffu;
+        if (m < 0x7f80u) most = max(most, m);
+      }
     }
-  }
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
-    const float a = fabsf(y[e]);
-    if (a < INFINITY) most = fmaxf(most, a);
+    for (int o = 1; o < 8; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
   }
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  const int e = scale8_exponent(most);
+  const int e = scale8_exponent(__uint_as_float(most << 16));
   const float down = exp2_int(-e);
 #pragma unroll
-  for (int i = 0; i < N / 4; ++i) {
-    uint32_t h[2], l[2];
+  for (int i = 0; i < N / 8; ++i) {
+    const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    uint32_t h[4], l[4];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float a = y[4 * i + 2 * j] * down, b = y[4 * i + 2 * j + 1] * down;
-      if (!(fabsf(a) <= 448.f)) a = NAN;
-      if (!(fabsf(b) <= 448.f)) b = NAN;
-      h[j] = e4m3_pair(a, b);
-      const float2 v = e4m3_values(h[j]);
-      l[j] = e4m3_pair(a - v.x, b - v.y);
+    for (int j = 0; j < 4; ++j) {
+      float2 a = mul2(make_float2(__uint_as_float(v[j] << 16), __uint_as_float(v[j] & 0xffff0000u)),
+                      make_float2(down, down));
+      if (!finite) {
+        if (!(fabsf(a.x) <= 448.f)) a.x = NAN;
+        if (!(fabsf(a.y) <= 448.f)) a.y = NAN;
+      }
+      h[j] = e4m3_pair(a.x, a.y);
+      const float2 back = e4m3_values(h[j]);
+      l[j] = e4m3_pair(a.x - back.x, a.y - back.y);
     }
-    hi[i] = h[0] | h[1] << 16;
-    lo[i] = l[0] | l[1] << 16;
+    hi[2 * i] = h[0] | h[1] << 16;
+    hi[2 * i + 1] = h[2] | h[3] << 16;
+    lo[2 * i] = l[0] | l[1] << 16;
+    lo[2 * i + 1] = l[2] | l[3] << 16;
   }
   return e;
 }
@@ -481,7 +486,7 @@ __device__ __forceinline__ void fetch_row(const ChunkParams &p, const Work &d, i
 // in flight.  store(row, u, hi, lo, e) takes a lane's part u of a row.  `loads` works before this
 // one had their Q here.
 template <class Lay, class Store>
-__device__ __forceinline__ bool split_rows(const Cta<Lay> &c, const ChunkParams &p, const Work &d,
+__device__ __forceinline__ bool split_rows(const Cta<Lay> &c, const ChunkParams &p, const Work d,
                                            uint32_t loads, Store store) {
   constexpr int HD = Lay::kHD, kLoads = HD / 64, kAhead = 4;
   const int lane = c.lane, warp = threadIdx.x >> 5, tok0 = d.row0 / p.G, u = lane & 7;

@@ -308,42 +308,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int kb = (t0 + t) * kKT;
         const uint32_t bad = tile.bad;
         const bool cut = !(lo <= kb && hi >= kb + kKT - 1);
-        float sv[128];
-        tmem_ld128(tm_s, sv);
-        if (bad) {
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if ((bad >> (c >> 4)) & 1u) sv[c] = -INFINITY;
-        }
-        if (cut) {
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (kb + c < lo || kb + c > hi) sv[c] = -INFINITY;
-        }
+        // Two passes of 32 scores a step, read from tensor memory each.  (Short loops: unrolled over
+        // the row, the tile's 600 instructions came at three cycles each from a cache that they
+        // share with seven other warps' code.)
         // the factor of 16 keys' scores; never 0, which would make a masked one NaN
-        auto factor = [&](int i) { return fmaxf(row_scale * tile.k[i], 0x1p-126f); };
-        float f[8], tmax = -INFINITY;
+        auto factor = [&](int i) {
+          const float f = row_scale * tile.k[i];
+          return f < 0x1p-126f ? 0x1p-126f : f;
+        };
+        float tmax = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          float s[64];
+          ptx::tmem_ld64f_sync(tm_s + 64 * c, s);
+          if (__any_sync(0xffffffffu, cut) || bad) {  // what the row does not see: -inf, for both passes
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          f[i] = factor(i);
-          float a = fmaxf(sv[16 * i], sv[16 * i + 1]);
+            for (int h = 0; h < 64; h += 32) {
+              const int k0 = kb + 64 * c + h, from = max(lo - k0, 0), to = min(hi - k0, 31);
+              uint32_t vis = from <= to ? (0xffffffffu >> (31 - to + from)) << from : 0u;
+              if (bad >> (4 * c + h / 16) & 1u) vis &= 0xffff0000u;
+              if (bad >> (4 * c + h / 16) & 2u) vis &= 0x0000ffffu;
+              uint32_t w[32];
 #pragma unroll
-          for (int c = 2; c < 16; c += 2) a = fmaxf(fmaxf(a, sv[16 * i + c]), sv[16 * i + c + 1]);
-          tmax = fmaxf(tmax, a * f[i]);
+              for (int e = 0; e < 32; ++e) {
+                if (!(vis >> e & 1u)) s[h + e] = -INFINITY;
+                w[e] = __float_as_uint(s[h + e]);
+              }
+              tmem_st32(tm_s + 64 * c + h, w);
+            }
+            ptx::tmem_wait_st();
+          }
+#pragma unroll
+          for (int i = 0; i < 64; i += 16) {
+            float a = fmaxf(s[i], s[i + 1]), a2 = fmaxf(s[i + 2], s[i + 3]);
+#pragma unroll
+            for (int e = 4; e < 16; e += 4) {
+              a = fmaxf(fmaxf(a, s[i + e]), s[i + e + 1]);
+              a2 = fmaxf(fmaxf(a2, s[i + e + 2]), s[i + e + 3]);
+            }
+            tmax = fmaxf(tmax, fmaxf(a, a2) * factor(4 * c + i / 16));
+          }
         }
-        const int grown = tile.E - E;
-        float corr = 1.f, corr_o = 1.f;
+        float corr = 1.f;
         if (m_ref == -INFINITY) {
           m_ref = tmax;
         } else if (tmax > m_ref + 8.f) {
           corr = ptx::ex2(m_ref - tmax);
           m_ref = tmax;
         }
-        corr_o = corr * ptx::ex2(static_cast<float>(-grown));
-        E = tile.E;
         // the group's previous product completed before this S did
-        if (t >= step && __any_sync(0xffffffffu, corr_o != 1.f)) {
-          for (int c = 0; c < HD; c += 16) {
+        if (__any_sync(0xffffffffu, corr != 1.f || tile.E != E)) {
+          const float corr_o = corr * ptx::ex2(static_cast<float>(E - tile.E));
+          E = tile.E;
+          l *= corr;
+#pragma unroll 1
+          for (int c = 0; c < HD && t >= step; c += 16) {
             uint32_t ov[16];
             ptx::tmem_ld16_sync(tm_o + c, ov);
 #pragma unroll
@@ -356,32 +375,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool far = tile.far != 0;
         const float2 nm2 = make_float2(nm, nm);
         float2 sum[2] = {};
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 2; ++c) {
+          float s[64];
+          ptx::tmem_ld64f_sync(tm_s + 64 * c, s);
+          uint32_t pk[32];
 #pragma unroll
-          for (int x = 64 * c; x < 64 * c + 64; x += 2) {
-            const float2 f2 = make_float2(f[x / 16], f[x / 16]);
-            float2 w = fma2(make_float2(sv[x], sv[x + 1]), f2, nm2);
+          for (int x = 0; x < 64; x += 2) {
+            const float f = factor(4 * c + x / 16);
+            float2 w = fma2(make_float2(s[x], s[x + 1]), make_float2(f, f), nm2);
             w.x = ptx::ex2(w.x);
             w.y = ptx::ex2(w.y);
             sum[x / 2 & 1] = add2(sum[x / 2 & 1], w);
-            sv[x] = w.x;
-            sv[x + 1] = w.y;
+            s[x] = w.x;
+            s[x + 1] = w.y;
           }
-          uint32_t pk[32];
           if (far) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              pk[e] = ptx::pack_bf16x2(sv[64 * c + 2 * e], sv[64 * c + 2 * e + 1]);
+            for (int e = 0; e < 32; ++e) pk[e] = ptx::pack_bf16x2(s[2 * e], s[2 * e + 1]);
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              pk[e] = pack_f16x2(sv[64 * c + 2 * e], sv[64 * c + 2 * e + 1]);
+            for (int e = 0; e < 32; ++e) pk[e] = pack_f16x2(s[2 * e], s[2 * e + 1]);
           }
           tmem_st32(tm_s + 32 * c, pk);
         }
         sum[0] = add2(sum[0], sum[1]);
-        l = l * corr + (sum[0].x + sum[0].y);
+        l += sum[0].x + sum[0].y;
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
@@ -486,11 +505,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                   make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
           }
         } else if (any) {
-          float4 *dst = reinterpret_cast<float4 *>(
-              p.ws_o + ((orow * p.hq + h) * p.S + seg) * HD + d0 + c);
+          float *dst = p.ws_o + ((orow * p.hq + h) * p.S + seg) * HD + d0 + c;
+          if ((reinterpret_cast<uintptr_t>(p.ws_o) & 31) == 0) {
+            uint32_t w[32];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e]);
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) store_32b(dst + e, w + e);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4 *>(dst + e) =
+                  make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
         }
       }
       ptx::tc_fence_before();
