@@ -1,5 +1,5 @@
-// chunk8_roles.cuh -- what the kernels of chunk_attention8.cu and chunk_attention8_few.cu share: the
-// warps that find the work, look up scales and load tiles, the split of Q, the widening of V.
+// chunk8_roles.cuh -- what the kernels of chunk_attention8.cu and chunk_attention8_few.cu share:
+// the warps that find the work, look up scales and load tiles, the split of Q, V's widening.
 #pragma once
 
 #include "cache8.cuh"
@@ -14,10 +14,10 @@ cudaError_t launch_attn8_few(int shift, const CUtensorMap &tm, const ChunkParams
 
 namespace {
 
-
 constexpr int kThreads = 512;
-// Registers: 512 threads launch with 128 each; the softmax groups take more (a row's 128 scores),
-// the others give them up: 2 x 128 x 184 + 128 x 64 + 128 x 80 = 65536.
+// Registers: 512 threads launch with 128 each; the softmax groups take more (64 scores, or as many
+// results, beside a work's state), the others give them up: 2 x 128 x 184 + 128 x 64 + 128 x 80 =
+// 65536.
 constexpr int kSoftmaxRegs = 184, kIssueRegs = 64, kWidenRegs = 80;
 static_assert(256 * kSoftmaxRegs + 128 * (kIssueRegs + kWidenRegs) <= kThreads * 128, "");
 constexpr int kWidenTeam = 4;  // warps that widen a tile of V
@@ -381,7 +381,7 @@ __device__ __forceinline__ void load_tiles(const Cta<Lay> &c, const ChunkParams 
         int bar = kEmpty + ring.slot;
         uint32_t phase = ring.phase;
         bool used = true;
-        if (!kV && Lay::kScores == 4) {  // the scores are done: one barrier tells who waits for them too
+        if (!kV && Lay::kFew) {  // the scores are done: the barrier that tells the softmax
           const int before = loaded - kSlots;
           used = before >= 0;
           bar = Lay::kSFull + (before & 3);
@@ -475,7 +475,8 @@ __device__ __forceinline__ void fetch_row(const ChunkParams &p, const Work &d, i
 #pragma unroll
   for (int i = 0; i < HD / 64; ++i) x[i] = make_uint4(0, 0, 0, 0);
   if (row >= d.nrow) return;
-  const int f = d.row0 - tok0 * p.G + row, tok = p.G == 1 ? f : static_cast<int>(__umulhi(f, p.g_inv));
+  const int f = d.row0 - tok0 * p.G + row;
+  const int tok = p.G == 1 ? f : static_cast<int>(__umulhi(f, p.g_inv));
   const uint16_t *src = p.q + (d.a + tok0 + tok) * p.qs +
                         static_cast<int64_t>(d.kvh * p.G + f - tok * p.G) * HD + u * (HD / 8);
 #pragma unroll
@@ -552,7 +553,8 @@ struct Widener {
         if (i == 2) f = (v1 & 0xffffu) * 0x10001u;
         uint4 x[kSub];
 #pragma unroll
-        for (int e = 0; e < kSub; ++e) x[e] = *reinterpret_cast<const uint4 *>(src + from[e] + i * 8 * Lay::kHD);
+        for (int e = 0; e < kSub; ++e)
+          x[e] = *reinterpret_cast<const uint4 *>(src + from[e] + i * 8 * Lay::kHD);
 #pragma unroll
         for (int e = 0; e < kSub; ++e) {
           const uint32_t c[4] = {x[e].x, x[e].y, x[e].z, x[e].w};

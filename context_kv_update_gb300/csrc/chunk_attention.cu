@@ -881,7 +881,8 @@ int tile_shift(const dflash_geom &g, int B, int n_rows) { return pair_form(g, B,
 // 16384 keys 162 with one segment, 105 with two, 124 with three; over up to 2048 keys 31
 // and 32 with two; one token over 32768 keys 33 with 19).
 int chunk_attention_num_segments(const dflash_geom &g, int B, int n_rows, int window) {
-  return segments_of(g, B, n_rows, window, tile_shift(g, B, n_rows), 7.0, 3.0, 1.5);
+  const int shift = tile_shift(g, B, n_rows);
+  return segments_of(g, B, n_rows, window, shift, chunk_tiles(g, B, n_rows, shift), 7.0, 3.0, 1.5);
 }
 
 size_t chunk_attention_workspace_bytes(const dflash_geom &g, int B, int n_rows, int S) {
@@ -895,8 +896,8 @@ cudaError_t launch_chunk_attention(const dflash_geom &g, int B, int layer, int n
                                    const int32_t *kv, int32_t window, const float *sinks,
                                    float scale, int mask_mode, int S, void *ws, void *out,
                                    int64_t out_stride, int32_t *st, cudaStream_t s) {
-  ChunkParams p = chunk_params(g, tile_shift(g, B, n_rows), B, layer, n_rows, q, q_stride, tbl, cu, ctx, kv, window, sinks,
-                               scale, mask_mode, S, ws, out, out_stride, st);
+  ChunkParams p = chunk_params(g, tile_shift(g, B, n_rows), B, layer, n_rows, q, q_stride, tbl, cu,
+                               ctx, kv, window, sinks, scale, mask_mode, S, ws, out, out_stride, st);
   CUtensorMap tm;
   const uint64_t pool_rows = static_cast<uint64_t>(g.num_layers) * g.num_pool_pages * 2 * g.nkv *
                              static_cast<uint64_t>(g.page_size);

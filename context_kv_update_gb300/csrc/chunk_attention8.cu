@@ -17,10 +17,17 @@
 // than that, and all tiles after it, are widened to bf16 with the scale itself instead, and E
 // is 0: a power of two times four bits is a bf16 number.
 //
-// Four warpgroups, 128 registers a thread: warps 0-3 and 4-7 softmax, 8 finds the CTA's next work
-// tile, 9 looks up scales (four key tiles at a time, a ring of its own), 10 issues the loads of K
-// and V, 11 every product, 12-15 split Q and widen V.  A row's 128 scores are read from tensor
-// memory twice, 64 at a time: once for the maximum, once for the weights.
+// Four warpgroups, 128 registers a thread: warps 0-3 and 4-7 split Q, then softmax; 8 loads V; 9
+// finds the CTA's next work tile and looks up its scales (four key tiles at a time, a ring of their
+// own); 10 loads K; 11 issues every product; 12-15 widen V.  A row's 128 scores are read from
+// tensor memory twice, 64 at a time: once for the maximum, once for the weights.
+//
+// What bounds it: for each group a chain of products (16 of 64 cycles, as many as in 16 bits: half
+// the time an operand's, twice the operands), their latency (450), the softmax (1700) and its
+// way back (450); two groups fill the tensor cores to about a half.  1024 rows behind 32768 keys,
+// 32 heads of 128 over 8: 550 us, 1.02 PFLOP/s of the 558 GFLOP that attention is.  A quarter of
+// the softmax warps' time goes to the instruction cache: unrolled over a row's 128 scores, with
+// no other change, 8 drafts of 16 tokens over up to 16384 keys took 90 us, so 74.
 #include "chunk8_roles.cuh"
 
 namespace dflash {
@@ -32,7 +39,7 @@ template <int HD, bool kPairs>
 struct Layout8 : Bars<HD == 64 ? 6 : kPairs ? 3 : 4, HD == 64 ? 4 : kPairs ? 2 : 3, 2, 2> {
   using B = Bars<HD == 64 ? 6 : kPairs ? 3 : 4, HD == 64 ? 4 : kPairs ? 2 : 3, 2, 2>;
   static constexpr int kHD = HD, kShift = kPairs ? 8 : 7, kWideners = 4;
-  static constexpr bool kPair = kPairs;
+  static constexpr bool kPair = kPairs, kFew = false;
   static constexpr uint32_t kTile = kKT * HD, kTile16 = 2 * kTile;
   static constexpr uint32_t kK = (kPair ? 2 : 1) * kTile16;
   static constexpr uint32_t kV = kK + B::kKs * kTile;
@@ -52,7 +59,8 @@ struct Layout8 : Bars<HD == 64 ? 6 : kPairs ? 3 : 4, HD == 64 ? 4 : kPairs ? 2 :
 template <int HD, bool kPair, bool kMany>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_attn8_kernel(const __grid_constant__ CUtensorMap tm,
-                       const __grid_constant__ ChunkParams p, const __grid_constant__ Cache8 cache) {
+                       const __grid_constant__ ChunkParams p,
+                       const __grid_constant__ Cache8 cache) {
   using Lay = Layout8<HD, kPair>;
   constexpr int kKs = Lay::kKs, kWides = Lay::kWides;
   extern __shared__ uint8_t smem_raw[];
@@ -112,7 +120,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
     // ------------------------------------------------ MMA issuer
     constexpr uint32_t idesc_qk = idesc_of(128, kKT, 0, false);
-    constexpr uint32_t idesc_f16 = idesc_of(128, HD, 0, true), idesc_bf16 = idesc_of(128, HD, 1, true);
+    constexpr uint32_t idesc_f16 = idesc_of(128, HD, 0, true),
+                       idesc_bf16 = idesc_of(128, HD, 1, true);
     // warp-uniform copies
     const uint32_t tm0 = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t base = __shfl_sync(0xffffffffu, sm0, 0);
@@ -275,7 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (u == 0) q_scale[(wk & 1) * 256 + row] = exp2_int(e);
         });
         if (ok)
-          ok = __all_sync(0xffffffffu, chunk_wait<false>(cta.bar(Lay::kQReady), loads & 1, abort_flag));
+          ok = __all_sync(0xffffffffu,
+                          chunk_wait<false>(cta.bar(Lay::kQReady), loads & 1, abort_flag));
         ++loads;
         if (ok && real) row_scale = q_scale[(wk & 1) * 256 + rt] * p.scale_log2;
       }
@@ -308,9 +318,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int kb = (t0 + t) * kKT;
         const uint32_t bad = tile.bad;
         const bool cut = !(lo <= kb && hi >= kb + kKT - 1);
-        // Two passes of 32 scores a step, read from tensor memory each.  (Short loops: unrolled over
-        // the row, the tile's 600 instructions came at three cycles each from a cache that they
-        // share with seven other warps' code.)
+        // Two passes of 64 scores a step, read from tensor memory each.  (Short loops: the tile's
+        // 600 instructions, unrolled over the row, come at three cycles each, from a cache that
+        // they share with the other warps' code.  32 a step: 1024 rows behind 32768 keys 591 us
+        // instead of 550, for the loads' latency.)
         // the factor of 16 keys' scores; never 0, which would make a masked one NaN
         auto factor = [&](int i) {
           const float f = row_scale * tile.k[i];
@@ -321,7 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 2; ++c) {
           float s[64];
           ptx::tmem_ld64f_sync(tm_s + 64 * c, s);
-          if (__any_sync(0xffffffffu, cut) || bad) {  // what the row does not see: -inf, for both passes
+          // what the row does not see: -inf, for both passes
+          if (__any_sync(0xffffffffu, cut) || bad) {
 #pragma unroll
             for (int h = 0; h < 64; h += 32) {
               const int k0 = kb + 64 * c + h, from = max(lo - k0, 0), to = min(hi - k0, 31);
@@ -412,8 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------- epilogue
       const bool had0 = n > 0, had1 = split ? n > 1 : n > 0;  // groups with products
       if (ok && (g ? had1 : had0)) {
-        ok = __all_sync(0xffffffffu, chunk_wait<false>(cta.bar(Lay::kODone + g), (g ? outs1 : outs0) & 1,
-                                                       abort_flag));
+        ok = __all_sync(0xffffffffu, chunk_wait<false>(cta.bar(Lay::kODone + g),
+                                                       (g ? outs1 : outs0) & 1, abort_flag));
         ptx::tc_fence_after();
       }
       if (split && ok && (g ? had0 : had1)) {  // the other group's products
@@ -563,8 +575,10 @@ cudaError_t launch_main(bool pair, const CUtensorMap &tm, const ChunkParams &p,
               : launch_form<HD, false, false>(tm, p, cache, grid, s);
 }
 
-// Rows of a work tile, as a power of two.  Heads of 128 whose mean request has few rows take the
-// kernel of chunk_attention8_few.cu.
+// Rows of a work tile, as a power of two.  Heads of 128 whose mean request has at most 32 rows take
+// the kernel of chunk_attention8_few.cu: 64 single tokens of 4 rows a head over up to 8192 keys
+// take 131 us there, 219 here with a row a softmax thread; 8 drafts of 64 rows 120 there (two works
+// of 32 rows read the same keys), 74 here.
 int tile_shift(const dflash_geom &g, int B, int n_rows) {
   const int64_t rows = static_cast<int64_t>(n_rows) * (g.hq / g.nkv);
   if (g.head_dim == 128 && rows <= 32LL * B)
@@ -575,7 +589,15 @@ int tile_shift(const dflash_geom &g, int B, int n_rows) {
 }  // namespace
 
 int chunk_attention8_num_segments(const dflash_geom &g, int B, int n_rows, int window) {
-  return segments_of(g, B, n_rows, window, tile_shift(g, B, n_rows), 7.0, 3.0, 1.5);
+  // Work tiles as if the requests had a mean's rows each (the most there can be is one more a
+  // request: 16 requests of 16 tokens over up to 8192 keys took 102 us uncut for it, 83 in two).
+  // Where a work begins and ends the key stream stops: ten to twelve tiles' time.
+  const int shift = tile_shift(g, B, n_rows);
+  const int64_t flat = static_cast<int64_t>(n_rows) * (g.hq / g.nkv);
+  const int64_t per = static_cast<int64_t>(B) << shift;
+  const int64_t tiles = (flat + per - 1) / per * B;
+  return shift <= kMostFewShift ? segments_of(g, B, n_rows, window, shift, tiles, 10.0, 2.0, 0.7)
+                                : segments_of(g, B, n_rows, window, shift, tiles, 12.0, 2.0, 1.0);
 }
 
 size_t chunk_attention8_workspace_bytes(const dflash_geom &g, int B, int n_rows, int S) {
@@ -590,8 +612,8 @@ cudaError_t launch_chunk_attention8(const dflash_geom &g, int B, int layer, int 
                                     float scale, int mask_mode, int S, void *ws, void *out,
                                     int64_t out_stride, int32_t *st, cudaStream_t s) {
   const int shift = tile_shift(g, B, n_rows);
-  const ChunkParams p = chunk_params(g, shift, B, layer, n_rows, q, q_stride, tbl, cu, ctx, kv, window,
-                                     sinks, scale, mask_mode, S, ws, out, out_stride, st);
+  const ChunkParams p = chunk_params(g, shift, B, layer, n_rows, q, q_stride, tbl, cu, ctx, kv,
+                                     window, sinks, scale, mask_mode, S, ws, out, out_stride, st);
   CUtensorMap tm;
   const uint64_t rows = static_cast<uint64_t>(g.num_layers) * g.num_pool_pages * 2 * g.nkv *
                         static_cast<uint64_t>(g.page_size);

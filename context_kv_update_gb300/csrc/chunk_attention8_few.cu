@@ -1,5 +1,5 @@
 // chunk_attention8_few.cu -- attention over a cache held in 8 bits where a work tile has few rows
-// (at most 64 of a token and head; single tokens, short drafts) and the key stream is the work.
+// (at most 32 of a token and head; single tokens, short drafts) and the key stream is the work.
 //
 // The kernel of chunk_attention8.cu with the products turned round: the 128 keys of a tile are
 // the rows of both results' operands, S^T = K Q^T and O^T = V^T P^T.  The tensor cores then do
@@ -13,30 +13,36 @@
 // the accumulators (as a rule with its first tile alone).  A row's sum stays in the threads,
 // each its keys', until the end.
 //
-// Bound by HBM: see the launcher.
+// What bounds it: a key tile takes the chain of warps about 1400 cycles, HBM 1310 (32 KB at 6.8
+// TB/s over 152 SMs); where a work ends and the next begins the stream stops for 4 to 6 us,
+// and a launch takes 7 us to its first weights.  64 single tokens over up to 8192 keys, 32 heads of
+// 128 over 8: 131 us, 4.7 TB/s; one token over 32768: 23.7 us.
 #include "chunk8_roles.cuh"
 
 namespace dflash {
 namespace {
 
-// 20 warps: as in chunk_attention8.cu, but eight that widen V.  640 threads launch with 96
-// registers each: 256 x 128 + 128 x 64 + 256 x 80 = 640 x 96.
+// 20 warps: as in chunk_attention8.cu, but eight that split Q and widen V, a team of four a tile
+// (all eight on each tile: 141 us instead of 133 for 64 single tokens over up to 8192 keys).  640
+// threads launch with 96 registers each: 256 x 128 + 128 x 64 + 256 x 80 = 640 x 96.
 constexpr int kFewThreads = 640;
 // A row's weights carry 2^4 and may exceed its reference by 2^11 more: fp16 holds 2^15, and its
 // smallest step is 2^-28 of the reference's weight.
 constexpr float kFewLift = 4.f, kFewLag = 11.f;
 constexpr int kFewSoftmaxRegs = 128, kFewIssueRegs = 64, kFewWidenRegs = 80;
-static_assert(256 * (kFewSoftmaxRegs + kFewWidenRegs) + 128 * kFewIssueRegs <= kFewThreads * 96, "");
+static_assert(256 * (kFewSoftmaxRegs + kFewWidenRegs) + 128 * kFewIssueRegs <= kFewThreads * 96,
+              "");
 
 template <int N>
 struct LayoutFew : Bars<3, N == 16 ? 4 : 3, 3, 4> {
   using B = Bars<3, N == 16 ? 4 : 3, 3, 4>;
   static constexpr int kHD = 128, kShift = N == 16 ? 4 : 5, kWideners = 8;
+  static constexpr bool kFew = true;
   static constexpr uint32_t kTile = kKT * kHD, kTile16 = 2 * kTile;
   static constexpr uint32_t kK = 2 * N * 128;  // Q: N rows of hi, N of lo
   static constexpr uint32_t kV = kK + B::kKs * kTile;
   static constexpr uint32_t kWide = kV + B::kVs * kTile;
-  static constexpr uint32_t kP = kWide + B::kWides * kTile16;  // of each group: 128 keys of N weights
+  static constexpr uint32_t kP = kWide + B::kWides * kTile16;  // a group's: 128 keys of N weights
   static constexpr uint32_t kRowState = kP + 2 * kKT * 2 * N;
   static constexpr uint32_t kMeta = kRowState + (2 * N + 2 * N * 11 + 12) * 4;
   static constexpr uint32_t kSortTiles = kMeta + kMetaBatch * kMetaBatches * sizeof(TileMeta);
@@ -294,15 +300,15 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const int g = warp >> 2, w4 = warp & 3;
     const int tid = threadIdx.x & 127;  // TMEM lane = key of the tile, at the end a dim
     const uint32_t lane_off = static_cast<uint32_t>(w4 * 32) << 16;
-    // a group's rows: lo, hi, factor, kFewLift - reference, scaling; the warps' maxima [4]; reference,
-    // what was added to the scores; of both groups, units of the accumulators; rows that moved, and
-    // that have no reference
+    // a group's rows: lo, hi, factor, what is added to the scores (kFewLift - reference, or 0
+    // without one), scaling; the warps' maxima, then sums [4]; reference, the last change of what
+    // is added; of both groups: units of the accumulators; rows that moved, and without a reference
     float *rows = q_scale + 2 * N + g * 11 * N;
     int *row_lo = reinterpret_cast<int *>(rows), *row_hi = row_lo + N;
     float *row_f = rows + 2 * N, *row_nm = rows + 3 * N, *row_corr = rows + 4 * N,
           *part = rows + 5 * N, *row_m = rows + 9 * N, *row_delta = rows + 10 * N;
     float *units = q_scale + 2 * N + 22 * N;
-    uint32_t *marks = reinterpret_cast<uint32_t *>(units) + 4 + 4 * g;  // of the groups' accumulators
+    uint32_t *marks = reinterpret_cast<uint32_t *>(units) + 4 + 4 * g;
     int batches = 0;
     int at = 0;  // tiles before this work
     uint32_t loads = 0u, outs0 = 0u, outs1 = 0u;  // of q_ready, o_done
@@ -374,7 +380,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         const bool cut = !(all_lo <= kb && all_hi >= kb + kKT - 1);
         const bool far = tile.far != 0;
         float y[N] = {};
-        if (got) {  // scores, in powers of two: relative to the rows' references where they have one
+        if (got) {  // scores, in powers of two, relative to the rows' references (if they have one)
           float low[N];
           tmem_ld<N>(tm_s, y);
           tmem_ld<N>(tm_s + N, low);

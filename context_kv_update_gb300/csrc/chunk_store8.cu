@@ -510,10 +510,12 @@ __global__ void __launch_bounds__(256) chunk_read8_kernel(const __grid_constant_
         if (y == 0) raise_status(p.st, DFLASH_DEV_BAD_PAGE);
         continue;
       }
-      const int kv = p.sides == 1 ? (p.out[0] ? 0 : 1) : y >= p.vecs, c = y - (p.sides == 2 && kv ? p.vecs : 0);
+      const int kv = p.sides == 1 ? (p.out[0] ? 0 : 1) : y >= p.vecs;
+      const int c = y - (p.sides == 2 && kv ? p.vecs : 0);
       const int h = c / head;
       to[i] = p.out[kv] + t * p.stride[kv] + 16 * c;
-      codes[i] = __ldcs(reinterpret_cast<const uint4 *>(p.cache.code(pg, kv, h, sl)) + (c - h * head));
+      codes[i] =
+          __ldcs(reinterpret_cast<const uint4 *>(p.cache.code(pg, kv, h, sl)) + (c - h * head));
       scale[i] = *p.cache.scale(pg, kv, h, sl);
     }
 #pragma unroll

@@ -443,11 +443,11 @@ inline int tail_tiles(const dflash_geom &g, int B, int n_rows, int shift) {
   return idle == 0 ? 1 : static_cast<int>(std::min<int64_t>((works + idle - 1) / idle, 64));
 }
 
-// `fixed`: what a CTA costs beside its key tiles, `merge`: what the second launch does, both in
-// key tiles, of `tile_us` each where few rows stream them.
-inline int segments_of(const dflash_geom &g, int B, int n_rows, int window, int shift, double fixed,
-                       double merge, double tile_us) {
-  const double ctas = static_cast<double>(chunk_tiles(g, B, n_rows, shift)) * g.nkv;
+// `tiles`: work tiles expected; `fixed`: what a CTA costs beside its key tiles, `merge`: what the
+// second launch does, both in key tiles, of `tile_us` each where few rows stream them.
+inline int segments_of(const dflash_geom &g, int B, int n_rows, int window, int shift,
+                       int64_t tiles, double fixed, double merge, double tile_us) {
+  const double ctas = static_cast<double>(tiles) * g.nkv;
   const double sms = device_sm_count();
   double longest = static_cast<double>(g.max_pages) * g.page_size / kKT;
   if (window > 0) longest = std::min(longest, (static_cast<double>(window) + n_rows) / kKT + 1.0);
