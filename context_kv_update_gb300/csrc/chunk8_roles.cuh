@@ -32,7 +32,8 @@ struct __align__(16) TileMeta {
   uint32_t v[8];  // V's: an fp16 factor, the scale byte << 16, 1 << 24 where the keys are there
   int E;          // the tile's weights times V give units of 2^E
   int far;        // bf16 instead of fp16 (E = 0)
-  int bad;        // bits of the 16 keys each that are visible on a page outside the pool
+  int bad;        // bits of the 16 keys each that are visible on a page outside the pool, then
+                  // (bits 8 to 15) of those whose K has a scale of NaN
   int pad;
 };
 
@@ -231,6 +232,7 @@ __device__ __forceinline__ bool look_up_scales(const Cta<Lay> &c, const ChunkPar
       }
     }
     const uint32_t bad = __ballot_sync(0xffffffffu, page == -1);
+    const uint32_t nans = __ballot_sync(0xffffffffu, page >= 0 && kb == 255u);
     any_bad |= bad != 0;
     TileMeta &m = c.meta[batches % kMetaBatches * kMetaBatch + mine];
     m.k[lane & 7] = page >= 0 ? scale8_value(kb) : 1.f;
@@ -240,7 +242,7 @@ __device__ __forceinline__ bool look_up_scales(const Cta<Lay> &c, const ChunkPar
     if ((lane & 7) == 0) {
       m.E = my_E;
       m.far = my_far;
-      m.bad = static_cast<int>(bad >> (8 * mine) & 255u);
+      m.bad = static_cast<int>((bad >> (8 * mine) & 255u) | (nans >> (8 * mine) & 255u) << 8);
     }
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(c.bar(Lay::kMFull + batches % kMetaBatches));

@@ -322,11 +322,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 600 instructions, unrolled over the row, come at three cycles each, from a cache that
         // they share with the other warps' code.  32 a step: 1024 rows behind 32768 keys 591 us
         // instead of 550, for the loads' latency.)
-        // the factor of 16 keys' scores; never 0, which would make a masked one NaN
-        auto factor = [&](int i) {
-          const float f = row_scale * tile.k[i];
-          return f < 0x1p-126f ? 0x1p-126f : f;
-        };
+        // the factor of 16 keys' scores; never 0 or NaN, which would make a masked one NaN
+        auto factor = [&](int i) { return fmaxf(row_scale * tile.k[i], 0x1p-126f); };
         float tmax = -INFINITY;
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
@@ -338,11 +335,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int h = 0; h < 64; h += 32) {
               const int k0 = kb + 64 * c + h, from = max(lo - k0, 0), to = min(hi - k0, 31);
               uint32_t vis = from <= to ? (0xffffffffu >> (31 - to + from)) << from : 0u;
-              if (bad >> (4 * c + h / 16) & 1u) vis &= 0xffff0000u;
-              if (bad >> (4 * c + h / 16) & 2u) vis &= 0x0000ffffu;
+              const uint32_t groups = bad >> (4 * c + h / 16);  // bits 0 and 1: the 32 keys'
+              if (groups & 1u) vis &= 0xffff0000u;
+              if (groups & 2u) vis &= 0x0000ffffu;
+              const uint32_t nans =
+                  (groups & 256u ? 0xffffu : 0u) | (groups & 512u ? 0xffff0000u : 0u);
               uint32_t w[32];
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
+                if (nans >> e & 1u) s[h + e] = NAN;
                 if (!(vis >> e & 1u)) s[h + e] = -INFINITY;
                 w[e] = __float_as_uint(s[h + e]);
               }

@@ -461,6 +461,27 @@ def test_attention_stale_scales_and_codes(dl):  # noqa: F811
         run_attn8(dl, pb, **kw, block=block, S=S, cache=(codes, scales), window=40, causal=False)
 
 
+@pytest.mark.parametrize("kv", [0, 1])
+@pytest.mark.parametrize("hd,rows", [(64, 40), (128, 4), (128, 7), (128, 40), (128, 90)])
+def test_attention_scale_of_nan(dl, hd, rows, kv):  # noqa: F811
+    """A scale of 255 among finite codes: NaN for the rows that see the block, and nothing for the
+    requests (and, K's, for the rows) that do not."""
+    rng = np.random.default_rng(35)
+    kw = dict(hq=4, nkv=1, hd=hd, P=16)
+    pb = attn_problem(rng, [rows, rows], [150, 150], **kw)
+    codes, scales = chunk8.quantise(pb["pool"], 16)
+    want = run_attn8(dl, pb, **kw, check=False, cache=(codes, scales))
+    broken = scales.copy()
+    at = 150 + rows // 2   # the block of the middle row's own key: seen from its first slot on
+    broken[0, pb["table"][1, at // 16], kv] = 255
+    got = run_attn8(dl, pb, **kw, check=False, cache=(codes, broken))
+    np.testing.assert_array_equal(got[:rows], want[:rows])
+    sees = np.maximum(at // 16 * 16 - 150, 0)
+    assert np.all(np.isnan(got[rows + sees:]))
+    if kv == 0:
+        np.testing.assert_array_equal(got[rows:rows + sees], want[rows:rows + sees])
+
+
 def test_attention_extreme_scores(dl):  # noqa: F811
     rng = np.random.default_rng(16)
     hq, nkv, hd, P = 4, 2, 64, 16
