@@ -25,9 +25,9 @@
 // What bounds it: for each group a chain of products (16 of 64 cycles, as many as in 16 bits: half
 // the time an operand's, twice the operands), their latency (450), the softmax (1700) and its
 // way back (450); two groups fill the tensor cores to about a half.  1024 rows behind 32768 keys,
-// 32 heads of 128 over 8: 550 us, 1.02 PFLOP/s of the 558 GFLOP that attention is.  A quarter of
-// the softmax warps' time goes to the instruction cache: unrolled over a row's 128 scores, with
-// no other change, 8 drafts of 16 tokens over up to 16384 keys took 90 us, so 74.
+// 32 heads of 128 over 8: 550 us, 1.02 PFLOP/s of the 558 GFLOP that attention is.  The
+// softmax stays in short loops for the instruction cache: unrolled over a row's 128 scores, with no
+// other change, 8 drafts of 16 tokens over up to 16384 keys took 90 us, so 74.
 #include "chunk8_roles.cuh"
 
 namespace dflash {

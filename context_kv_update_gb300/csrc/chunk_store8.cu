@@ -128,8 +128,8 @@ __global__ void __launch_bounds__(128)
 //
 // Q.  A CTA takes 16 pieces, each as many heads of a row as a warp holds.
 //
-// Bound by HBM: 8192 rows of 32 + 8 + 8 heads of 128 are 184 MB with their codes and take 53 us, 3.5
-// TB/s: q alone 29 us (134 MB), k and v alone 29 (50 MB, a window of rows a CTA).
+// Bound by HBM: 8192 rows of 32 + 8 + 8 heads of 128 are 184 MB with their codes and take 54 us, 3.4
+// TB/s: q alone 29 us (134 MB), k and v alone 31 (50 MB, a window of rows a CTA).
 constexpr int kQPieces = 16;
 
 struct Store8Fast {
