@@ -417,55 +417,62 @@ __device__ __forceinline__ void load_tiles(const Cta<Lay> &c, const ChunkParams 
 template <int N>
 __device__ __forceinline__ int split_q(const uint4 (&x)[N / 8], uint32_t (&hi)[N / 4],
                                        uint32_t (&lo)[N / 4]) {
-  // the largest magnitude, on the numbers' bits, two at a time
-  uint32_t most2 = 0u;
+  constexpr int kWords = N / 2;
+  uint32_t v[kWords];
 #pragma unroll
   for (int i = 0; i < N / 8; ++i) {
-    const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) most2 = __vmaxu2(most2, v[e] & 0x7fff7fffu);
+    v[4 * i] = x[i].x;
+    v[4 * i + 1] = x[i].y;
+    v[4 * i + 2] = x[i].z;
+    v[4 * i + 3] = x[i].w;
   }
-  uint32_t most = max(most2 & 0xffffu, most2 >> 16);
+  // the largest magnitude, on the numbers' bits, two at a time
+  auto largest = [&] {
+    uint32_t two = 0u;
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-  // Numbers that are not finite become NaN, and the others keep their size.
-  const bool finite = __all_sync(0xffffffffu, most < 0x7f80u);
-  if (!finite) {
-    most = 0;
-#pragma unroll
-    for (int i = 0; i < N / 8; ++i) {
-      const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t m = v[e >> 1] >> (16 * (e & 1)) & 0x7fffu;
-        if (m < 0x7f80u) most = max(most, m);
-      }
-    }
+    for (int i = 0; i < kWords; ++i) two = __vmaxu2(two, v[i] & 0x7fff7fffu);
+    uint32_t most = max(two & 0xffffu, two >> 16);
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    return most;
+  };
+  uint32_t most = largest();
+  uint32_t lost[kWords / 4] = {};  // bits of the numbers that are not finite: NaN, and no size
+  const bool finite = __all_sync(0xffffffffu, most < 0x7f80u);
+  if (!finite) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if ((v[i] >> (16 * h) & 0x7fffu) >= 0x7f80u) {
+          lost[i / 4] |= 1u << (2 * (i % 4) + h);
+          v[i] &= h ? 0xffffu : 0xffff0000u;
+        }
+    most = largest();
   }
   const int e = scale8_exponent(__uint_as_float(most << 16));
   const float down = exp2_int(-e);
 #pragma unroll
-  for (int i = 0; i < N / 8; ++i) {
-    const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    uint32_t h[4], l[4];
+  for (int i = 0; i < kWords; i += 2) {
+    uint32_t h[2], l[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float2 a = mul2(make_float2(__uint_as_float(v[j] << 16), __uint_as_float(v[j] & 0xffff0000u)),
-                      make_float2(down, down));
-      if (!finite) {
-        if (!(fabsf(a.x) <= 448.f)) a.x = NAN;
-        if (!(fabsf(a.y) <= 448.f)) a.y = NAN;
-      }
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t w = v[i + j];
+      const float2 a = mul2(make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)),
+                            make_float2(down, down));
       h[j] = e4m3_pair(a.x, a.y);
       const float2 back = e4m3_values(h[j]);
       l[j] = e4m3_pair(a.x - back.x, a.y - back.y);
     }
-    hi[2 * i] = h[0] | h[1] << 16;
-    hi[2 * i + 1] = h[2] | h[3] << 16;
-    lo[2 * i] = l[0] | l[1] << 16;
-    lo[2 * i + 1] = l[2] | l[3] << 16;
+    hi[i / 2] = h[0] | h[1] << 16;
+    lo[i / 2] = l[0] | l[1] << 16;
+  }
+  if (!finite) {
+#pragma unroll
+    for (int i = 0; i < kWords / 2; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (lost[i / 2] >> (4 * (i & 1) + k) & 1u) hi[i] |= 0x7fu << (8 * k);
   }
   return e;
 }

@@ -25,7 +25,7 @@
 // What bounds it: for each group a chain of products (16 of 64 cycles, as many as in 16 bits: half
 // the time an operand's, twice the operands), their latency (450), the softmax (1700) and its
 // way back (450); two groups fill the tensor cores to about a half.  1024 rows behind 32768 keys,
-// 32 heads of 128 over 8: 550 us, 1.02 PFLOP/s of the 558 GFLOP that attention is.  The
+// 32 heads of 128 over 8: 548 us, 1.02 PFLOP/s of the 558 GFLOP that attention is.  The
 // softmax stays in short loops for the instruction cache: unrolled over a row's 128 scores, with no
 // other change, 8 drafts of 16 tokens over up to 16384 keys took 90 us, so 74.
 #include "chunk8_roles.cuh"
@@ -317,11 +317,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const TileMeta &tile = cta.scales(b, t);
         const int kb = (t0 + t) * kKT;
         const uint32_t bad = tile.bad;
-        const bool cut = !(lo <= kb && hi >= kb + kKT - 1);
         // Two passes of 64 scores a step, read from tensor memory each.  (Short loops: the tile's
         // 600 instructions, unrolled over the row, come at three cycles each, from a cache that
         // they share with the other warps' code.  32 a step: 1024 rows behind 32768 keys 591 us
-        // instead of 550, for the loads' latency.)
+        // instead of 548, for the loads' latency.)
         // the factor of 16 keys' scores; never 0 or NaN, which would make a masked one NaN
         auto factor = [&](int i) { return fmaxf(row_scale * tile.k[i], 0x1p-126f); };
         float tmax = -INFINITY;
@@ -330,7 +329,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           float s[64];
           ptx::tmem_ld64f_sync(tm_s + 64 * c, s);
           // what the row does not see: -inf, for both passes
+          const bool cut = lo > kb + 64 * c || hi < kb + 64 * c + 63;
           if (__any_sync(0xffffffffu, cut) || bad) {
+            if (bad >> 8) {  // K's scale is NaN
+#pragma unroll
+              for (int e = 0; e < 64; ++e)
+                if (bad >> (8 + 4 * c + e / 16) & 1u) s[e] = NAN;
+            }
 #pragma unroll
             for (int h = 0; h < 64; h += 32) {
               const int k0 = kb + 64 * c + h, from = max(lo - k0, 0), to = min(hi - k0, 31);
@@ -338,12 +343,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t groups = bad >> (4 * c + h / 16);  // bits 0 and 1: the 32 keys'
               if (groups & 1u) vis &= 0xffff0000u;
               if (groups & 2u) vis &= 0x0000ffffu;
-              const uint32_t nans =
-                  (groups & 256u ? 0xffffu : 0u) | (groups & 512u ? 0xffff0000u : 0u);
               uint32_t w[32];
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
-                if (nans >> e & 1u) s[h + e] = NAN;
                 if (!(vis >> e & 1u)) s[h + e] = -INFINITY;
                 w[e] = __float_as_uint(s[h + e]);
               }
@@ -578,8 +580,8 @@ cudaError_t launch_main(bool pair, const CUtensorMap &tm, const ChunkParams &p,
 
 // Rows of a work tile, as a power of two.  Heads of 128 whose mean request has at most 32 rows take
 // the kernel of chunk_attention8_few.cu: 64 single tokens of 4 rows a head over up to 8192 keys
-// take 131 us there, 219 here with a row a softmax thread; 8 drafts of 64 rows 120 there (two works
-// of 32 rows read the same keys), 74 here.
+// take 130 us there, 219 here with a row a softmax thread; 8 drafts of 64 rows 120 there (two works
+// of 32 rows read the same keys), 73 here.
 int tile_shift(const dflash_geom &g, int B, int n_rows) {
   const int64_t rows = static_cast<int64_t>(n_rows) * (g.hq / g.nkv);
   if (g.head_dim == 128 && rows <= 32LL * B)

@@ -16,7 +16,7 @@
 // What bounds it: a key tile takes the chain of warps about 1400 cycles, HBM 1310 (32 KB at 6.8
 // TB/s over 152 SMs); where a work ends and the next begins the stream stops for 4 to 6 us,
 // and a launch takes 7 us to its first weights.  64 single tokens over up to 8192 keys, 32 heads of
-// 128 over 8: 131 us, 4.7 TB/s; one token over 32768: 23.7 us.
+// 128 over 8: 130 us, 4.8 TB/s; one token over 32768: 23.8 us.
 #include "chunk8_roles.cuh"
 
 namespace dflash {
