@@ -406,9 +406,9 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkParams p) {
   Request rq;
   load_request(p, lo, &rq);
   if (!check_request(p, false, &rq) || t < rq.a || t >= rq.b) return;
-  float f[E];
+  float f[E];  // (0 without keys; a sum of NaN, from any segment, makes the row NaN)
 #pragma unroll
-  for (int e = 0; e < E; ++e) f[e] = l > 0.f ? acc[e] / l : 0.f;
+  for (int e = 0; e < E; ++e) f[e] = l != 0.f ? acc[e] / l : 0.f;
   uint16_t *dst = p.out + t * p.os + static_cast<int64_t>(h) * HD + lane * E;
   const uint32_t a = ptx::pack_bf16x2(f[0], f[1]);
   if constexpr (E == 4)
