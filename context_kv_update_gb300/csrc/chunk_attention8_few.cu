@@ -548,7 +548,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       if (tid < N) {
         const float *g0 = q_scale + 2 * N, *g1 = g0 + 11 * N;
         const float m0 = ok ? g0[9 * N + tid] : -INFINITY, m1 = ok ? g1[9 * N + tid] : -INFINITY;
-        const bool any = tid < nrow && fmaxf(m0, m1) != -INFINITY;
         const float m = fmaxf(m0, m1) - kFewLift;  // weights are relative to this
         const float w0 = m0 == -INFINITY ? 0.f : ptx::ex2(m0 - kFewLift - m),
                     w1 = m1 == -INFINITY ? 0.f : ptx::ex2(m1 - kFewLift - m);
@@ -559,6 +558,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           sum1 += g1[i * N + tid];
         }
         const float sum = sum0 * w0 + sum1 * w1;
+        // the row saw a key (where all its scores are NaN it has no reference, and a sum of NaN)
+        const bool any = tid < nrow && ok && (m != -INFINITY || sum != 0.f);
         const int flat = row0 + tid, tok = flat / p.G, h = d.kvh * p.G + flat - tok * p.G;
         const int64_t orow = static_cast<int64_t>(d.a) + tok;
         int64_t to = orow * p.os + static_cast<int64_t>(h) * HD;
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           const int64_t at = (orow * p.hq + h) * p.S + d.seg;
           to = any ? at * HD : -1;
           if (tid < nrow && g == 0) {
-            p.ws_m[at] = any ? m : -INFINITY;
+            p.ws_m[at] = any && m == -INFINITY ? 0.f : m;
             p.ws_l[at] = any ? sum : 0.f;
           }
         }

@@ -51,3 +51,58 @@ def test_a_key_of_nan_among_others(dl, hd, hq, rows, bits, S):  # noqa: F811
             got = run_attn8(dl, pb, **kw, S=S, check=False, cache=(codes, scales))
         lost = compare(got, bf16(pb["q"])[1], values, pb, scale=hd ** -0.5)
         assert lost.sum() == hq * (rows if key < ctx else rows - rows // 2)
+
+
+@pytest.mark.parametrize("S", [1, 3])
+@pytest.mark.parametrize("sinks", [False, True])
+@pytest.mark.parametrize("hd,hq,rows", FORMS)
+def test_queries_that_are_not_finite_8(dl, hd, hq, rows, sinks, S):  # noqa: F811
+    rng = np.random.default_rng(51)
+    kw = dict(hq=hq, nkv=1, hd=hd, P=32)
+    pb = attn_problem(rng, [rows, rows], [300, 0], **kw)
+    q = pb["q"]
+    q[0, 1, hd - 1], q[rows - 1, 0, 3], q[rows, 1, 0] = np.nan, np.nan, np.nan
+    if not sinks:  # (a sink makes rows whose scores are all -inf 0)
+        q[rows + 1, 0, 17], q[2 * rows - 1, 1, 40] = np.inf, -np.inf
+    sk = rng.standard_normal(hq).astype(np.float32) if sinks else None
+    codes, scales = chunk8.quantise(pb["pool"], 16)
+    got = run_attn8(dl, pb, **kw, S=S, sinks=sk, check=False, cache=(codes, scales))
+    lost = compare(got, bf16(q)[1], chunk8.values(codes[0], scales[0], 16), pb, scale=hd ** -0.5,
+                   sinks=None if sk is None else sk.astype(np.float64))
+    assert lost.sum() == (3 if sinks else 5)
+
+
+@pytest.mark.parametrize("S", [1, 2, 3])
+@pytest.mark.parametrize("window", [0, 1, 20])
+@pytest.mark.parametrize("hd,hq,rows", FORMS)
+def test_every_visible_block_of_nan_8(dl, hd, hq, rows, window, S):  # noqa: F811
+    """K's scales are 255 in all that some rows see: the whole context, or the window's blocks; rows
+    without keys are 0 beside them."""
+    rng = np.random.default_rng(52)
+    kw = dict(hq=hq, nkv=1, hd=hd, P=16)
+    pb = attn_problem(rng, [rows, rows, 2, 1], [200, 40, 3, 0], **kw)
+    pb["kv"][2] = 0
+    codes, scales = chunk8.quantise(pb["pool"], 16)
+    at = np.arange(0, 200 + rows) if window == 0 else np.arange(200, 200 + (rows + 1) // 2)
+    scales[0, pb["table"][0, np.unique(at // 16)], 0] = 255
+    scales[0, pb["table"][3, 0], 0] = 255  # a request's first token
+    got = run_attn8(dl, pb, **kw, S=S, window=window, check=False, cache=(codes, scales))
+    lost = compare(got, bf16(pb["q"])[1], chunk8.values(codes[0], scales[0], 16), pb,
+                   scale=hd ** -0.5, window=window)
+    assert lost[0].all() and lost[-1].all() and not lost[rows:-1].any()
+    assert np.all(got[2 * rows:-1] == 0)
+
+
+@pytest.mark.parametrize("S", [1, 3])
+def test_first_tokens_that_were_not_finite_8(dl, S):  # noqa: F811
+    """Stored as NaN, such a key is all that its own row sees."""
+    rng = np.random.default_rng(53)
+    for hd, rows in ((128, 4), (128, 60), (64, 4)):
+        kw = dict(hq=4, nkv=2, hd=hd, P=16)
+        pb = attn_problem(rng, [rows] * 3, [0] * 3, **kw)
+        codes, scales = chunk8.quantise(pb["pool"], 16)
+        codes[0, pb["table"][1, 0], 0, 0, 0] = 0x7f
+        got = run_attn8(dl, pb, **kw, S=S, check=False, cache=(codes, scales))
+        lost = compare(got, bf16(pb["q"])[1], chunk8.values(codes[0], scales[0], 16), pb,
+                       scale=hd ** -0.5)
+        assert lost[rows:2 * rows, :2].all() and lost.sum() == 2 * rows
