@@ -737,7 +737,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         other = bad || m2 == -INFINITY ? 0.f : ptx::ex2(m2 - m);
         l = l * own + l2 * other;
       }
-      const bool any = real && m != -INFINITY;  // the row saw a key
+      // the row saw a key (where all its scores are NaN it has no reference, and a sum of NaN)
+      const bool any = real && ok && (m != -INFINITY || l != 0.f);
       const int flat = d.row0 + (real ? rt : 0), tok = flat / p.G, seg = d.seg;
       const int h = d.kvh * p.G + flat - tok * p.G;
       const int64_t orow = static_cast<int64_t>(d.a) + tok;
@@ -752,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         gain = any ? ptx::ex2(m - top) / den : 0.f;
       } else if (real && (!split || g == 0)) {
         const int64_t w = (orow * p.hq + h) * p.S + seg;
-        p.ws_m[w] = m;
+        p.ws_m[w] = any && m == -INFINITY ? 0.f : m;
         p.ws_l[w] = any ? l : 0.f;
       }
       own *= gain;

@@ -106,3 +106,25 @@ def test_first_tokens_that_were_not_finite_8(dl, S):  # noqa: F811
         lost = compare(got, bf16(pb["q"])[1], chunk8.values(codes[0], scales[0], 16), pb,
                        scale=hd ** -0.5)
         assert lost[rows:2 * rows, :2].all() and lost.sum() == 2 * rows
+
+
+@pytest.mark.parametrize("S", [1, 2, 3])
+@pytest.mark.parametrize("hd,hq,rows", FORMS)
+def test_every_score_of_nan_16(dl, hd, hq, rows, S):  # noqa: F811
+    """Queries of NaN, a window whose keys are all NaN, and a first token's."""
+    rng = np.random.default_rng(54)
+    P = 16
+    kw = dict(hq=hq, nkv=1, hd=hd, P=P)
+    for window in (0, 1, 20):
+        for sinks in (None, rng.standard_normal(hq).astype(np.float32)):
+            pb = attn_problem(rng, [rows, rows, 2, 1], [300, 40, 3, 0], **kw)
+            pb["kv"][2] = 0
+            pb["q"][0, 1, hd - 1], pb["q"][2 * rows - 1, 0, 3] = np.nan, np.nan
+            pages = pb["table"][0, np.arange(300 - 32, 300 + 16) // P]
+            pb["pool"][0, pages, 0] = np.nan
+            pb["pool"][0, pb["table"][3, 0], 0, 0, 0, 7] = np.nan
+            got = run_attn(dl, pb, **kw, S=S, window=window, sinks=sinks, check=False)
+            lost = compare(got, bf16(pb["q"])[1], bf16(pb["pool"])[1][0], pb, scale=hd ** -0.5,
+                           window=window, sinks=None if sinks is None else sinks.astype(np.float64))
+            assert lost[0].all() and lost[-1].all() and lost[2 * rows - 1, 0]
+            assert np.all(got[2 * rows:-1] == 0)
