@@ -346,7 +346,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         row_m[tid] = real ? -INFINITY : 0.f;
         row_nm[tid] = 0.f;
       }
-      ptx::bar_sync(2 + g, 128);
+      // (A wait that ran out ends the work for the whole group: its warps meet at barriers below,
+      // and a barrier has no limit.)
+      ok = !ptx::bar_or(2 + g, 128, !ok);
 
       float l[N];  // this key's share of the rows' sums
 #pragma unroll
