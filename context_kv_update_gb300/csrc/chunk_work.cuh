@@ -359,6 +359,7 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkParams p) {
   const float *o = p.ws_o + w * p.S * HD + lane * E;
   float m = p.sinks ? p.sinks[h] * kLog2e : -INFINITY, l = p.sinks ? 1.f : 0.f;
   float acc[E] = {};
+  bool any = false;  // the row saw a key
   for (int s0 = 0; s0 < p.S; s0 += kBatch) {
     const bool in = lane < kBatch && s0 + lane < p.S;
     const float mj = in ? __ldcg(p.ws_m + w * p.S + s0 + lane) : -INFINITY;
@@ -379,8 +380,10 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkParams p) {
         ov[j][1] = v.y;
       }
     }
-    const float mn = fmaxf(m, warp_max(mj));
-    if (mn == -INFINITY) continue;
+    const float top = warp_max(mj);
+    if (top == -INFINITY) continue;
+    any = true;
+    const float mn = fmaxf(m, top);
     const float sc = m == -INFINITY ? 0.f : ptx::ex2(m - mn);
     const float wj = mj == -INFINITY ? 0.f : ptx::ex2(mj - mn);
     l = l * sc + warp_sum(wj * lj);
@@ -406,9 +409,9 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkParams p) {
   Request rq;
   load_request(p, lo, &rq);
   if (!check_request(p, false, &rq) || t < rq.a || t >= rq.b) return;
-  float f[E];  // (0 without keys; a sum of NaN, from any segment, makes the row NaN)
+  float f[E];  // (a sum of NaN, from any segment or the sink, makes the row NaN)
 #pragma unroll
-  for (int e = 0; e < E; ++e) f[e] = l != 0.f ? acc[e] / l : 0.f;
+  for (int e = 0; e < E; ++e) f[e] = any ? acc[e] / l : 0.f;
   uint16_t *dst = p.out + t * p.os + static_cast<int64_t>(h) * HD + lane * E;
   const uint32_t a = ptx::pack_bf16x2(f[0], f[1]);
   if constexpr (E == 4)

@@ -128,3 +128,20 @@ def test_every_score_of_nan_16(dl, hd, hq, rows, S):  # noqa: F811
                            window=window, sinks=None if sinks is None else sinks.astype(np.float64))
             assert lost[0].all() and lost[-1].all() and lost[2 * rows - 1, 0]
             assert np.all(got[2 * rows:-1] == 0)
+
+
+@pytest.mark.parametrize("S", [1, 2, 5])
+@pytest.mark.parametrize("run", [run_attn8, run_attn])
+@pytest.mark.parametrize("rows,hd", [(1, 128), (10, 128), (40, 128), (20, 64)])
+def test_sinks_at_the_ends(dl, rows, hd, run, S):  # noqa: F811
+    """-inf is no sink, one of 1e30 takes all weight; NaN and infinity make their head's rows NaN,
+    but those that see no key."""
+    rng = np.random.default_rng(74)
+    kw = dict(hq=4, nkv=1, hd=hd, P=32)
+    pb = attn_problem(rng, [rows, 2], [200, 40], **kw)
+    pb["kv"][1] = 0
+    none = run(dl, pb, **kw, S=S)
+    got = run(dl, pb, **kw, S=S, check=False, sinks=np.array([-np.inf, 1e30, np.nan, np.inf]))
+    np.testing.assert_array_equal(got[:, 0], none[:, 0])
+    assert np.all(got[:, 1] == 0) and np.all(got[rows:] == 0)
+    assert np.all(np.isnan(got[:rows, 2:]))
