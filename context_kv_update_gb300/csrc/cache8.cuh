@@ -38,6 +38,11 @@ __device__ __forceinline__ int scale8_exponent(float a) {
   return max((bits >> 23) - 127 - 8 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0), kLeastExp8);
 }
 
+// The exponent of a positive number's leading bit (2^e <= x < 2^(e + 1)); 128 of NaN.
+__device__ __forceinline__ int leading_exponent(float x) {
+  return static_cast<int>(__float_as_uint(x) >> 23 & 255u) - 127;
+}
+
 // Byte offset of a (page, K|V, head) of a layer in the codes, and place of its first scale.
 struct Cache8 {
   uint8_t *codes, *scales;

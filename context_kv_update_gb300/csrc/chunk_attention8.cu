@@ -479,9 +479,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           den = l * ptx::ex2(m - top) + ptx::ex2(sk - top);
         }
         gain = any ? ptx::ex2(m - top) / den : 0.f;
-      } else if (real && (!split || g == 0)) {
+      } else if (any) {
+        // A partial result is about the size of a value: a sum of weights times the largest that
+        // the cache holds, 2^127, would not be an fp32 number.
+        const int e = leading_exponent(l);
+        m = m == -INFINITY ? 0.f : m + static_cast<float>(e);
+        gain = exp2_int(-e);
+        l *= gain;
+      }
+      if (p.S > 1 && real && (!split || g == 0)) {
         const int64_t w = (orow * p.hq + h) * p.S + seg;
-        p.ws_m[w] = any && m == -INFINITY ? 0.f : m;
+        p.ws_m[w] = any ? m : -INFINITY;
         p.ws_l[w] = any ? l : 0.f;
       }
       own *= gain;

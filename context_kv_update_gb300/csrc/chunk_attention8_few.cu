@@ -577,9 +577,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         } else {
           const int64_t at = (orow * p.hq + h) * p.S + d.seg;
           to = any ? at * HD : -1;
+          // a partial result of about the size of a value, as in chunk_attention8.cu
+          const int e = any ? leading_exponent(sum) : 0;
+          gain = exp2_int(-e);
           if (tid < nrow && g == 0) {
-            p.ws_m[at] = any && m == -INFINITY ? 0.f : m;
-            p.ws_l[at] = any ? sum : 0.f;
+            p.ws_m[at] = !any ? -INFINITY : m == -INFINITY ? 0.f : m + static_cast<float>(e);
+            p.ws_l[at] = any ? sum * gain : 0.f;
           }
         }
         f0[tid] = any ? w0 * units[0] * gain : 0.f;
