@@ -525,7 +525,7 @@ __device__ __forceinline__ bool split_rows(const Cta<Lay> &c, const ChunkParams 
   return true;
 }
 
-// Widens V's tiles to 16 bits: the calling warp's share of the rows, 32 or 16.
+// Widens V's tiles to 16 bits: the calling warp's share of the rows, 32.
 template <class Lay>
 struct Widener {
   static constexpr int kSub = Lay::kHD / 64, kRows = 128 / kWidenTeam;

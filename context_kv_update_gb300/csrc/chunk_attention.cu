@@ -866,7 +866,7 @@ int tile_shift(const dflash_geom &g, int B, int n_rows) { return pair_form(g, B,
 }  // namespace
 
 // Segments the keys are cut into, by a model of the call's time in key tiles: a CTA
-// costs its tiles and kFixed more, and a merge costs kMerge and its bytes.  Lengths are on
+// costs its tiles and seven more, and a merge three and its bytes.  Lengths are on
 // the device: the table's width, or the window, stands for the longest span, so the
 // figures below hold for tables about as wide as the longest request.  Behind 32768 keys of
 // table a prompt of 4096 rows takes two segments and 181 us instead of 117, 64 single tokens

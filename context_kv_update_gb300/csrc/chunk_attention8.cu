@@ -589,8 +589,12 @@ cudaError_t launch_main(bool pair, const CUtensorMap &tm, const ChunkParams &p,
 
 // Rows of a work tile, as a power of two.  Heads of 128 whose mean request has at most 32 rows take
 // the kernel of chunk_attention8_few.cu: 64 single tokens of 4 rows a head over up to 8192 keys
-// take 130 us there, 219 here with a row a softmax thread; 8 drafts of 64 rows 120 there (two works
-// of 32 rows read the same keys), 73 here.
+// take 130 us there, 191 here with a row a softmax thread; 32 drafts of 32 rows over as many 93 and
+// 103; 8 drafts of 64 rows 120 there (two works of 32 rows read the same keys), 73 here.
+// The mean is all that the host knows: a long request among short ones goes there as well, in as many
+// works of 32 rows, each over all its keys (63 single tokens and a piece of 400 tokens behind
+// 32768 keys: 774 us there, 376 here; the piece at the start of its prompt 185 and 190).
+// Heads of 64 have no such kernel: 64 single tokens take 176 us, in 16 bits 171.
 int tile_shift(const dflash_geom &g, int B, int n_rows) {
   const int64_t rows = static_cast<int64_t>(n_rows) * (g.hq / g.nkv);
   if (g.head_dim == 128 && rows <= 32LL * B)
@@ -603,7 +607,8 @@ int tile_shift(const dflash_geom &g, int B, int n_rows) {
 int chunk_attention8_num_segments(const dflash_geom &g, int B, int n_rows, int window) {
   // Work tiles as if the requests had a mean's rows each (the most there can be is one more a
   // request: 16 requests of 16 tokens over up to 8192 keys took 102 us uncut for it, 83 in two).
-  // Where a work begins and ends the key stream stops: ten to twelve tiles' time.
+  // Where a work begins and ends the key stream stops: ten to twelve tiles' time.  (Costs of heads
+  // of 128; those of 64 take them as they are.)
   const int shift = tile_shift(g, B, n_rows);
   const int64_t flat = static_cast<int64_t>(n_rows) * (g.hq / g.nkv);
   const int64_t per = static_cast<int64_t>(B) << shift;
